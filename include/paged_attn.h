@@ -77,6 +77,7 @@ typedef enum {
 #define PKA_DEVERR_SEQ_LEN 4    /* seq_len beyond max_blocks*bs or the split cover */
 #define PKA_DEVERR_QUERY_LOC 8  /* query_start_loc span outside [0, total_q], negative,
                                    or longer than max_query_len (request skipped) */
+#define PKA_DEVERR_REFCOUNT 16  /* a block's reference count fell below zero */
 
 /* One layer's K/V block pool.  k and v are device pointers, 16-byte aligned,
  * bf16 [num_blocks][num_kv_heads][block_size][head_dim]. */
@@ -380,6 +381,127 @@ int paged_decode_attn_noalloc(const void* q, void* out, const pka_kv_pool* kv,
                               const int32_t* seq_lens, int32_t B, int32_t Hq,
                               int32_t max_seq_len, const pka_attn_params* params,
                               void* stream);
+
+/* 4-bit cache.  The pages store the cache in bf16; these entry points keep it
+ * in 4 bits (4.5 with the scales), so that the same memory holds 3.6 times the
+ * tokens and a decode step reads 3.6 times fewer bytes.
+ *
+ * Format: a value is stored as e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign)
+ * with one e4m3 scale for every 16 channels of a token and KV head, and one
+ * fp32 scale per pool: value = pool scale * e4m3 * e2m1.
+ *   k, v   device pointers, 16-byte aligned, uint8
+ *          [num_blocks][num_kv_heads][head_dim / 128][1152]: units of 16
+ *          tokens x 128 channels (paged_kv4_pool_bytes bytes for each of K and V).
+ *          K unit: codes [16 tokens][64], channel 2i in the low nibble of
+ *          byte i; then scales [16 tokens][8 groups].
+ *          V unit: codes [8 groups][16 tokens][8], in the odd groups tokens
+ *          8..15 before tokens 0..7; then scales [8 groups][16 tokens].
+ *   k_scale, v_scale   > 0 and finite, 6 * scale finite.  A scale of max|x| / 2688
+ *          over the values to be stored uses the whole range of the e4m3
+ *          scales.
+ * Quantisation of a group x of 16 channels, each operation rounded once to
+ * fp32: r = max|x| / (6 * pool scale); s = e4m3(min(r, 448)); code =
+ * e2m1(x / (s * pool scale)), both to the nearest, ties to even, saturating;
+ * s = 0 gives zeros.  A group that holds an infinity or a NaN reads back as
+ * NaN in all its 16 channels. */
+typedef struct {
+  void* k;
+  void* v;
+  int32_t num_blocks;
+  int32_t num_kv_heads;
+  int32_t block_size; /* 16 */
+  int32_t head_dim;   /* 128 or 256 */
+  float k_scale;
+  float v_scale;
+} pka_kv4_pool;
+
+/* Bytes of one 4-bit pool (K or V): num_blocks * num_kv_heads * 9 * head_dim;
+ * 0 for sizes that are not supported. */
+size_t paged_kv4_pool_bytes(int32_t num_blocks, int32_t num_kv_heads, int32_t head_dim);
+
+/* paged_kv_append into a 4-bit pool: token t's K and V rows are quantised and
+ * written at slot_mapping[t] (< 0 skips the token; a slot past the pool is
+ * skipped and ORs PKA_DEVERR_BAD_TABLE into *err; slots must be distinct).
+ *   k_new, v_new  bf16 [T][Hkv][D], device, 16-byte aligned; consecutive
+ *                 tokens k_stride / v_stride elements apart (at least Hkv * D,
+ *                 a multiple of 8: rows may be slices of a wider projection).
+ * Other slots of the blocks written are left as they are.  T = 0 is a no-op. */
+int paged_kv4_append(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride,
+                     const pka_kv4_pool* kv, const int32_t* slot_mapping, int32_t T,
+                     int32_t* err, void* stream);
+
+/* Blocks of a 4-bit pool as bf16 (rounded to nearest even), for the entry
+ * points that read bf16 pools: a prefill chunk over a 4-bit prefix expands its
+ * requests' blocks and runs paged_prefill_attn on them.  For i < n, block
+ * src_blocks[i] of kv is written to block dst_blocks[i] of dst (dst_blocks
+ * NULL: to block i; n at most dst's num_blocks then).  A negative id skips the
+ * item, so that rows of a padded block table can be passed as they are; an id
+ * past its pool skips it and ORs PKA_DEVERR_BAD_TABLE into *err.  All 16
+ * slots are written.  Destinations must be distinct.  The pools agree in KV
+ * heads, block size and head_dim. */
+int paged_kv4_expand(const pka_kv4_pool* kv, const pka_kv_pool* dst, const int32_t* src_blocks,
+                     const int32_t* dst_blocks, int32_t n, int32_t* err, void* stream);
+
+/* Decode over a 4-bit cache: paged_decode_attn_ws on the values the pool
+ * holds (arithmetic on them in fp32, or in f16 where that is exact; softmax weights
+ * rounded to f16; bf16 out).  Arguments, masks and errors as there; any group
+ * of 1 to 8 query heads per KV head.  A table id outside the pool reads as
+ * zeros and ORs PKA_DEVERR_BAD_TABLE into params->err.
+ * workspace: at least paged_kv4_decode_attn_ws_bytes() bytes, 16-byte
+ * aligned: B * Hkv int32 arrival counters (padded to 16 bytes), then the
+ * partials.  Counters zero before the first call, left zero by every call.
+ * Calls sharing one workspace must not overlap on the GPU. */
+size_t paged_kv4_decode_attn_ws_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D,
+                                      int32_t max_seq_len, int32_t window);
+int paged_kv4_decode_attn_ws(const void* q, void* out, const pka_kv4_pool* kv,
+                             const int32_t* block_tables, int32_t max_blocks,
+                             const int32_t* seq_lens, int32_t B, int32_t Hq,
+                             int32_t max_seq_len, const pka_attn_params* params,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Pages of a cache ("refcounted blocks, lazy allocation", github README,
+ * "What's inside", Paged KV cache row; "repeated or shared-system prompts skip
+ * prefill", prefix sharing row).  The reference counts, free lists and tables
+ * are the engine's; these entry points do the device side of forking, freeing
+ * and compacting.  A pool is any device array of num_blocks blocks of
+ * block_bytes bytes (bf16: Hkv*16*D*2 each of K and V; 4-bit: Hkv*9*D).
+ *
+ * paged_kv_ref_blocks: adds delta to refcounts[id] for every block the B
+ *   table rows use (entries j < ceil(seq_len / 16)): +1 when a request is
+ *   forked, -1 when it ends.  Negative entries (no block, or one a sliding
+ *   layer gave back) are skipped; an id past the pool ORs PKA_DEVERR_BAD_TABLE
+ *   into *err, a count that falls below zero PKA_DEVERR_REFCOUNT.  A block that
+ *   occurs in several entries counts for each.
+ * paged_kv_copy_blocks: block src[i] -> block dst[i] for i < n in each of
+ *   num_pools pools (pools: host array of device pointers, 16-byte aligned;
+ *   block_bytes a multiple of 16), e.g. the last, partly filled block of a
+ *   forked request in every layer.  The destinations must be distinct and
+ *   none of them another pair's source (else those blocks' contents are
+ *   undefined); src[i] = dst[i] does nothing.  A pair with an id outside the
+ *   pool is skipped and ORs PKA_DEVERR_BAD_TABLE into *err.
+ * paged_kv_compact: closes a pool up.  With n = the number of live blocks
+ *   (refcount > 0), the j-th highest live id at or above n moves to the j-th
+ *   lowest free id below n, in each of num_pools pools; afterwards the live
+ *   blocks are 0 .. n - 1.  Outputs (device): remap[id] = new id (-1: free);
+ *   new_refcounts[new id] (0 from n on; may be refcounts itself); new_tables
+ *   = block_tables with the used entries (j < ceil(seq_len / 16)) remapped
+ *   (a free block's becomes -1; unused and negative entries are kept; may be
+ *   block_tables itself); moves int32 [2 + num_blocks]: [0] the number of
+ *   moves, [1] = n, then (old id, new id) for each move, -1 after the last.
+ *   A used entry past the pool is kept and ORs PKA_DEVERR_BAD_TABLE into *err.
+ *   num_pools = 0 plans only; B = 0 leaves tables out.  Blocks from n on keep
+ *   their old contents. */
+int paged_kv_ref_blocks(const int32_t* block_tables, int32_t max_blocks, const int32_t* seq_lens,
+                        int32_t B, int32_t num_blocks, int32_t delta, int32_t* refcounts,
+                        int32_t* err, void* stream);
+int paged_kv_copy_blocks(void* const* pools, int32_t num_pools, int32_t num_blocks,
+                         int64_t block_bytes, const int32_t* src, const int32_t* dst, int32_t n,
+                         int32_t* err, void* stream);
+int paged_kv_compact(void* const* pools, int32_t num_pools, int32_t num_blocks,
+                     int64_t block_bytes, const int32_t* refcounts, int32_t* new_refcounts,
+                     const int32_t* block_tables, int32_t* new_tables, int32_t max_blocks,
+                     const int32_t* seq_lens, int32_t B, int32_t* remap, int32_t* moves,
+                     int32_t* err, void* stream);
 
 #ifdef __cplusplus
 }

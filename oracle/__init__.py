@@ -13,3 +13,5 @@ from .brute_force import brute_force_attention  # noqa: F401
 from .kv_append import kv_append  # noqa: F401
 from .key_mass import key_mass  # noqa: F401
 from .rope_norm import rms_norm, rope, kv_append_rope  # noqa: F401
+from .kv4 import kv4_append, kv4_decode, kv4_place, kv4_quantise  # noqa: F401
+from .pages import compact, copy_blocks, ref_blocks  # noqa: F401

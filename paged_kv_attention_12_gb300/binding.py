@@ -28,6 +28,7 @@ DEVERR_BAD_TABLE = 1
 DEVERR_TIMEOUT = 2
 DEVERR_SEQ_LEN = 4
 DEVERR_QUERY_LOC = 8
+DEVERR_REFCOUNT = 16
 
 EXPORTS = [
     "pka_version", "pka_status_string", "paged_decode_attn", "paged_decode_splitk_plan",
@@ -36,8 +37,12 @@ EXPORTS = [
     "paged_decode_attn_noalloc", "paged_decode_attn_ws_bytes", "paged_decode_attn_ws",
     "paged_kv_append", "paged_decode_splitk_logits", "paged_decode_key_mass",
     "paged_kv_append_rope", "paged_prefill_attn_ws_bytes", "paged_prefill_attn_ws",
-    "pka_selftest_bounded_wait",
+    "pka_selftest_bounded_wait", "paged_kv4_pool_bytes", "paged_kv4_append", "paged_kv4_expand",
+    "paged_kv4_decode_attn_ws_bytes", "paged_kv4_decode_attn_ws", "paged_kv_ref_blocks",
+    "paged_kv_copy_blocks", "paged_kv_compact",
 ]
+
+KV4_UNIT_BYTES = 1152  # 16 tokens x 128 channels of a 4-bit pool
 
 
 class PkaKvPool(ctypes.Structure):
@@ -49,6 +54,13 @@ class PkaKvPool(ctypes.Structure):
 class PkaAttnParams(ctypes.Structure):
     _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float),
                 ("window", ctypes.c_int32), ("err", ctypes.c_void_p)]
+
+
+class PkaKv4Pool(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("num_blocks", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
 
 
 class PagedAttnError(RuntimeError):
@@ -125,6 +137,24 @@ def lib() -> ctypes.CDLL:
     L.pka_selftest_bounded_wait.argtypes = [VP, ctypes.c_int64, VP]
     L.paged_kv_append.restype = ctypes.c_int
     L.paged_kv_append.argtypes = [VP, VP, VP, VP, I32, I32, I32, I32, VP, I32, VP, VP]
+    I64 = ctypes.c_int64
+    L.paged_kv4_pool_bytes.restype = ctypes.c_size_t
+    L.paged_kv4_pool_bytes.argtypes = [I32, I32, I32]
+    L.paged_kv4_append.restype = ctypes.c_int
+    L.paged_kv4_append.argtypes = [VP, VP, I64, I64, P(PkaKv4Pool), VP, I32, VP, VP]
+    L.paged_kv4_expand.restype = ctypes.c_int
+    L.paged_kv4_expand.argtypes = [P(PkaKv4Pool), P(PkaKvPool), VP, VP, I32, VP, VP]
+    L.paged_kv4_decode_attn_ws_bytes.restype = ctypes.c_size_t
+    L.paged_kv4_decode_attn_ws_bytes.argtypes = [I32, I32, I32, I32, I32, I32]
+    L.paged_kv4_decode_attn_ws.restype = ctypes.c_int
+    L.paged_kv4_decode_attn_ws.argtypes = [VP, VP, P(PkaKv4Pool), VP, I32, VP, I32, I32, I32,
+                                           P(PkaAttnParams), VP, ctypes.c_size_t, VP]
+    L.paged_kv_ref_blocks.restype = ctypes.c_int
+    L.paged_kv_ref_blocks.argtypes = [VP, I32, VP, I32, I32, I32, VP, VP, VP]
+    L.paged_kv_copy_blocks.restype = ctypes.c_int
+    L.paged_kv_copy_blocks.argtypes = [VP, I32, I32, I64, VP, VP, I32, VP, VP]
+    L.paged_kv_compact.restype = ctypes.c_int
+    L.paged_kv_compact.argtypes = [VP, I32, I32, I64, VP, VP, VP, VP, I32, VP, I32, VP, VP, VP, VP]
     _lib = L
     return L
 
@@ -331,6 +361,222 @@ def paged_kv_append_rope(q, k_new, v_new, k_pool, v_pool, slot_mapping, position
         _ptr(positions), slot_mapping.shape[0], _ptr(q_norm_weight), _ptr(k_norm_weight),
         1 if v_norm else 0, float(eps), float(rope_theta), rd, _ptr(err), _stream(stream))
     _check("paged_kv_append_rope", st)
+
+
+# ------------------------------------------------- 4-bit cache and its pages
+# These check their tensors (device, type, layout, shape) before the call and
+# raise ValueError; they run on the tensors' device, on its current stream
+# unless one is given.
+def _want(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _tensor(t, name: str, dtype, device=None, contiguous: bool = True) -> None:
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name}: a tensor on {device or 'a CUDA device'} is wanted, "
+                         f"got one on {t.device}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: {dtype} is wanted, got {t.dtype}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor is wanted")
+
+
+def _ids(t, name: str, shape, device) -> None:
+    import torch
+    _tensor(t, name, torch.int32, device)
+    if t.shape != shape:
+        raise ValueError(f"{name}: int32 {list(shape)} is wanted, got {list(t.shape)}")
+
+
+def _err(err, device) -> Optional[int]:
+    import torch
+    if err is None:
+        return None
+    _tensor(err, "err", torch.int32, device)
+    _want(err.numel() >= 1, "err: at least one int32 is wanted")
+    return err.data_ptr()
+
+
+def _run_on(device, stream, name: str, *args) -> None:
+    """Calls the library function ``name`` with ``args`` and the stream, with
+    ``device`` current."""
+    import torch
+    fn = getattr(lib(), name)
+    if device.index == torch.cuda.current_device():
+        s = torch.cuda.current_stream(device) if stream is None else stream
+        st = fn(*args, s.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            s = torch.cuda.current_stream(device) if stream is None else stream
+            st = fn(*args, s.cuda_stream)
+    if st != PKA_OK:
+        raise PagedAttnError(name, st)
+
+
+class Kv4Pool:
+    """A layer's 4-bit cache: uint8 ``k`` and ``v`` of shape
+    ``[num_blocks][Hkv][D / 128][1152]`` and their fp32 scales (the format is
+    described at ``pka_kv4_pool`` in ``include/paged_attn.h``)."""
+
+    def __init__(self, k, v, k_scale: float, v_scale: float):
+        import torch
+        for t, name in ((k, "k"), (v, "v")):
+            _tensor(t, name, torch.uint8, k.device)
+            _want(t.dim() == 4 and t.shape[3] == KV4_UNIT_BYTES and t.shape[2] in (1, 2) and
+                  t.shape == k.shape,
+                  f"{name}: uint8 [num_blocks][Hkv][D / 128][{KV4_UNIT_BYTES}] is wanted, "
+                  f"got {list(t.shape)}")
+        self.k, self.v = k, v
+        self.k_scale, self.v_scale = float(k_scale), float(v_scale)
+        self.num_blocks, self.num_kv_heads, units, _ = k.shape
+        self.head_dim = 128 * units
+        self.device = k.device
+        self._c = PkaKv4Pool(k.data_ptr(), v.data_ptr(), self.num_blocks, self.num_kv_heads, 16,
+                             self.head_dim, self.k_scale, self.v_scale)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def zeros(cls, num_blocks: int, num_kv_heads: int, head_dim: int, k_scale: float,
+              v_scale: float, device="cuda") -> "Kv4Pool":
+        """An empty pool (every value 0)."""
+        import torch
+        _want(head_dim in (128, 256), f"head_dim 128 or 256 is wanted, got {head_dim}")
+        shape = (num_blocks, num_kv_heads, head_dim // 128, KV4_UNIT_BYTES)
+        return cls(torch.zeros(shape, dtype=torch.uint8, device=device),
+                   torch.zeros(shape, dtype=torch.uint8, device=device), k_scale, v_scale)
+
+
+def paged_kv4_append(k_new, v_new, pool: Kv4Pool, slot_mapping, err=None, stream=None):
+    """Quantise token t's K/V rows (``k_new``/``v_new`` bf16 [T][Hkv][D]; the
+    tokens may be strided, as slices of a wider projection are) and write them
+    to ``pool`` at slot ``slot_mapping[t]`` (int32; < 0 skips the token)."""
+    import torch
+    dev, row = pool.device, (pool.num_kv_heads, pool.head_dim)
+    T = k_new.shape[0]
+    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
+        _tensor(t, name, torch.bfloat16, dev, False)
+        _want(t.dim() == 3 and t.shape[0] == T and t.shape[1:] == row,
+              f"{name}: bf16 [{T}][{row[0]}][{row[1]}] is wanted, got {list(t.shape)}")
+        _want(T == 0 or (t.stride(2) == 1 and (row[0] == 1 or t.stride(1) == row[1])),
+              f"{name}: a token's rows must be contiguous, got strides {t.stride()}")
+    _ids(slot_mapping, "slot_mapping", (T,), dev)
+    # a single token has no next one: its stride is any that the call takes
+    ks, vs = (row[0] * row[1] if T < 2 else t.stride(0) for t in (k_new, v_new))
+    _run_on(dev, stream, "paged_kv4_append", k_new.data_ptr(), v_new.data_ptr(), ks, vs, pool._ref,
+            slot_mapping.data_ptr(), T, _err(err, dev))
+
+
+def paged_kv4_expand(pool: Kv4Pool, k_pool, v_pool, src_blocks, dst_blocks=None, err=None,
+                     stream=None):
+    """Write blocks ``src_blocks`` (int32, any shape; < 0 skips) of a 4-bit
+    pool to blocks ``dst_blocks`` (default 0, 1, ...) of bf16 pools
+    [num_blocks][Hkv][16][D], as the prefill entry points read them."""
+    import torch
+    dev = pool.device
+    for t, name in ((k_pool, "k_pool"), (v_pool, "v_pool")):
+        _tensor(t, name, torch.bfloat16, dev)
+        _want(t.dim() == 4 and t.shape == k_pool.shape and
+              t.shape[1:] == (pool.num_kv_heads, 16, pool.head_dim),
+              f"{name}: bf16 [num_blocks][{pool.num_kv_heads}][16][{pool.head_dim}] is wanted, "
+              f"got {list(t.shape)}")
+    _tensor(src_blocks, "src_blocks", torch.int32, dev)
+    if dst_blocks is not None:
+        _ids(dst_blocks, "dst_blocks", src_blocks.shape, dev)
+    dst = kv_pool(k_pool, v_pool)
+    _run_on(dev, stream, "paged_kv4_expand", pool._ref, ctypes.byref(dst), src_blocks.data_ptr(),
+            _ptr(dst_blocks), src_blocks.numel(), _err(err, dev))
+
+
+def paged_kv4_decode_attn_ws_bytes(B, Hq, Hkv, D, max_seq_len, window=0) -> int:
+    return int(lib().paged_kv4_decode_attn_ws_bytes(B, Hq, Hkv, D, int(max_seq_len), int(window)))
+
+
+def paged_kv4_decode_attn_ws(q, out, pool: Kv4Pool, block_tables, seq_lens, max_seq_len, workspace,
+                             *, scale, softcap=0.0, window=0, err=None, stream=None):
+    """Decode over a 4-bit cache in one launch: ``q``, ``out`` bf16
+    [B][Hq][D].  ``workspace``: device bytes, zero before their first use, at
+    least ``paged_kv4_decode_attn_ws_bytes``; not to be shared by calls that
+    can overlap."""
+    import torch
+    dev = pool.device
+    B = seq_lens.shape[0]
+    for t, name in ((q, "q"), (out, "out")):
+        _tensor(t, name, torch.bfloat16, dev)
+        _want(t.dim() == 3 and t.shape[0] == B and t.shape[2] == pool.head_dim and
+              t.shape[1] == q.shape[1],
+              f"{name}: bf16 [{B}][Hq][{pool.head_dim}] is wanted, got {list(t.shape)}")
+    _tensor(block_tables, "block_tables", torch.int32, dev)
+    _want(block_tables.dim() == 2 and block_tables.shape[0] == B,
+          f"block_tables: int32 [{B}][max_blocks] is wanted, got {list(block_tables.shape)}")
+    _ids(seq_lens, "seq_lens", (B,), dev)
+    _tensor(workspace, "workspace", workspace.dtype, dev)
+    par = PkaAttnParams(scale, softcap, window, _err(err, dev))
+    _run_on(dev, stream, "paged_kv4_decode_attn_ws", q.data_ptr(), out.data_ptr(), pool._ref,
+            block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(), B, q.shape[1],
+            int(max_seq_len), ctypes.byref(par), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+
+
+def paged_kv_ref_blocks(block_tables, seq_lens, refcounts, delta: int, err=None, stream=None):
+    """Add ``delta`` to ``refcounts`` (int32 [num_blocks]) for every block the
+    rows of ``block_tables`` use: +1 forks the requests, -1 frees them."""
+    import torch
+    _tensor(block_tables, "block_tables", torch.int32)
+    dev = block_tables.device
+    _want(block_tables.dim() == 2, "block_tables: int32 [B][max_blocks] is wanted")
+    B, width = block_tables.shape
+    _ids(seq_lens, "seq_lens", (B,), dev)
+    _ids(refcounts, "refcounts", (refcounts.numel(),), dev)
+    _run_on(dev, stream, "paged_kv_ref_blocks", block_tables.data_ptr(), width,
+            seq_lens.data_ptr(), B, refcounts.numel(), int(delta), refcounts.data_ptr(),
+            _err(err, dev))
+
+
+def _pool_list(pools):
+    """The pools' device pointers as a C array, their blocks and bytes per block."""
+    import torch
+    first = pools[0]
+    n = first.shape[0]
+    nbytes = first.numel() // max(n, 1) * first.element_size()
+    for p in pools:
+        if not p.is_cuda or p.device != first.device or not p.is_contiguous():
+            raise ValueError("pools: contiguous tensors on one CUDA device are wanted")
+        if p.shape[0] != n or p.numel() * p.element_size() != n * nbytes:
+            raise ValueError("pools: tensors of equally many blocks of equal size are wanted")
+    return (ctypes.c_void_p * len(pools))(*[p.data_ptr() for p in pools]), n, nbytes, first.device
+
+
+def paged_kv_copy_blocks(pools, src, dst, err=None, stream=None):
+    """Copy block ``src[i]`` to block ``dst[i]`` (int32) in each of ``pools``
+    (tensors [num_blocks][...], of equal block size: K and V of every layer).
+    The destinations must be distinct and none of them a source."""
+    ptrs, n, nbytes, dev = _pool_list(pools)
+    _ids(src, "src", (src.numel(),), dev)
+    _ids(dst, "dst", src.shape, dev)
+    _run_on(dev, stream, "paged_kv_copy_blocks", ptrs, len(ptrs), n, nbytes, src.data_ptr(),
+            dst.data_ptr(), src.numel(), _err(err, dev))
+
+
+def paged_kv_compact(pools, refcounts, block_tables, seq_lens, new_refcounts, new_tables, remap,
+                     moves, err=None, stream=None):
+    """Move the live blocks (``refcounts`` > 0) of every pool to ids 0, 1, ...
+    and give the new counts, tables, the map old id -> new id and the moves
+    (int32 [2 + num_blocks]: their number, the live blocks, then pairs).
+    ``new_refcounts`` and ``new_tables`` may be the old ones."""
+    import torch
+    ptrs, n, nbytes, dev = _pool_list(pools)
+    for t, name, size in ((refcounts, "refcounts", n), (new_refcounts, "new_refcounts", n),
+                          (remap, "remap", n), (moves, "moves", n + 2)):
+        _ids(t, name, (size,), dev)
+    _tensor(block_tables, "block_tables", torch.int32, dev)
+    _want(block_tables.dim() == 2, "block_tables: int32 [B][max_blocks] is wanted")
+    B, width = block_tables.shape
+    _ids(new_tables, "new_tables", (B, width), dev)
+    _ids(seq_lens, "seq_lens", (B,), dev)
+    _run_on(dev, stream, "paged_kv_compact", ptrs, len(ptrs), n, nbytes, refcounts.data_ptr(),
+            new_refcounts.data_ptr(), block_tables.data_ptr(), new_tables.data_ptr(), width,
+            seq_lens.data_ptr(), B, remap.data_ptr(), moves.data_ptr(), _err(err, dev))
 
 
 # ------------------------------------------------------------ batch runners

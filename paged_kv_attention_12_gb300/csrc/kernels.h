@@ -136,7 +136,92 @@ struct AppendRopeArgs {
 
 cudaError_t launch_kv_append_rope(const AppendRopeArgs& a, int sm_count, cudaStream_t stream);
 
+// Append of new tokens' K/V rows into a 4-bit pool (kv4.cuh has the format).
+struct Kv4AppendArgs {
+  const uint16_t* k_new;        // bf16 [T][Hkv][D], tokens k_stride elements apart
+  const uint16_t* v_new;
+  long long k_stride, v_stride;
+  uint8_t* k_pool;              // [num_blocks][Hkv][D / 128][1152]
+  uint8_t* v_pool;
+  float k_scale, v_scale;       // the pools' scales, and 6 times them
+  float k_scale6, v_scale6;
+  const int32_t* slot_mapping;  // [T]: block * bs + offset, < 0: skip
+  int32_t* err;
+  int32_t T, Hkv, head_dim, num_blocks;
+};
+
+cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int sm_count, cudaStream_t stream);
+
+// Blocks of a 4-bit pool written to a bf16 pool.
+struct Kv4ExpandArgs {
+  const uint8_t* k4;
+  const uint8_t* v4;
+  uint16_t* k16;                // bf16 [dst_num_blocks][Hkv][bs][D]
+  uint16_t* v16;
+  float k_scale, v_scale;
+  const int32_t* src_blocks;    // [n], < 0: skip
+  const int32_t* dst_blocks;    // [n], < 0: skip; null: item i goes to block i
+  int32_t* err;
+  int32_t n, Hkv, head_dim, src_num_blocks, dst_num_blocks;
+};
+
+cudaError_t launch_kv4_expand(const Kv4ExpandArgs& a, int sm_count, cudaStream_t stream);
+
+// Split-K decode over a 4-bit cache with the combine fused in.  base: q, out,
+// partials, counters, tables and sizes as for launch_decode (k and v unused).
+struct Kv4DecodeArgs {
+  DecodeArgs base;
+  const uint8_t* k4;
+  const uint8_t* v4;
+  float k_scale, v_scale;
+};
+
+cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, int head_dim, int sms, cudaStream_t stream);
+
+// Block copies within pools, and the moves and tables of a compaction.
+constexpr int kMaxCopyPools = 256;  // pools per launch (their pointers travel as arguments)
+struct CopyArgs {
+  void* pools[kMaxCopyPools];
+  long long block_bytes;
+  const int32_t* src;       // [n] and [n], or null with moves
+  const int32_t* dst;
+  const int32_t* moves;     // compaction: [0] = pairs, then (src, dst) from [2] on
+  const int32_t* tables;    // compaction: [batch][max_blocks], or null
+  int32_t* new_tables;
+  const int32_t* seq_lens;
+  const int32_t* remap;
+  int32_t* err;
+  int32_t num_pools, num_blocks, n, batch, max_blocks;
+};
+
+// max_pairs: the most pairs there can be (sizes the grid).
+cudaError_t launch_copy_blocks(const CopyArgs& a, int max_pairs, int sm_count,
+                               cudaStream_t stream);
+
+struct RefArgs {
+  const int32_t* tables;
+  const int32_t* seq_lens;
+  int32_t* refcounts;
+  int32_t* err;
+  int32_t batch, max_blocks, num_blocks, delta;
+};
+
+cudaError_t launch_ref_blocks(const RefArgs& a, int sm_count, cudaStream_t stream);
+
+struct PlanArgs {
+  const int32_t* refcounts;
+  int32_t* new_refcounts;   // may be refcounts
+  int32_t* remap;
+  int32_t* moves;           // [2 + num_blocks]
+  int32_t num_blocks;
+};
+
+cudaError_t launch_compact_plan(const PlanArgs& a, cudaStream_t stream);
+
 int device_sm_count();
+
+// Whether the split-K work line of these sizes fits the kernels' 32-bit arithmetic.
+bool splitk_line_fits(int32_t B, int32_t Hkv, int32_t max_blocks, int32_t window);
 
 // The argument checks of paged_decode_attn (host only, nothing launched):
 // PKA_OK or the pka_status the entry points return for these arguments.
