@@ -366,27 +366,28 @@ def paged_kv_append_rope(q, k_new, v_new, k_pool, v_pool, slot_mapping, position
 # ------------------------------------------------- 4-bit cache and its pages
 # These check their tensors (device, type, layout, shape) before the call and
 # raise ValueError; they run on the tensors' device, on its current stream
-# unless one is given.
-def _want(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+# unless one is given.  A decode step makes these calls for every layer, so the
+# checks build no text unless they fail.
+def _refuse(t, name: str, want: str):
+    raise ValueError(f"{name}: {want} is wanted, got {t.dtype} {list(t.shape)} with strides "
+                     f"{t.stride()} on {t.device}")
 
 
-def _tensor(t, name: str, dtype, device=None, contiguous: bool = True) -> None:
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{name}: a tensor on {device or 'a CUDA device'} is wanted, "
-                         f"got one on {t.device}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name}: {dtype} is wanted, got {t.dtype}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous tensor is wanted")
+def _dims(*shape) -> str:
+    return "".join(f"[{x}]" for x in shape)
 
 
-def _ids(t, name: str, shape, device) -> None:
-    import torch
-    _tensor(t, name, torch.int32, device)
-    if t.shape != shape:
-        raise ValueError(f"{name}: int32 {list(shape)} is wanted, got {list(t.shape)}")
+def _tensor(t, name: str, dtype, device, shape=None) -> None:
+    """A contiguous tensor of ``dtype`` on ``device``, of ``shape`` if given."""
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous() or \
+            (shape is not None and t.shape != shape):
+        _refuse(t, name, f"contiguous {dtype} {'' if shape is None else _dims(*shape)} on {device}")
+
+
+def _cuda_device(t, name: str):
+    if not t.is_cuda:
+        raise ValueError(f"{name}: a tensor on a CUDA device is wanted, got one on {t.device}")
+    return t.device
 
 
 def _err(err, device) -> Optional[int]:
@@ -394,7 +395,8 @@ def _err(err, device) -> Optional[int]:
     if err is None:
         return None
     _tensor(err, "err", torch.int32, device)
-    _want(err.numel() >= 1, "err: at least one int32 is wanted")
+    if err.numel() < 1:
+        _refuse(err, "err", "at least one int32")
     return err.data_ptr()
 
 
@@ -403,13 +405,14 @@ def _run_on(device, stream, name: str, *args) -> None:
     ``device`` current."""
     import torch
     fn = getattr(lib(), name)
-    if device.index == torch.cuda.current_device():
-        s = torch.cuda.current_stream(device) if stream is None else stream
-        st = fn(*args, s.cuda_stream)
+    idx = device.index
+    if idx == torch._C._cuda_getDevice():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(idx) if stream is None
+                else stream.cuda_stream)
     else:
         with torch.cuda.device(device):
-            s = torch.cuda.current_stream(device) if stream is None else stream
-            st = fn(*args, s.cuda_stream)
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(idx) if stream is None
+                    else stream.cuda_stream)
     if st != PKA_OK:
         raise PagedAttnError(name, st)
 
@@ -421,17 +424,16 @@ class Kv4Pool:
 
     def __init__(self, k, v, k_scale: float, v_scale: float):
         import torch
+        dev = _cuda_device(k, "k")
         for t, name in ((k, "k"), (v, "v")):
-            _tensor(t, name, torch.uint8, k.device)
-            _want(t.dim() == 4 and t.shape[3] == KV4_UNIT_BYTES and t.shape[2] in (1, 2) and
-                  t.shape == k.shape,
-                  f"{name}: uint8 [num_blocks][Hkv][D / 128][{KV4_UNIT_BYTES}] is wanted, "
-                  f"got {list(t.shape)}")
+            _tensor(t, name, torch.uint8, dev, k.shape)
+            if t.dim() != 4 or t.shape[3] != KV4_UNIT_BYTES or t.shape[2] not in (1, 2):
+                _refuse(t, name, f"uint8 [num_blocks][Hkv][D / 128][{KV4_UNIT_BYTES}]")
         self.k, self.v = k, v
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
         self.num_blocks, self.num_kv_heads, units, _ = k.shape
         self.head_dim = 128 * units
-        self.device = k.device
+        self.device = dev
         self._c = PkaKv4Pool(k.data_ptr(), v.data_ptr(), self.num_blocks, self.num_kv_heads, 16,
                              self.head_dim, self.k_scale, self.v_scale)
         self._ref = ctypes.byref(self._c)
@@ -441,10 +443,26 @@ class Kv4Pool:
               v_scale: float, device="cuda") -> "Kv4Pool":
         """An empty pool (every value 0)."""
         import torch
-        _want(head_dim in (128, 256), f"head_dim 128 or 256 is wanted, got {head_dim}")
+        if head_dim not in (128, 256):
+            raise ValueError(f"head_dim 128 or 256 is wanted, got {head_dim}")
         shape = (num_blocks, num_kv_heads, head_dim // 128, KV4_UNIT_BYTES)
         return cls(torch.zeros(shape, dtype=torch.uint8, device=device),
                    torch.zeros(shape, dtype=torch.uint8, device=device), k_scale, v_scale)
+
+
+def _token_rows(t, name: str, T: int, pool: Kv4Pool) -> int:
+    """Checks bf16 rows [T][Hkv][D], contiguous within a token; their token stride."""
+    import torch
+    h, d = pool.num_kv_heads, pool.head_dim
+    if t.dtype is not torch.bfloat16 or t.device != pool.device or t.shape != (T, h, d):
+        _refuse(t, name, f"bfloat16 {_dims(T, h, d)} on {pool.device}")
+    if T == 0:
+        return h * d
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (h > 1 and s1 != d):
+        _refuse(t, name, f"rows of a token side by side (strides [...][{d}][1])")
+    # a single token has no next one: its stride says nothing
+    return h * d if T == 1 else s0
 
 
 def paged_kv4_append(k_new, v_new, pool: Kv4Pool, slot_mapping, err=None, stream=None):
@@ -452,17 +470,9 @@ def paged_kv4_append(k_new, v_new, pool: Kv4Pool, slot_mapping, err=None, stream
     tokens may be strided, as slices of a wider projection are) and write them
     to ``pool`` at slot ``slot_mapping[t]`` (int32; < 0 skips the token)."""
     import torch
-    dev, row = pool.device, (pool.num_kv_heads, pool.head_dim)
-    T = k_new.shape[0]
-    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
-        _tensor(t, name, torch.bfloat16, dev, False)
-        _want(t.dim() == 3 and t.shape[0] == T and t.shape[1:] == row,
-              f"{name}: bf16 [{T}][{row[0]}][{row[1]}] is wanted, got {list(t.shape)}")
-        _want(T == 0 or (t.stride(2) == 1 and (row[0] == 1 or t.stride(1) == row[1])),
-              f"{name}: a token's rows must be contiguous, got strides {t.stride()}")
-    _ids(slot_mapping, "slot_mapping", (T,), dev)
-    # a single token has no next one: its stride is any that the call takes
-    ks, vs = (row[0] * row[1] if T < 2 else t.stride(0) for t in (k_new, v_new))
+    dev, T = pool.device, slot_mapping.shape[0]
+    ks, vs = _token_rows(k_new, "k_new", T, pool), _token_rows(v_new, "v_new", T, pool)
+    _tensor(slot_mapping, "slot_mapping", torch.int32, dev, (T,))
     _run_on(dev, stream, "paged_kv4_append", k_new.data_ptr(), v_new.data_ptr(), ks, vs, pool._ref,
             slot_mapping.data_ptr(), T, _err(err, dev))
 
@@ -474,16 +484,13 @@ def paged_kv4_expand(pool: Kv4Pool, k_pool, v_pool, src_blocks, dst_blocks=None,
     [num_blocks][Hkv][16][D], as the prefill entry points read them."""
     import torch
     dev = pool.device
-    for t, name in ((k_pool, "k_pool"), (v_pool, "v_pool")):
-        _tensor(t, name, torch.bfloat16, dev)
-        _want(t.dim() == 4 and t.shape == k_pool.shape and
-              t.shape[1:] == (pool.num_kv_heads, 16, pool.head_dim),
-              f"{name}: bf16 [num_blocks][{pool.num_kv_heads}][16][{pool.head_dim}] is wanted, "
-              f"got {list(t.shape)}")
+    shape = (k_pool.shape[0], pool.num_kv_heads, 16, pool.head_dim)
+    _tensor(k_pool, "k_pool", torch.bfloat16, dev, shape)
+    _tensor(v_pool, "v_pool", torch.bfloat16, dev, shape)
     _tensor(src_blocks, "src_blocks", torch.int32, dev)
     if dst_blocks is not None:
-        _ids(dst_blocks, "dst_blocks", src_blocks.shape, dev)
-    dst = kv_pool(k_pool, v_pool)
+        _tensor(dst_blocks, "dst_blocks", torch.int32, dev, src_blocks.shape)
+    dst = PkaKvPool(k_pool.data_ptr(), v_pool.data_ptr(), *shape)
     _run_on(dev, stream, "paged_kv4_expand", pool._ref, ctypes.byref(dst), src_blocks.data_ptr(),
             _ptr(dst_blocks), src_blocks.numel(), _err(err, dev))
 
@@ -500,62 +507,55 @@ def paged_kv4_decode_attn_ws(q, out, pool: Kv4Pool, block_tables, seq_lens, max_
     can overlap."""
     import torch
     dev = pool.device
-    B = seq_lens.shape[0]
-    for t, name in ((q, "q"), (out, "out")):
-        _tensor(t, name, torch.bfloat16, dev)
-        _want(t.dim() == 3 and t.shape[0] == B and t.shape[2] == pool.head_dim and
-              t.shape[1] == q.shape[1],
-              f"{name}: bf16 [{B}][Hq][{pool.head_dim}] is wanted, got {list(t.shape)}")
-    _tensor(block_tables, "block_tables", torch.int32, dev)
-    _want(block_tables.dim() == 2 and block_tables.shape[0] == B,
-          f"block_tables: int32 [{B}][max_blocks] is wanted, got {list(block_tables.shape)}")
-    _ids(seq_lens, "seq_lens", (B,), dev)
+    shape = B, Hq, _ = (seq_lens.shape[0], q.shape[1], pool.head_dim)
+    _tensor(q, "q", torch.bfloat16, dev, shape)
+    _tensor(out, "out", torch.bfloat16, dev, shape)
+    width = block_tables.shape[-1]
+    _tensor(block_tables, "block_tables", torch.int32, dev, (B, width))
+    _tensor(seq_lens, "seq_lens", torch.int32, dev, (B,))
     _tensor(workspace, "workspace", workspace.dtype, dev)
     par = PkaAttnParams(scale, softcap, window, _err(err, dev))
     _run_on(dev, stream, "paged_kv4_decode_attn_ws", q.data_ptr(), out.data_ptr(), pool._ref,
-            block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(), B, q.shape[1],
-            int(max_seq_len), ctypes.byref(par), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
+            block_tables.data_ptr(), width, seq_lens.data_ptr(), B, Hq, int(max_seq_len),
+            ctypes.byref(par), workspace.data_ptr(), workspace.nbytes)
 
 
 def paged_kv_ref_blocks(block_tables, seq_lens, refcounts, delta: int, err=None, stream=None):
     """Add ``delta`` to ``refcounts`` (int32 [num_blocks]) for every block the
     rows of ``block_tables`` use: +1 forks the requests, -1 frees them."""
     import torch
-    _tensor(block_tables, "block_tables", torch.int32)
-    dev = block_tables.device
-    _want(block_tables.dim() == 2, "block_tables: int32 [B][max_blocks] is wanted")
-    B, width = block_tables.shape
-    _ids(seq_lens, "seq_lens", (B,), dev)
-    _ids(refcounts, "refcounts", (refcounts.numel(),), dev)
+    dev = _cuda_device(block_tables, "block_tables")
+    B, width = seq_lens.shape[0], block_tables.shape[-1]
+    _tensor(block_tables, "block_tables", torch.int32, dev, (B, width))
+    _tensor(seq_lens, "seq_lens", torch.int32, dev, (B,))
+    n = refcounts.shape[0]
+    _tensor(refcounts, "refcounts", torch.int32, dev, (n,))
     _run_on(dev, stream, "paged_kv_ref_blocks", block_tables.data_ptr(), width,
-            seq_lens.data_ptr(), B, refcounts.numel(), int(delta), refcounts.data_ptr(),
-            _err(err, dev))
+            seq_lens.data_ptr(), B, n, int(delta), refcounts.data_ptr(), _err(err, dev))
 
 
 def _pool_list(pools):
     """The pools' device pointers as a C array, their blocks and bytes per block."""
-    import torch
     first = pools[0]
-    n = first.shape[0]
-    nbytes = first.numel() // max(n, 1) * first.element_size()
+    dev, n, nbytes = _cuda_device(first, "pools"), first.shape[0], first.nbytes
     for p in pools:
-        if not p.is_cuda or p.device != first.device or not p.is_contiguous():
-            raise ValueError("pools: contiguous tensors on one CUDA device are wanted")
-        if p.shape[0] != n or p.numel() * p.element_size() != n * nbytes:
-            raise ValueError("pools: tensors of equally many blocks of equal size are wanted")
-    return (ctypes.c_void_p * len(pools))(*[p.data_ptr() for p in pools]), n, nbytes, first.device
+        if p.device != dev or not p.is_contiguous() or p.shape[0] != n or p.nbytes != nbytes:
+            _refuse(p, "pools", f"a contiguous tensor of {n} blocks, {nbytes} bytes, on {dev}")
+    return ((ctypes.c_void_p * len(pools))(*[p.data_ptr() for p in pools]), n,
+            nbytes // max(n, 1), dev)
 
 
 def paged_kv_copy_blocks(pools, src, dst, err=None, stream=None):
     """Copy block ``src[i]`` to block ``dst[i]`` (int32) in each of ``pools``
     (tensors [num_blocks][...], of equal block size: K and V of every layer).
     The destinations must be distinct and none of them a source."""
+    import torch
     ptrs, n, nbytes, dev = _pool_list(pools)
-    _ids(src, "src", (src.numel(),), dev)
-    _ids(dst, "dst", src.shape, dev)
+    pairs = src.shape[0]
+    _tensor(src, "src", torch.int32, dev, (pairs,))
+    _tensor(dst, "dst", torch.int32, dev, (pairs,))
     _run_on(dev, stream, "paged_kv_copy_blocks", ptrs, len(ptrs), n, nbytes, src.data_ptr(),
-            dst.data_ptr(), src.numel(), _err(err, dev))
+            dst.data_ptr(), pairs, _err(err, dev))
 
 
 def paged_kv_compact(pools, refcounts, block_tables, seq_lens, new_refcounts, new_tables, remap,
@@ -566,14 +566,14 @@ def paged_kv_compact(pools, refcounts, block_tables, seq_lens, new_refcounts, ne
     ``new_refcounts`` and ``new_tables`` may be the old ones."""
     import torch
     ptrs, n, nbytes, dev = _pool_list(pools)
-    for t, name, size in ((refcounts, "refcounts", n), (new_refcounts, "new_refcounts", n),
-                          (remap, "remap", n), (moves, "moves", n + 2)):
-        _ids(t, name, (size,), dev)
-    _tensor(block_tables, "block_tables", torch.int32, dev)
-    _want(block_tables.dim() == 2, "block_tables: int32 [B][max_blocks] is wanted")
-    B, width = block_tables.shape
-    _ids(new_tables, "new_tables", (B, width), dev)
-    _ids(seq_lens, "seq_lens", (B,), dev)
+    i32, B, width = torch.int32, seq_lens.shape[0], block_tables.shape[-1]
+    _tensor(refcounts, "refcounts", i32, dev, (n,))
+    _tensor(new_refcounts, "new_refcounts", i32, dev, (n,))
+    _tensor(remap, "remap", i32, dev, (n,))
+    _tensor(moves, "moves", i32, dev, (n + 2,))
+    _tensor(block_tables, "block_tables", i32, dev, (B, width))
+    _tensor(new_tables, "new_tables", i32, dev, (B, width))
+    _tensor(seq_lens, "seq_lens", i32, dev, (B,))
     _run_on(dev, stream, "paged_kv_compact", ptrs, len(ptrs), n, nbytes, refcounts.data_ptr(),
             new_refcounts.data_ptr(), block_tables.data_ptr(), new_tables.data_ptr(), width,
             seq_lens.data_ptr(), B, remap.data_ptr(), moves.data_ptr(), _err(err, dev))

@@ -174,6 +174,8 @@ struct Kv4DecodeArgs {
   const uint8_t* k4;
   const uint8_t* v4;
   float k_scale, v_scale;
+  int32_t most_parts;  // set by the launcher: CTAs / Hkv
+  float even_share;    // and Hkv / CTAs
 };
 
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, int head_dim, int sms, cudaStream_t stream);
@@ -219,9 +221,6 @@ struct PlanArgs {
 cudaError_t launch_compact_plan(const PlanArgs& a, cudaStream_t stream);
 
 int device_sm_count();
-
-// Whether the split-K work line of these sizes fits the kernels' 32-bit arithmetic.
-bool splitk_line_fits(int32_t B, int32_t Hkv, int32_t max_blocks, int32_t window);
 
 // The argument checks of paged_decode_attn (host only, nothing launched):
 // PKA_OK or the pka_status the entry points return for these arguments.

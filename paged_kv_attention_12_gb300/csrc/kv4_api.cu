@@ -195,7 +195,11 @@ int paged_kv4_decode_attn_ws(const void* q, void* out, const pka_kv4_pool* kv,
   st = kv4_layout(B, Hq, kv->num_kv_heads, kv->head_dim, max_seq_len, params->window, &L);
   if (st != PKA_OK) return st;
   if (workspace_bytes < L.total()) return PKA_ERR_WORKSPACE;
-  if (!pka::splitk_line_fits(B, kv->num_kv_heads, max_blocks, params->window))
+  // the work line (visible blocks and a fixed cost of 16 units per segment) in
+  // the kernels' 32-bit arithmetic
+  int64_t per = max_blocks;
+  if (params->window > 0) per = std::min<int64_t>(per, (params->window - 1) / 16 + 2);
+  if (static_cast<int64_t>(B) * kv->num_kv_heads * (per + 16) > (int64_t(1) << 30))
     return PKA_ERR_SHAPE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   pka::Kv4DecodeArgs a{};

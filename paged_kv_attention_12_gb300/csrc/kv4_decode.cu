@@ -43,13 +43,18 @@ namespace pka {
 
 namespace {
 
+// The shortest piece worth a merge, in tiles.
+constexpr int kMinPiece = 16;
+
+// A line piece's fixed cost, in tiles.
+constexpr int kLinePieceCost = 16;
+
 constexpr float kGrow = 7.f;
 constexpr float kShift = 8.f;
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                               uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -81,19 +86,8 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ uint16_t lds16(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
-  return v;
-}
+constexpr int kMaxParts = 34;  // partial slots per segment (33 at most), padded
+constexpr int kLens = 320;  // requests whose lengths a CTA keeps in shared memory
 
 template <int D, int NW_, int STAGES_>
 struct Kv4Shape {
@@ -101,10 +95,18 @@ struct Kv4Shape {
   static constexpr int UNITS = D / kUnitChannels;
   static constexpr int kTile = UNITS * kUnitBytes;  // one block and head of K (or V)
   static constexpr int kRing = NW * STAGES * 2 * kTile;
-  static constexpr int kLen = kLenCache * 4;
-  // the warps' (max, sum) per head, and a flag
-  static constexpr int kMl = NW * 8 * 8 + 16;
-  static constexpr int smem(int G) { return kRing + kLen + kMl + NW * G * D * 4; }
+  static constexpr int kLen = 2 * kLens * 4;
+  // the warps' (max, sum) per head, later the pieces' weights; the plan's
+  // piece; a flag
+  static constexpr int kMl = (NW * 8 * 8 > 8 * kMaxParts * 4 ? NW * 8 * 8 : 8 * kMaxParts * 4) +
+                             (sizeof(Piece) + 15) / 16 * 16 + 16;
+  static constexpr int kFrags = UNITS * 4 * 2 * 32; // float4 of a warp's O state
+  static constexpr int kItems = (kFrags + NW * 32 - 1) / (NW * 32);
+  // the warps' O states are merged kRound warps at a time
+  static constexpr int kRounds = (D == 256 && NW > 8) ? 2 : 1;
+  static constexpr int kRound = NW / kRounds;
+  static_assert(NW % kRounds == 0, "equal rounds");
+  static constexpr int kSmem = kRing + kLen + kMl + kRound * kFrags * 16;
 };
 
 // The four A registers of K's k-step S (0..7) of a unit: words of row g and
@@ -132,26 +134,23 @@ __device__ __forceinline__ void v_step(float (&o)[4], uint32_t lo0, uint32_t hi0
                 p1);
 }
 
-// One tile (16 keys of one head) for one warp.  Fragment roles (g = lane / 4,
-// t = lane % 4): K rows are keys g and g + 8, the lane's channels 32 t ..
-// 32 t + 31 of every unit; S^T holds those keys of heads 2t and 2t + 1; V's
-// lane holds group g of every unit for keys 2t, 2t + 1, 2t + 8, 2t + 9, and
-// O^T its 16 channels of heads 2t and 2t + 1.
+// S^T of one tile for one warp.  Fragment roles (g = lane / 4, t = lane % 4):
+// the rows are keys g and g + 8, the lane's channels 32 t .. 32 t + 31 of every
+// unit; S^T holds those keys of heads 2t and 2t + 1.
 template <int D>
-__device__ __forceinline__ void kv4_tile(uint32_t tile, const uint32_t (&bq)[D / 128][8][2],
-                                         float (&o)[D / 128][8][4], float (&m)[2], float (&l)[2],
-                                         float f0, float f1, float softcap, float inv_cap,
-                                         bool edge, int tok0, int t_lo, int pos, int lane) {
-  constexpr int UNITS = D / kUnitChannels;
-  const int g = lane >> 2, t = lane & 3;
+__device__ __forceinline__ void kv4_scores(const uint8_t* tile, const uint32_t (&bq)[D / 128][8][2],
+                                           float (&x)[4], int lane) {
   float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-  for (int u = 0; u < UNITS; ++u) {
-    const uint32_t base = tile + u * kUnitBytes;
-    const uint4 r0 = lds128(base + lane * 16);
-    const uint4 r1 = lds128(base + 512 + lane * 16);
-    const uint32_t c0 = e4m3x2_to_f16x2(lds16(base + kUnitCodes + g * 8 + t * 2));
-    const uint32_t c1 = e4m3x2_to_f16x2(lds16(base + kUnitCodes + g * 8 + t * 2 + 64));
+  for (int u = 0; u < D / kUnitChannels; ++u) {
+    const uint8_t* base = tile + u * kUnitBytes;
+    const uint4 r0 = *reinterpret_cast<const uint4*>(base + lane * 16);
+    const uint4 r1 = *reinterpret_cast<const uint4*>(base + 512 + lane * 16);
+    // scales of groups 2t and 2t + 1 of key g: byte 8 g + 2 t = 2 lane
+    const uint32_t c0 =
+        e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(base + kUnitCodes + lane * 2));
+    const uint32_t c1 =
+        e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(base + kUnitCodes + 64 + lane * 2));
     const uint32_t s0[2] = {prmt(c0, c0, 0x1010u), prmt(c0, c0, 0x3232u)};
     const uint32_t s1[2] = {prmt(c1, c1, 0x1010u), prmt(c1, c1, 0x3232u)};
     k_step<0>(s[0], r0, r1, s0, s1, bq[u][0][0], bq[u][0][1]);
@@ -163,28 +162,99 @@ __device__ __forceinline__ void kv4_tile(uint32_t tile, const uint32_t (&bq)[D /
     k_step<6>(s[0], r0, r1, s0, s1, bq[u][6][0], bq[u][6][1]);
     k_step<7>(s[1], r0, r1, s0, s1, bq[u][7][0], bq[u][7][1]);
   }
-  bool ok_lo = true, ok_hi = true;
-  if (edge) {
-    ok_lo = tok0 + g >= t_lo && tok0 + g <= pos;
-    ok_hi = tok0 + g + 8 >= t_lo && tok0 + g + 8 <= pos;
-  }
-  float x[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float v = (s[0][i] + s[1][i]) * ((i & 1) ? f1 : f0);
-    if (softcap > 0.f) {
-      // v = logit / cap; tanh(y) = 1 - 2 / (e^{2y} + 1), absolute error ~1e-7
-      const float e = fast_exp2(fminf(2.f * kLog2e * v, 126.f));
-      v = softcap * (1.f - __fdividef(2.f, e + 1.f)) * kLog2e;
+  for (int i = 0; i < 4; ++i) x[i] = s[0][i] + s[1][i];
+}
+
+// O^T += V^T P^T of one tile.  The lane holds group g of every unit for keys
+// 2t, 2t + 1, 2t + 8, 2t + 9; O^T its 16 channels of heads 2t and 2t + 1.
+// keep: byte masks of the scales of the four keys (0: an invisible key, whose
+// stale scale may be NaN).
+template <int D, bool EDGE>
+__device__ __forceinline__ void kv4_values(const uint8_t* tile, float (&o)[D / 128][8][4],
+                                           uint32_t pb0, uint32_t pb1, uint32_t keep0,
+                                           uint32_t keep1, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int u = 0; u < D / kUnitChannels; ++u) {
+    const uint8_t* base = tile + u * kUnitBytes;
+    const uint8_t* row = base + g * 128;
+    const int at = (t * 16) ^ ((g & 1) * 64);
+    const uint4 a = *reinterpret_cast<const uint4*>(row + at);         // keys 2t (x, y), 2t + 1
+    const uint4 b = *reinterpret_cast<const uint4*>(row + (at ^ 64));  // keys 2t + 8, 2t + 9
+    const uint8_t* sc = base + kUnitCodes + g * 16 + t * 2;
+    uint32_t ca = *reinterpret_cast<const uint16_t*>(sc);
+    uint32_t cb = *reinterpret_cast<const uint16_t*>(sc + 8);
+    if constexpr (EDGE) {
+      ca &= keep0;
+      cb &= keep1;
     }
-    x[i] = ((i & 2) ? ok_hi : ok_lo) ? v : -INFINITY;
+    const uint32_t sa = e4m3x2_to_f16x2(static_cast<uint16_t>(ca));
+    const uint32_t sb = e4m3x2_to_f16x2(static_cast<uint16_t>(cb));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t a0 = j ? a.y : a.x, a1 = j ? a.w : a.z;
+      const uint32_t b0 = j ? b.y : b.x, b1 = j ? b.w : b.z;
+      // nibble pairs (key 2t, key 2t + 1) of the even and the odd channels
+      const uint32_t alo = (a0 & 0x0f0f0f0fu) | ((a1 << 4) & 0xf0f0f0f0u);
+      const uint32_t ahi = ((a0 >> 4) & 0x0f0f0f0fu) | (a1 & 0xf0f0f0f0u);
+      const uint32_t blo = (b0 & 0x0f0f0f0fu) | ((b1 << 4) & 0xf0f0f0f0u);
+      const uint32_t bhi = ((b0 >> 4) & 0x0f0f0f0fu) | (b1 & 0xf0f0f0f0u);
+      v_step<0>(o[u][j * 4 + 0], alo, ahi, blo, bhi, sa, sb, pb0, pb1);
+      v_step<1>(o[u][j * 4 + 1], alo, ahi, blo, bhi, sa, sb, pb0, pb1);
+      v_step<2>(o[u][j * 4 + 2], alo, ahi, blo, bhi, sa, sb, pb0, pb1);
+      v_step<3>(o[u][j * 4 + 3], alo, ahi, blo, bhi, sa, sb, pb0, pb1);
+    }
   }
-  const bool grow = fmaxf(x[0], x[2]) > m[0] + kGrow || fmaxf(x[1], x[3]) > m[1] + kGrow;
-  if (__any_sync(0xffffffffu, grow)) {
+}
+
+// NT tiles for one warp: scores, softmax step, values.  EDGE (NT = 1): the
+// tile holds keys outside [t_lo, pos].
+template <int D, int NT, bool EDGE, bool CAP>
+__device__ __forceinline__ void kv4_tiles(const uint8_t* const (&tile)[NT],
+                                          const uint32_t (&bq)[D / 128][8][2],
+                                          float (&o)[D / 128][8][4], float (&m)[2], float (&l)[2],
+                                          float f0, float f1, float softcap, int tok0, int t_lo,
+                                          int pos, int lane) {
+  constexpr int UNITS = D / kUnitChannels;
+  static_assert(!EDGE || NT == 1, "an edge tile goes alone");
+  const int g = lane >> 2, t = lane & 3;
+  float x[NT][4];
+#pragma unroll
+  for (int k = 0; k < NT; ++k) kv4_scores<D>(tile[k], bq, x[k], lane);
+  uint32_t keep0 = 0xffffu, keep1 = 0xffffu;
+  bool ok_lo = true, ok_hi = true;
+  if constexpr (EDGE) {
+    const int lo = t_lo - tok0, hi = pos - tok0;  // visible: lo <= key <= hi
+    ok_lo = g >= lo && g <= hi;
+    ok_hi = g + 8 >= lo && g + 8 <= hi;
+    const int k0 = 2 * t;
+    keep0 = (k0 >= lo && k0 <= hi ? 0xffu : 0u) | (k0 + 1 >= lo && k0 + 1 <= hi ? 0xff00u : 0u);
+    keep1 = (k0 + 8 >= lo && k0 + 8 <= hi ? 0xffu : 0u) |
+            (k0 + 9 >= lo && k0 + 9 <= hi ? 0xff00u : 0u);
+  }
+  float top0 = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < NT; ++k) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float v = x[k][i] * ((i & 1) ? f1 : f0);
+      if constexpr (CAP) {
+        // v = logit / cap; tanh(y) = 1 - 2 / (e^{2y} + 1), absolute error ~1e-7
+        const float e = fast_exp2(fminf(2.f * kLog2e * v, 126.f));
+        v = softcap * (1.f - __fdividef(2.f, e + 1.f)) * kLog2e;
+      }
+      if constexpr (EDGE) v = ((i & 2) ? ok_hi : ok_lo) ? v : -INFINITY;
+      x[k][i] = v;
+    }
+    top0 = fmaxf(top0, fmaxf(x[k][0], x[k][2]));
+    top1 = fmaxf(top1, fmaxf(x[k][1], x[k][3]));
+  }
+  if (__any_sync(0xffffffffu, top0 > m[0] + kGrow || top1 > m[1] + kGrow)) {
     float alpha[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      float mx = fmaxf(x[j], x[j + 2]);
+      float mx = j ? top1 : top0;
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1)
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
@@ -206,50 +276,101 @@ __device__ __forceinline__ void kv4_tile(uint32_t tile, const uint32_t (&bq)[D /
   // a head whose keys so far are all invisible or NaN keeps m = -inf
   const float r0 = (m[0] == -INFINITY) ? 0.f : m[0] - kShift;
   const float r1 = (m[1] == -INFINITY) ? 0.f : m[1] - kShift;
-  const float p0 = fast_exp2(x[0] - r0), p1 = fast_exp2(x[1] - r1);
-  const float p2 = fast_exp2(x[2] - r0), p3 = fast_exp2(x[3] - r1);
-  l[0] += p0 + p2;
-  l[1] += p1 + p3;
-  const uint32_t pb0 = movmatrix_trans(pack_f16x2(p0, p1));  // keys 2t, 2t + 1 of head g
-  const uint32_t pb1 = movmatrix_trans(pack_f16x2(p2, p3));  // keys 2t + 8, 2t + 9
-
 #pragma unroll
-  for (int u = 0; u < UNITS; ++u) {
-    const uint32_t base = tile + (UNITS + u) * kUnitBytes;
-    const uint32_t row = base + g * 128 + ((t * 16) ^ ((g & 1) * 64));
-    const uint4 a = lds128(row);                       // keys 2t (x, y) and 2t + 1 (z, w)
-    const uint4 b = lds128(base + g * 128 + ((t * 16 + 64) ^ ((g & 1) * 64)));
-    uint32_t ca = lds16(base + kUnitCodes + g * 16 + t * 2);
-    uint32_t cb = lds16(base + kUnitCodes + g * 16 + t * 2 + 8);
-    if (edge) {
-      // stale slots may hold the scale NaN: an invisible key's value is 0
-      const int k0 = tok0 + 2 * t;
-      if (k0 < t_lo || k0 > pos) ca &= 0xff00u;
-      if (k0 + 1 < t_lo || k0 + 1 > pos) ca &= 0x00ffu;
-      if (k0 + 8 < t_lo || k0 + 8 > pos) cb &= 0xff00u;
-      if (k0 + 9 < t_lo || k0 + 9 > pos) cb &= 0x00ffu;
-    }
-    const uint32_t sa = e4m3x2_to_f16x2(static_cast<uint16_t>(ca));
-    const uint32_t sb = e4m3x2_to_f16x2(static_cast<uint16_t>(cb));
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t a0 = j ? a.y : a.x, a1 = j ? a.w : a.z;
-      const uint32_t b0 = j ? b.y : b.x, b1 = j ? b.w : b.z;
-      // nibble pairs (key 2t, key 2t + 1) of the even and the odd channels
-      const uint32_t alo = (a0 & 0x0f0f0f0fu) | ((a1 << 4) & 0xf0f0f0f0u);
-      const uint32_t ahi = ((a0 >> 4) & 0x0f0f0f0fu) | (a1 & 0xf0f0f0f0u);
-      const uint32_t blo = (b0 & 0x0f0f0f0fu) | ((b1 << 4) & 0xf0f0f0f0u);
-      const uint32_t bhi = ((b0 >> 4) & 0x0f0f0f0fu) | (b1 & 0xf0f0f0f0u);
-      v_step<0>(o[u][j * 4 + 0], alo, ahi, blo, bhi, sa, sb, pb0, pb1);
-      v_step<1>(o[u][j * 4 + 1], alo, ahi, blo, bhi, sa, sb, pb0, pb1);
-      v_step<2>(o[u][j * 4 + 2], alo, ahi, blo, bhi, sa, sb, pb0, pb1);
-      v_step<3>(o[u][j * 4 + 3], alo, ahi, blo, bhi, sa, sb, pb0, pb1);
-    }
+  for (int k = 0; k < NT; ++k) {
+    const float p0 = fast_exp2(x[k][0] - r0), p1 = fast_exp2(x[k][1] - r1);
+    const float p2 = fast_exp2(x[k][2] - r0), p3 = fast_exp2(x[k][3] - r1);
+    l[0] += p0 + p2;
+    l[1] += p1 + p3;
+    const uint32_t pb0 = movmatrix_trans(pack_f16x2(p0, p1));  // keys 2t, 2t + 1 of head g
+    const uint32_t pb1 = movmatrix_trans(pack_f16x2(p2, p3));  // keys 2t + 8, 2t + 9
+    kv4_values<D, EDGE>(tile[k] + UNITS * kUnitBytes, o, pb0, pb1, keep0, keep1, lane);
   }
 }
 
-template <int D, int NW, int STAGES>
-__global__ void __launch_bounds__(NW * 32, 1)
+// Pieces when the segments (request, KV head) number at most the CTAs: one
+// piece per CTA, so that no CTA pays a piece's fixed cost twice.  theta is the
+// smallest of 32 lengths with sum over segments of ceil(n / theta) <= CTAs;
+// segment n gets that many pieces of equal length (one: its output is written
+// without partials).  One warp of every CTA computes the plan, the same in all
+// of them; nbf holds the segments' tiles (an empty one counts a half, so that
+// it gets a piece of its own).
+__device__ __forceinline__ int theta_parts(float nb, float rtheta) {
+  // 2^23 + ceil(nb * rtheta), rounded up
+  return __float_as_int(__fmaf_ru(nb, rtheta, 8388608.f)) - 0x4b000000;
+}
+
+__device__ __forceinline__ bool theta_piece(const Kv4DecodeArgs& ka, const int* slen,
+                                            const float* nbf, int lane, int cta, Piece& p) {
+  const DecodeArgs& a = ka.base;
+  int itiles = 0, ilongest = 0;
+  for (int b = lane; b < a.batch; b += 32) {
+    const int nb = static_cast<int>(nbf[b]);
+    itiles += nb;
+    ilongest = max(ilongest, nb);
+  }
+  const float tiles = static_cast<float>(__reduce_add_sync(0xffffffffu, itiles));
+  const float longest = static_cast<float>(__reduce_max_sync(0xffffffffu, ilongest));
+  // from the even share (at least split_blocks, which bounds the workspace's
+  // slots, and kMinPiece tiles): 24 steps to twice of it, which fits whenever
+  // the segments number at most half the CTAs, then 7 up to the longest
+  const float lo = fmaxf(static_cast<float>(max(a.split_blocks, kMinPiece)),
+                         tiles * ka.even_share);
+  const float hi = fmaxf(longest, 2.f * lo);
+  float rtheta = __fdividef(1.f, lane < 25 ? lo + lo * (lane * (1.f / 24.f))
+                                           : 2.f * lo + (hi - 2.f * lo) * ((lane - 24) * (1.f / 7.f)));
+  int sum = 0;
+#pragma unroll 4
+  for (int b = 0; b < a.batch; b += 4) {  // padded with zeros, which give none
+    const float4 n = *reinterpret_cast<const float4*>(nbf + b);
+    sum += theta_parts(n.x, rtheta) + theta_parts(n.y, rtheta) + theta_parts(n.z, rtheta) +
+           theta_parts(n.w, rtheta);
+  }
+  if (lane == 31) {  // one piece each
+    rtheta = __fdividef(0.999f, hi);
+    sum = 0;
+  }
+  const unsigned fits = __ballot_sync(0xffffffffu, sum <= ka.most_parts);
+  rtheta = __shfl_sync(0xffffffffu, rtheta, __ffs(fits) - 1);
+  // the segment of piece `cta`: pieces lie in (request, head, part) order
+  int before = 0;
+  for (int base = 0; base < a.batch; base += 32) {
+    const int b = base + lane;
+    const float nb = b < a.batch ? nbf[b] : 0.f;
+    const int k = b < a.batch ? min(theta_parts(nb, rtheta), a.num_splits) : 0;
+    const int incl = warp_incl_scan(k * a.Hkv, lane);
+    const unsigned m = __ballot_sync(0xffffffffu, cta < before + incl);
+    if (m != 0) {
+      const int src = __ffs(m) - 1;
+      const int parts = __shfl_sync(0xffffffffu, k, src);
+      const int in = cta - before - __shfl_sync(0xffffffffu, incl - k * a.Hkv, src);
+      const float rparts = __fdividef(1.f, static_cast<float>(parts));
+      p.b = base + src;
+      p.kvh = static_cast<int>((static_cast<float>(in) + 0.5f) * rparts);
+      p.slot = in - p.kvh * parts;
+      p.npieces = parts;
+      const ReqGeo geo = geo_of_len(a, slen[p.b]);
+      // piece k starts at tile floor(k * n / parts), in fp32 and the same for
+      // both pieces that meet there
+      const float each = static_cast<float>(geo.nb) * rparts;
+      const int t0 = min(static_cast<int>(each * p.slot), geo.nb);
+      const int t1 = p.slot + 1 == parts ? geo.nb : min(static_cast<int>(each * (p.slot + 1)), geo.nb);
+      p.j0 = geo.jlo + t0;
+      p.ntiles = t1 - t0;
+      p.t_lo = geo.t_lo;
+      p.pos = geo.pos;
+      p.qrow = p.b;
+      return true;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return false;
+}
+
+// LINE: more segments than CTAs, which then take several pieces of the
+// split-K line each; else one piece per CTA.
+template <int D, int NW, int STAGES, int CTAS, bool CAP, bool LINE>
+__global__ void __launch_bounds__(NW * 32, CTAS)
     kv4_decode_kernel(const __grid_constant__ Kv4DecodeArgs ka) {
   using S = Kv4Shape<D, NW, STAGES>;
   constexpr int UNITS = S::UNITS;
@@ -257,31 +378,52 @@ __global__ void __launch_bounds__(NW * 32, 1)
   const DecodeArgs& a = ka.base;
   const int G = a.Hq / a.Hkv;
   int* slen = reinterpret_cast<int*>(smem + S::kRing);
+  float* nbf = reinterpret_cast<float*>(slen + kLens);
   float2* ml = reinterpret_cast<float2*>(smem + S::kRing + S::kLen);  // [NW][8]
-  volatile int* flag = reinterpret_cast<int*>(smem + S::kRing + S::kLen + NW * 8 * 8);
-  float* st = reinterpret_cast<float*>(smem + S::kRing + S::kLen + S::kMl);  // [NW][G][D]
+  Piece* plan = reinterpret_cast<Piece*>(smem + S::kRing + S::kLen + S::kMl - 16 - sizeof(Piece));
+  volatile int* flag = reinterpret_cast<int*>(smem + S::kRing + S::kLen + S::kMl - 16);
+  float4* st = reinterpret_cast<float4*>(smem + S::kRing + S::kLen + S::kMl);  // [kRound][kFrags]
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t ring = smem_u32(smem) + warp * STAGES * 2 * S::kTile;
+  uint8_t* ring = smem + warp * STAGES * 2 * S::kTile;
+  const uint32_t ring_addr = smem_u32(ring);
 
-  for (int b = threadIdx.x; b < min(a.batch, kLenCache); b += NW * 32)
-    slen[b] = req_len_of(a, 0, 0, a.seq_lens[b]);
+  for (int b = threadIdx.x; b < kLens; b += NW * 32) {
+    const int len = b < a.batch ? req_len_of(a, 0, 0, a.seq_lens[b]) : 0;
+    slen[b] = len;
+    nbf[b] = b < a.batch ? fmaxf(static_cast<float>(geo_of_len(a, len).nb), 0.5f) : 0.f;
+  }
   __syncthreads();
 
-  PieceIter iter;
-  iter.init(a, slen, lane, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
+  PieceIterT<kLinePieceCost> iter;
+  Piece pc;
+  bool have;
+  if constexpr (LINE) {
+    iter.init(a, slen, lane, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
+    have = iter.next(pc, true);
+  } else {
+    if (warp == 0) {
+      Piece p;
+      const bool any = theta_piece(ka, slen, nbf, lane, static_cast<int>(blockIdx.x), p);
+      if (lane == 0) {
+        p.fill_from = any;  // (a field of the line's pieces)
+        *plan = p;
+      }
+    }
+    __syncthreads();
+    pc = *plan;
+    have = pc.fill_from != 0;
+  }
   const float inv_cap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
   const float lscale = a.scale * ka.k_scale * (a.softcap > 0.f ? inv_cap : kLog2e);
 
-  Piece pc;
-  bool have = iter.next(pc, true);
-  int mine = 0;        // tiles of the piece that are this warp's
-  int ids = 0;         // block ids of its tiles base .. base + 31, one per lane
+  int first = 0, mine = 0;  // this warp's tiles of the piece: first .. first + mine - 1
+  int ids = 0;              // block ids of its tiles base .. base + 31, one per lane
   auto load_ids = [&](const Piece& P, int base) {
-    const int i = warp + (base + lane) * NW;
+    const int i = base + lane;
     int id = -1;
-    if (i < P.ntiles) {
-      id = a.tables[static_cast<size_t>(P.b) * a.max_blocks + P.j0 + i];
+    if (i < mine) {
+      id = a.tables[static_cast<size_t>(P.b) * a.max_blocks + P.j0 + first + i];
       if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.num_blocks)) {
         report(a.err, PKA_DEVERR_BAD_TABLE);
         id = -1;
@@ -295,7 +437,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
     const uint32_t bytes = id >= 0 ? 16u : 0u;  // a bad id reads as zeros
     const long long off =
         (static_cast<long long>(max(id, 0)) * a.Hkv + P.kvh) * S::kTile;
-    const uint32_t dst = ring + (n % STAGES) * 2 * S::kTile;
+    const uint32_t dst = ring_addr + (n % STAGES) * 2 * S::kTile;
 #pragma unroll
     for (int c = 0; c < S::kTile / 512; ++c) {
       cp_async16(dst + c * 512 + lane * 16, ka.k4 + off + c * 512 + lane * 16, bytes);
@@ -311,10 +453,11 @@ __global__ void __launch_bounds__(NW * 32, 1)
     }
   };
   auto prologue = [&](const Piece& P) {
-    mine = P.ntiles > warp ? (P.ntiles - warp + NW - 1) / NW : 0;
+    first = P.ntiles * warp / NW;
+    mine = P.ntiles * (warp + 1) / NW - first;
     ids = load_ids(P, 0);
 #pragma unroll
-    for (int n = 0; n < STAGES - 1; ++n) {
+    for (int n = 0; n < STAGES; ++n) {
       if (n < mine) issue(P, n);
       cp_async_commit();
     }
@@ -369,28 +512,55 @@ __global__ void __launch_bounds__(NW * 32, 1)
       for (int i = 0; i < 8; ++i) o[u][i][0] = o[u][i][1] = o[u][i][2] = o[u][i][3] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-    const int count = mine;
-    for (int n = 0; n < count; ++n) {
-      cp_async_wait<STAGES - 2>();
-      __syncwarp();  // every lane's part of tile n has landed; tile n - 1 is consumed
-      const int ahead = n + STAGES - 1;
+    // Invariant: tiles n .. n + STAGES - 1 are requested, one group each (empty
+    // groups behind the last).
+    const int count = mine, tok_first = (pc.j0 + first) * kBlockSize;
+    int n = 0;
+    auto is_edge = [&](int k) {
+      const int tok0 = tok_first + k * kBlockSize;
+      return tok0 < pc.t_lo || tok0 + kBlockSize - 1 > pc.pos;
+    };
+    auto refill = [&](int k) {  // the slot of tile k is free
+      const int ahead = k + STAGES;
       if (ahead < count) {
         if ((ahead & 31) == 0) ids = load_ids(pc, ahead);
         issue(pc, ahead);
       }
       cp_async_commit();
-      const int tok0 = (pc.j0 + warp + n * NW) * kBlockSize;
-      const bool edge = tok0 < pc.t_lo || tok0 + kBlockSize - 1 > pc.pos;
-      kv4_tile<D>(ring + (n % STAGES) * 2 * S::kTile, bq, o, m, l, f0, f1, a.softcap, inv_cap,
-                  edge, tok0, pc.t_lo, pc.pos, lane);
+    };
+    while (n < count) {
+      const uint8_t* t0 = ring + (n % STAGES) * 2 * S::kTile;
+      if (n + 1 < count && !is_edge(n) && !is_edge(n + 1)) {
+        cp_async_wait<STAGES - 2>();
+        __syncwarp();  // every lane's part of the tiles has landed
+        const uint8_t* const tiles[2] = {t0, ring + ((n + 1) % STAGES) * 2 * S::kTile};
+        kv4_tiles<D, 2, false, CAP>(tiles, bq, o, m, l, f0, f1, a.softcap, 0, 0, 0, lane);
+        __syncwarp();
+        refill(n);
+        refill(n + 1);
+        n += 2;
+      } else {
+        cp_async_wait<STAGES - 1>();
+        __syncwarp();
+        const uint8_t* const tiles[1] = {t0};
+        kv4_tiles<D, 1, true, CAP>(tiles, bq, o, m, l, f0, f1, a.softcap,
+                                   tok_first + n * kBlockSize, pc.t_lo, pc.pos, lane);
+        __syncwarp();
+        refill(n);
+        ++n;
+      }
     }
-    __syncwarp();
 
     Piece nx;
-    const bool have_next = iter.next(nx, true);
-    if (have_next) prologue(nx);
+    bool have_next = false;
+    if constexpr (LINE) {
+      have_next = iter.next(nx, true);
+      if (have_next) prologue(nx);
+    }
 
-    // ---- the warps' states through shared memory, merged in warp order
+    // ---- the warps' states merged in warp order: (max, sum) first, from which
+    // every warp takes the factor of its own O, then the sum of the scaled O
+    // states through shared memory (a warp without tiles holds zeros)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -399,65 +569,89 @@ __global__ void __launch_bounds__(NW * 32, 1)
       ml[warp * 8 + 2 * t] = make_float2(m[0], l[0]);
       ml[warp * 8 + 2 * t + 1] = make_float2(m[1], l[1]);
     }
-    if (count > 0) {
+    __syncthreads();
+    if constexpr (!LINE) pc = *plan;  // not kept in registers over the loop
+    const bool split = pc.npieces > 1;
+    const size_t head0 = static_cast<size_t>(pc.qrow) * a.Hq + pc.kvh * G;
+    const int slot = min(pc.slot, a.num_splits - 1);
+    // lane (g, t) takes warps g and g + 8
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int h = 2 * t + j;
-        if (h < G) {
+    for (int j = 0; j < 2; ++j) {
+      const float2 none = make_float2(-INFINITY, 0.f);
+      const float2 v0 = g < NW ? ml[g * 8 + 2 * t + j] : none;
+      const float2 v1 = g + 8 < NW ? ml[(g + 8) * 8 + 2 * t + j] : none;
+      float M = fmaxf(v0.x, v1.x);
 #pragma unroll
-          for (int u = 0; u < UNITS; ++u)
+      for (int off = 4; off < 32; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+      if (M == -INFINITY) M = 0.f;
+      float den = ((v0.x == -INFINITY) ? 1.f : fast_exp2(v0.x - M)) * v0.y +
+                  ((v1.x == -INFINITY) ? 1.f : fast_exp2(v1.x - M)) * v1.y;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<float4*>(st + (warp * G + h) * D + u * kUnitChannels + g * 16 +
-                                         i * 4) =
+      for (int off = 4; off < 32; off <<= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
+      const float f = den == 0.f ? 0.f
+                                 : ((m[j] == -INFINITY) ? 1.f : fast_exp2(m[j] - M)) *
+                                       __fdividef(ka.v_scale, den);
+      // P carries a factor 2^kShift, the same in every piece; a NaN sum keeps
+      // its weight, so that the merge of the pieces passes it on
+      if (split && warp == 0 && g == 0 && 2 * t + j < G)
+        __stcg(a.partial_lse + (head0 + 2 * t + j) * a.num_splits + slot,
+               den == 0.f ? -INFINITY : (isnan(den) ? M : M + log2f(den)) * kLn2);
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          o[u][i][j] *= f;
+          o[u][i][2 + j] *= f;
+        }
+    }
+    float4 y[S::kItems];
+#pragma unroll
+    for (int r = 0; r < S::kRounds; ++r) {
+      if (r > 0) __syncthreads();  // the last round's states are read
+      if (warp / S::kRound == r && 2 * t < G) {
+        float4* row = st + (warp - r * S::kRound) * S::kFrags + lane;
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              row[((u * 4 + i) * 2 + j) * 32] =
                   make_float4(o[u][2 * i][j], o[u][2 * i][2 + j], o[u][2 * i + 1][j],
                               o[u][2 * i + 1][2 + j]);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < S::kItems; ++k) {
+        const int item = threadIdx.x + k * NW * 32;
+        if (item >= S::kFrags || 2 * (item & 3) + ((item >> 5) & 1) >= G) continue;
+        if (r == 0) y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < S::kRound; ++w) {
+          const float4 x = st[w * S::kFrags + item];
+          y[k].x += x.x;
+          y[k].y += x.y;
+          y[k].z += x.z;
+          y[k].w += x.w;
         }
       }
     }
-    __syncthreads();
-    const bool split = !iter.direct;
-    const bool has_keys = pc.ntiles > 0;
-    if (!split || !has_keys || pc.slot < a.num_splits) {
-      const int warps = min(NW, pc.ntiles);  // warps that had a tile
-      for (int item = threadIdx.x; item < G * (D / 4); item += NW * 32) {
-        const int h = item / (D / 4), d0 = item % (D / 4) * 4;
-        float M = -INFINITY;
-        for (int w = 0; w < warps; ++w) M = fmaxf(M, ml[w * 8 + h].x);
-        const float Ms = (M == -INFINITY) ? 0.f : M;
-        float den = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int w = 0; w < warps; ++w) {
-          const float2 v = ml[w * 8 + h];
-          const float4 x = *reinterpret_cast<const float4*>(st + (w * G + h) * D + d0);
-          const float sc = (v.x == -INFINITY) ? 1.f : fast_exp2(v.x - Ms);
-          den = fmaf(sc, v.y, den);
-          acc.x = fmaf(sc, x.x, acc.x);
-          acc.y = fmaf(sc, x.y, acc.y);
-          acc.z = fmaf(sc, x.z, acc.z);
-          acc.w = fmaf(sc, x.w, acc.w);
-        }
-        const float inv = den == 0.f ? 0.f : ka.v_scale / den;
-        acc.x *= inv;
-        acc.y *= inv;
-        acc.z *= inv;
-        acc.w *= inv;
-        const size_t head = static_cast<size_t>(pc.qrow) * a.Hq + pc.kvh * G + h;
-        if (split && has_keys) {
-          const size_t row = head * a.num_splits + pc.slot;
-          __stcg(reinterpret_cast<float4*>(a.partial_o + row * D + d0), acc);
-          // a NaN sum keeps its weight, so that the merge passes it on
-          if (d0 == 0)
-            __stcg(a.partial_lse + row, den == 0.f  ? -INFINITY
-                                        : isnan(den) ? Ms * kLn2
-                                                     : (Ms + log2f(den)) * kLn2);
-        } else {
-          *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + head * D + d0) =
-              make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-        }
-      }
+#pragma unroll
+    for (int k = 0; k < S::kItems; ++k) {
+      const int item = threadIdx.x + k * NW * 32;
+      const int il = item & 31, ij = (item >> 5) & 1, ii = (item >> 6) & 3, iu = item >> 8;
+      const int h = 2 * (il & 3) + ij;
+      const int d0 = iu * kUnitChannels + (il >> 2) * 16 + ii * 4;
+      if (item >= S::kFrags || h >= G) continue;
+      if (split)
+        __stcg(reinterpret_cast<float4*>(a.partial_o +
+                                         ((head0 + h) * a.num_splits + slot) * D + d0),
+               y[k]);
+      else
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + (head0 + h) * D + d0) =
+            make_uint2(pack_bf16x2(y[k].x, y[k].y), pack_bf16x2(y[k].z, y[k].w));
     }
-    if (split && has_keys) {
+    if (split) {
       // ---- the piece that arrives last at its segment merges the partials
       const int np = min(pc.npieces, a.num_splits);
       __syncthreads();
@@ -475,53 +669,121 @@ __global__ void __launch_bounds__(NW * 32, 1)
       }
       __syncthreads();
       if (*flag != 0) {
-        for (int item = threadIdx.x; item < G * (D / 4); item += NW * 32) {
-          const int h = item / (D / 4), d0 = item % (D / 4) * 4;
-          const size_t head = static_cast<size_t>(pc.qrow) * a.Hq + pc.kvh * G + h;
-          float M = -INFINITY, den = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int s0 = 0; s0 < np; s0 += 4) {
-            float lv[4];
-            float4 x[4];
+        // the threads of an output item take every parts-th piece each; their
+        // first eight loads are in flight while the weights are computed
+        constexpr int kRow = D / 4;
+        constexpr int kFlight = 8;
+        const int items = G * kRow;
+        const int parts = max(1, NW * 32 / items);
+        float* wts = reinterpret_cast<float*>(ml);  // [G][kMaxParts]
+        auto load = [&](int item, int s0, float4 (&x)[kFlight]) {
+          const int it = item % items;
+          const float* po =
+              a.partial_o + (head0 + it / kRow) * a.num_splits * D + it % kRow * 4;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const size_t row = head * a.num_splits + min(s0 + k, np - 1);
-              lv[k] = s0 + k < np ? __ldcg(a.partial_lse + row) : -INFINITY;
-              x[k] = __ldcg(reinterpret_cast<const float4*>(a.partial_o + row * D + d0));
-              if (s0 + k >= np) x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            lse_merge4(M, den, acc, lv, x);
-          }
+          for (int k = 0; k < kFlight; ++k)
+            x[k] = __ldcg(reinterpret_cast<const float4*>(
+                po + static_cast<size_t>(min(s0 + k * parts, np - 1)) * D));
+        };
+        float4 x[kFlight];
+        if (static_cast<int>(threadIdx.x) < items * parts)
+          load(threadIdx.x, threadIdx.x / items, x);
+        if (warp < G) {
+          const float* lse = a.partial_lse + (head0 + warp) * a.num_splits;
+          const float v0 = lane < np ? __ldcg(lse + lane) : -INFINITY;
+          const float v1 = lane + 32 < np ? __ldcg(lse + lane + 32) : -INFINITY;
+          float M = fmaxf(v0, v1);
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+          if (M == -INFINITY) M = 0.f;
+          const float w0 = fast_exp2((v0 - M) * kLog2e), w1 = fast_exp2((v1 - M) * kLog2e);
+          float den = w0 + w1;
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
           const float inv = den == 0.f ? 0.f : 1.f / den;
-          *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + head * D + d0) =
-              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
-                         pack_bf16x2(acc.z * inv, acc.w * inv));
+          if (lane < np) wts[warp * kMaxParts + lane] = w0 * inv;
+          if (lane + 32 < np) wts[warp * kMaxParts + lane + 32] = w1 * inv;
+        }
+        __syncthreads();
+        auto store = [&](int it, const float4& acc) {
+          *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + (head0 + it / kRow) * D +
+                                    it % kRow * 4) =
+              make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+        };
+        for (int item = threadIdx.x; item < items * parts; item += NW * 32) {
+          const int part = item / items, it = item % items;
+          if (item >= NW * 32) load(item, part, x);
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int s0 = part; s0 < np; s0 += kFlight * parts) {
+            if (s0 != part) load(item, s0, x);
+#pragma unroll
+            for (int k = 0; k < kFlight; ++k) {
+              if (s0 + k * parts < np) {
+                const float w = wts[it / kRow * kMaxParts + s0 + k * parts];
+                acc.x = fmaf(w, x[k].x, acc.x);
+                acc.y = fmaf(w, x[k].y, acc.y);
+                acc.z = fmaf(w, x[k].z, acc.z);
+                acc.w = fmaf(w, x[k].w, acc.w);
+              }
+            }
+          }
+          if (parts > 1)
+            st[item] = acc;
+          else
+            store(it, acc);
+        }
+        if (parts > 1) {
+          __syncthreads();
+          for (int it = threadIdx.x; it < items; it += NW * 32) {
+            float4 acc = st[it];
+            for (int k = 1; k < parts; ++k) {
+              const float4 z = st[k * items + it];
+              acc.x += z.x;
+              acc.y += z.y;
+              acc.z += z.z;
+              acc.w += z.w;
+            }
+            store(it, acc);
+          }
         }
       }
     }
+    if (!have_next) break;
     __syncthreads();  // the states' shared memory is free again
-    pc = nx;
-    have = have_next;
+    if constexpr (LINE) pc = nx;
   }
   cp_async_wait<0>();
 }
 
-template <int D, int NW, int STAGES>
-cudaError_t launch_t(const Kv4DecodeArgs& a, int sms, cudaStream_t stream) {
+template <int D, int NW, int STAGES, int CTAS, bool CAP, bool LINE>
+cudaError_t launch_t(const Kv4DecodeArgs& a, int grid, cudaStream_t stream) {
   using S = Kv4Shape<D, NW, STAGES>;
-  auto kern = kv4_decode_kernel<D, NW, STAGES>;
-  static_assert(S::smem(8) <= 232448, "shared memory of one CTA");
-  const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), S::smem(8));
+  auto kern = kv4_decode_kernel<D, NW, STAGES, CTAS, CAP, LINE>;
+  static_assert(S::kSmem <= 232448 / CTAS - 1024, "shared memory of a CTA");
+  const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), S::kSmem);
   if (e != cudaSuccess) return e;
-  kern<<<sms, NW * 32, S::smem(a.base.Hq / a.base.Hkv), stream>>>(a);
+  kern<<<grid, NW * 32, S::kSmem, stream>>>(a);
   return cudaGetLastError();
+}
+
+template <int D, int NW, int STAGES, int CTAS>
+cudaError_t launch_d(Kv4DecodeArgs a, int sms, cudaStream_t stream) {
+  const int grid = sms * CTAS;
+  a.most_parts = grid / a.base.Hkv;
+  a.even_share = static_cast<float>(a.base.Hkv) / grid;
+  const bool line = static_cast<int64_t>(a.base.batch) * a.base.Hkv > grid || a.base.batch > kLens;
+  if (a.base.softcap > 0.f)
+    return line ? launch_t<D, NW, STAGES, CTAS, true, true>(a, grid, stream)
+                : launch_t<D, NW, STAGES, CTAS, true, false>(a, grid, stream);
+  return line ? launch_t<D, NW, STAGES, CTAS, false, true>(a, grid, stream)
+              : launch_t<D, NW, STAGES, CTAS, false, false>(a, grid, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, int head_dim, int sms, cudaStream_t stream) {
-  if (head_dim == 128) return launch_t<128, 16, 4>(a, sms, stream);
-  if (head_dim == 256) return launch_t<256, 8, 4>(a, sms, stream);
+  if (head_dim == 128) return launch_d<128, 16, 4, 1>(a, sms, stream);
+  if (head_dim == 256) return launch_d<256, 8, 4, 1>(a, sms, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -106,10 +106,6 @@ int check_decode_call(const void* q, const void* out, const pka_kv_pool* kv,
   return aligned16(out) ? PKA_OK : PKA_ERR_ALIGN;
 }
 
-bool splitk_line_fits(int32_t B, int32_t Hkv, int32_t max_blocks, int32_t window) {
-  return line_fits(B, Hkv, max_blocks, window);
-}
-
 int device_sm_count() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
