@@ -94,49 +94,77 @@ __device__ __forceinline__ uint32_t f32_to_e4m3(float x) {
   return r & 0xffu;
 }
 
-// Two fp32 -> two e2m1 codes (nearest, ties to even, saturating) in a byte,
-// `lo` in the low nibble.
-__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
+// Eight fp32 -> eight e2m1 codes (nearest, ties to even, saturating), the
+// first in the lowest nibble.
+__device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float (&q)[8]) {
   uint32_t r;
-  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\t"
-      "mov.b32 %0, {b, b, b, b};\n\t}"
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
-  return r & 0xffu;
+      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+  return r;
 }
 
-// A group of 16 values -> 8 code bytes and the scale byte.  s6 = 6 * pool
+// A group of 16 bf16 values -> 8 code bytes and the scale byte.  s6 = 6 * pool
 // scale, rounded to fp32.
-__device__ __forceinline__ uint2 quantise_group(const float (&x)[16], float pool_scale, float s6,
+__device__ __forceinline__ uint2 quantise_group(const uint4& in0, const uint4& in1,
+                                                float pool_scale, float s6,
                                                 uint32_t& scale_byte) {
-  float top = 0.f;
-  bool finite = true;
+  const uint32_t in[8] = {in0.x, in0.y, in0.z, in0.w, in1.x, in1.y, in1.z, in1.w};
+  // the largest magnitude, as bf16 bits (from 0x7f80 on: infinity or NaN)
+  uint32_t top2 = in[0] & 0x7fff7fffu;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float a = fabsf(x[i]);
-    finite = finite && (a <= 3.402823466e38f);
-    top = fmaxf(top, a);
-  }
-  if (!finite) {
+  for (int i = 1; i < 8; ++i) top2 = __vmaxu2(top2, in[i] & 0x7fff7fffu);
+  const uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+  if (top >= 0x7f80u) {
     scale_byte = 0x7fu;
     return make_uint2(0u, 0u);
   }
-  scale_byte = f32_to_e4m3(fminf(__fdiv_rn(top, s6), 448.f));
+  const float ftop = __uint_as_float(top << 16);
+  scale_byte = f32_to_e4m3(fminf(__fdiv_rn(ftop, s6), 448.f));
   float s, unused;
   f16x2_to_f32(e4m3x2_to_f16x2(static_cast<uint16_t>(scale_byte)), s, unused);
   const float step = __fmul_rn(s, pool_scale);
+  // x / step, rounded to nearest: with the correctly rounded reciprocal y and
+  // q = x y, the remainder x - q step is exact in one fma and q + remainder * y
+  // is the correctly rounded quotient (P. Markstein, "Computation of elementary
+  // functions on the IBM RISC System/6000 processor", 1990), as long as nothing
+  // leaves the normal range.  Steps near its ends, and groups that saturate by
+  // more than their rounding, take the division itself.
+  const float y = __frcp_rn(step);
+  const bool plain = step > 0x1p-60f && step < 0x1p60f && __fmul_rn(ftop, y) < 16.f;
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    w[h] = 0;
+    float q[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      // s = 0 (or s * pool scale below the smallest fp32): zeros with a sign
-      const float a = x[h * 8 + 2 * i], b = x[h * 8 + 2 * i + 1];
-      const float ya = step > 0.f ? __fdiv_rn(a, step) : copysignf(0.f, a);
-      const float yb = step > 0.f ? __fdiv_rn(b, step) : copysignf(0.f, b);
-      w[h] |= f32x2_to_e2m1x2(ya, yb) << (8 * i);
+      float v[2];
+      bf16x2_to_f32(in[h * 4 + i], v[0], v[1]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float q0 = __fmul_rn(v[j], y);
+        // (-0 stays -0)
+        q[2 * i + j] = copysignf(__fmaf_rn(__fmaf_rn(-q0, step, v[j]), y, q0), v[j]);
+      }
     }
+    if (!plain) {
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t word = (i >> 1) == 0 ? in[h * 4] : (i >> 1) == 1 ? in[h * 4 + 1]
+                              : (i >> 1) == 2 ? in[h * 4 + 2] : in[h * 4 + 3];
+        const float v = __uint_as_float((i & 1) ? word & 0xffff0000u : word << 16);
+        // s = 0 (or s * pool scale below the smallest fp32): signed zeros
+        const float d = step > 0.f ? __fdiv_rn(v, step) : copysignf(0.f, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q[k] = k == i ? d : q[k];
+      }
+    }
+    w[h] = f32x8_to_e2m1x8(q);
   }
   return make_uint2(w[0], w[1]);
 }

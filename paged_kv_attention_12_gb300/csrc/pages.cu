@@ -130,9 +130,19 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanWarps *
   const int hi = static_cast<int>(min(first + per_warp, static_cast<long long>(a.num_blocks)));
   if (threadIdx.x == 0) moves_total = 0;
 
+  // the first kKeep steps' counts stay in registers for the second pass
+  constexpr int kKeep = 8;
+  int ref[kKeep];
   int count = 0;
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) {
+    const int i = lo + 32 * k + lane;
+    ref[k] = i < hi ? a.refcounts[i] : 0;
+  }
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) count += __popc(__ballot_sync(0xffffffffu, ref[k] > 0));
 #pragma unroll 8
-  for (int base = lo; base < hi; base += 32) {
+  for (int base = lo + 32 * kKeep; base < hi; base += 32) {
     const int i = base + lane;
     count += __popc(__ballot_sync(0xffffffffu, i < hi && a.refcounts[i] > 0));
   }
@@ -161,27 +171,32 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanWarps *
   below += warp_total[warp];
 
   int movers = 0;
-  for (int base = lo; base < hi; base += 32) {
-    const int i = base + lane;
-    const int ref = i < hi ? a.refcounts[i] : 0;
-    const unsigned m = __ballot_sync(0xffffffffu, ref > 0);
-    const int r = below + __popc(m & ((1u << lane) - 1u));  // live ids below i
+  auto place = [&](int i, int r) {  // r: the refcount of id i, 0 past the end
+    const unsigned m = __ballot_sync(0xffffffffu, r > 0);
+    const int at = below + __popc(m & ((1u << lane) - 1u));  // live ids below i
     below += __popc(m);
     if (i < hi) {
-      if (ref > 0 && i < live) {
+      if (r > 0 && i < live) {
         a.remap[i] = i;
-        a.new_refcounts[i] = ref;
-      } else if (ref > 0) {
-        a.moves[2 + 2 * (live - 1 - r)] = i;
+        a.new_refcounts[i] = r;
+      } else if (r > 0) {
+        a.moves[2 + 2 * (live - 1 - at)] = i;
       } else {
         a.remap[i] = -1;
         if (i < live)
-          a.moves[3 + 2 * (i - r)] = i;
+          a.moves[3 + 2 * (i - at)] = i;
         else
           a.new_refcounts[i] = 0;
       }
     }
-    movers += __popc(__ballot_sync(0xffffffffu, ref > 0 && i >= live));
+    movers += __popc(__ballot_sync(0xffffffffu, r > 0 && i >= live));
+  };
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k)
+    if (lo + 32 * k < hi) place(lo + 32 * k + lane, ref[k]);
+  for (int base = lo + 32 * kKeep; base < hi; base += 32) {
+    const int i = base + lane;
+    place(i, i < hi ? a.refcounts[i] : 0);
   }
   if (lane == 0 && movers > 0) atomicAdd(cluster.map_shared_rank(&moves_total, 0), movers);
   cluster.sync();  // the lists and the count are complete

@@ -69,7 +69,7 @@ def test_append_bit_exact(D, hkv, T, wide):
     assert np.array_equal(pool.v.cpu().numpy(), want[1])
 
 
-@pytest.mark.parametrize("scale", [2.0 ** -9, 0.0123, 1e-30, 3e37])
+@pytest.mark.parametrize("scale", [2.0 ** -9, 0.0123, 1e-4, 1e-30, 3e37])
 def test_append_borders_and_special_values(scale):
     """Values on and next to every rounding border, zeros of both signs,
     subnormals, the largest values, infinities and NaN."""
