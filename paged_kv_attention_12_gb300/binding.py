@@ -377,10 +377,14 @@ def _dims(*shape) -> str:
     return "".join(f"[{x}]" for x in shape)
 
 
+def _fits(t, dtype, device, shape) -> bool:
+    """Whether t is a contiguous tensor of ``dtype`` and ``shape`` on ``device``."""
+    return t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()
+
+
 def _tensor(t, name: str, dtype, device, shape=None) -> None:
-    """A contiguous tensor of ``dtype`` on ``device``, of ``shape`` if given."""
-    if t.dtype is not dtype or t.device != device or not t.is_contiguous() or \
-            (shape is not None and t.shape != shape):
+    """Refuses what is no contiguous tensor of ``dtype`` on ``device`` (and ``shape``)."""
+    if not _fits(t, dtype, device, t.shape if shape is None else shape):
         _refuse(t, name, f"contiguous {dtype} {'' if shape is None else _dims(*shape)} on {device}")
 
 

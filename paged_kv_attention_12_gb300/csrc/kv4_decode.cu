@@ -48,6 +48,7 @@ constexpr int kMinPiece = 16;
 
 // A line piece's fixed cost, in tiles.
 constexpr int kLinePieceCost = 16;
+using LineIter = PieceIterT<kLinePieceCost>;
 
 constexpr float kGrow = 7.f;
 constexpr float kShift = 8.f;
@@ -96,17 +97,18 @@ struct Kv4Shape {
   static constexpr int kTile = UNITS * kUnitBytes;  // one block and head of K (or V)
   static constexpr int kRing = NW * STAGES * 2 * kTile;
   static constexpr int kLen = 2 * kLens * 4;
-  // the warps' (max, sum) per head, later the pieces' weights; the plan's
-  // piece; a flag
-  static constexpr int kMl = (NW * 8 * 8 > 8 * kMaxParts * 4 ? NW * 8 * 8 : 8 * kMaxParts * 4) +
-                             (sizeof(Piece) + 15) / 16 * 16 + 16;
+  // the warps' (max, sum) per head, later the pieces' weights
+  static constexpr int kMl = NW * 8 * 8 > 8 * kMaxParts * 4 ? NW * 8 * 8 : 8 * kMaxParts * 4;
+  // two pieces, the line's iterator, a flag
+  static constexpr int kPlan = (2 * sizeof(Piece) + sizeof(LineIter) + 4 + 15) / 16 * 16;
   static constexpr int kFrags = UNITS * 4 * 2 * 32; // float4 of a warp's O state
   static constexpr int kItems = (kFrags + NW * 32 - 1) / (NW * 32);
   // the warps' O states are merged kRound warps at a time
   static constexpr int kRounds = (D == 256 && NW > 8) ? 2 : 1;
   static constexpr int kRound = NW / kRounds;
   static_assert(NW % kRounds == 0, "equal rounds");
-  static constexpr int kSmem = kRing + kLen + kMl + kRound * kFrags * 16;
+  static constexpr int kQ = UNITS * 8 * 32 * 8;     // q as B fragments
+  static constexpr int kSmem = kRing + kLen + kMl + kPlan + kQ + kRound * kFrags * 16;
 };
 
 // The four A registers of K's k-step S (0..7) of a unit: words of row g and
@@ -134,36 +136,58 @@ __device__ __forceinline__ void v_step(float (&o)[4], uint32_t lo0, uint32_t hi0
                 p1);
 }
 
-// S^T of one tile for one warp.  Fragment roles (g = lane / 4, t = lane % 4):
+// S^T of NT tiles for one warp.  Fragment roles (g = lane / 4, t = lane % 4):
 // the rows are keys g and g + 8, the lane's channels 32 t .. 32 t + 31 of every
-// unit; S^T holds those keys of heads 2t and 2t + 1.
-template <int D>
-__device__ __forceinline__ void kv4_scores(const uint8_t* tile, const uint32_t (&bq)[D / 128][8][2],
-                                           float (&x)[4], int lane) {
-  float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+// unit; S^T holds those keys of heads 2t and 2t + 1.  bq: the CTA's q fragments
+// in shared memory, [UNITS][8 k-steps][32 lanes].
+template <int D, int NT>
+__device__ __forceinline__ void kv4_scores(const uint8_t* const (&tile)[NT], const uint2* bq,
+                                           float (&x)[NT][4], int lane) {
+  float s[NT][2][4];
+#pragma unroll
+  for (int k = 0; k < NT; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[k][0][i] = s[k][1][i] = 0.f;
 #pragma unroll
   for (int u = 0; u < D / kUnitChannels; ++u) {
-    const uint8_t* base = tile + u * kUnitBytes;
-    const uint4 r0 = *reinterpret_cast<const uint4*>(base + lane * 16);
-    const uint4 r1 = *reinterpret_cast<const uint4*>(base + 512 + lane * 16);
-    // scales of groups 2t and 2t + 1 of key g: byte 8 g + 2 t = 2 lane
-    const uint32_t c0 =
-        e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(base + kUnitCodes + lane * 2));
-    const uint32_t c1 =
-        e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(base + kUnitCodes + 64 + lane * 2));
-    const uint32_t s0[2] = {prmt(c0, c0, 0x1010u), prmt(c0, c0, 0x3232u)};
-    const uint32_t s1[2] = {prmt(c1, c1, 0x1010u), prmt(c1, c1, 0x3232u)};
-    k_step<0>(s[0], r0, r1, s0, s1, bq[u][0][0], bq[u][0][1]);
-    k_step<1>(s[1], r0, r1, s0, s1, bq[u][1][0], bq[u][1][1]);
-    k_step<2>(s[0], r0, r1, s0, s1, bq[u][2][0], bq[u][2][1]);
-    k_step<3>(s[1], r0, r1, s0, s1, bq[u][3][0], bq[u][3][1]);
-    k_step<4>(s[0], r0, r1, s0, s1, bq[u][4][0], bq[u][4][1]);
-    k_step<5>(s[1], r0, r1, s0, s1, bq[u][5][0], bq[u][5][1]);
-    k_step<6>(s[0], r0, r1, s0, s1, bq[u][6][0], bq[u][6][1]);
-    k_step<7>(s[1], r0, r1, s0, s1, bq[u][7][0], bq[u][7][1]);
+    uint4 r0[NT], r1[NT];
+    uint32_t s0[NT][2], s1[NT][2];
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+      const uint8_t* base = tile[k] + u * kUnitBytes;
+      r0[k] = *reinterpret_cast<const uint4*>(base + lane * 16);
+      r1[k] = *reinterpret_cast<const uint4*>(base + 512 + lane * 16);
+      // scales of groups 2t and 2t + 1 of key g: byte 8 g + 2 t = 2 lane
+      const uint32_t c0 =
+          e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(base + kUnitCodes + lane * 2));
+      const uint32_t c1 =
+          e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(base + kUnitCodes + 64 + lane * 2));
+      s0[k][0] = prmt(c0, c0, 0x1010u);
+      s0[k][1] = prmt(c0, c0, 0x3232u);
+      s1[k][0] = prmt(c1, c1, 0x1010u);
+      s1[k][1] = prmt(c1, c1, 0x3232u);
+    }
+    const uint2* q = bq + u * 8 * 32 + lane;
+#define PKA_KV4_STEP(K_)                                                                \
+  {                                                                                     \
+    const uint2 b = q[(K_) * 32];                                                       \
+    _Pragma("unroll") for (int k = 0; k < NT; ++k)                                      \
+        k_step<K_>(s[k][(K_) & 1], r0[k], r1[k], s0[k], s1[k], b.x, b.y);               \
+  }
+    PKA_KV4_STEP(0)
+    PKA_KV4_STEP(1)
+    PKA_KV4_STEP(2)
+    PKA_KV4_STEP(3)
+    PKA_KV4_STEP(4)
+    PKA_KV4_STEP(5)
+    PKA_KV4_STEP(6)
+    PKA_KV4_STEP(7)
+#undef PKA_KV4_STEP
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = s[0][i] + s[1][i];
+  for (int k = 0; k < NT; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[k][i] = s[k][0][i] + s[k][1][i];
 }
 
 // O^T += V^T P^T of one tile.  The lane holds group g of every unit for keys
@@ -212,16 +236,15 @@ __device__ __forceinline__ void kv4_values(const uint8_t* tile, float (&o)[D / 1
 // tile holds keys outside [t_lo, pos].
 template <int D, int NT, bool EDGE, bool CAP>
 __device__ __forceinline__ void kv4_tiles(const uint8_t* const (&tile)[NT],
-                                          const uint32_t (&bq)[D / 128][8][2],
-                                          float (&o)[D / 128][8][4], float (&m)[2], float (&l)[2],
+                                          const uint2* bq, float (&o)[D / 128][8][4],
+                                          float (&m)[2], float (&l)[2],
                                           float f0, float f1, float softcap, int tok0, int t_lo,
                                           int pos, int lane) {
   constexpr int UNITS = D / kUnitChannels;
   static_assert(!EDGE || NT == 1, "an edge tile goes alone");
   const int g = lane >> 2, t = lane & 3;
   float x[NT][4];
-#pragma unroll
-  for (int k = 0; k < NT; ++k) kv4_scores<D>(tile[k], bq, x[k], lane);
+  kv4_scores<D, NT>(tile, bq, x, lane);
   uint32_t keep0 = 0xffffu, keep1 = 0xffffu;
   bool ok_lo = true, ok_hi = true;
   if constexpr (EDGE) {
@@ -380,14 +403,19 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
   int* slen = reinterpret_cast<int*>(smem + S::kRing);
   float* nbf = reinterpret_cast<float*>(slen + kLens);
   float2* ml = reinterpret_cast<float2*>(smem + S::kRing + S::kLen);  // [NW][8]
-  Piece* plan = reinterpret_cast<Piece*>(smem + S::kRing + S::kLen + S::kMl - 16 - sizeof(Piece));
-  volatile int* flag = reinterpret_cast<int*>(smem + S::kRing + S::kLen + S::kMl - 16);
-  float4* st = reinterpret_cast<float4*>(smem + S::kRing + S::kLen + S::kMl);  // [kRound][kFrags]
+  Piece* plan = reinterpret_cast<Piece*>(smem + S::kRing + S::kLen + S::kMl);  // [2]
+  LineIter* line = reinterpret_cast<LineIter*>(plan + 2);
+  volatile int* flag = reinterpret_cast<int*>(line + 1);
+  uint2* bq = reinterpret_cast<uint2*>(smem + S::kRing + S::kLen + S::kMl + S::kPlan);  // [UNITS][8][32]
+  float4* st = reinterpret_cast<float4*>(smem + S::kRing + S::kLen + S::kMl + S::kPlan +
+                                         S::kQ);  // [kRound][kFrags]
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * STAGES * 2 * S::kTile;
   const uint32_t ring_addr = smem_u32(ring);
 
+  launch_dependents();
+  wait_predecessor();
   for (int b = threadIdx.x; b < kLens; b += NW * 32) {
     const int len = b < a.batch ? req_len_of(a, 0, 0, a.seq_lens[b]) : 0;
     slen[b] = len;
@@ -395,25 +423,36 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
   }
   __syncthreads();
 
-  PieceIterT<kLinePieceCost> iter;
-  Piece pc;
-  bool have;
-  if constexpr (LINE) {
-    iter.init(a, slen, lane, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
-    have = iter.next(pc, true);
-  } else {
-    if (warp == 0) {
+  // the CTA's piece, worked out by warp 0 (fill_from: whether there is one);
+  // with LINE thread 0 walks the line, one piece ahead in the other slot
+  auto next_piece = [&](Piece* to) {
+    LineIter it = *line;
+    Piece p{};
+    const bool any = it.next(p, true);
+    p.fill_from = any;
+    *to = p;
+    *line = it;
+  };
+  if (warp == 0) {
+    if constexpr (LINE) {
+      LineIter it;
+      it.init(a, slen, lane, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
+      if (lane == 0) {
+        *line = it;
+        next_piece(plan);
+      }
+    } else {
       Piece p;
       const bool any = theta_piece(ka, slen, nbf, lane, static_cast<int>(blockIdx.x), p);
       if (lane == 0) {
-        p.fill_from = any;  // (a field of the line's pieces)
+        p.fill_from = any;
         *plan = p;
       }
     }
-    __syncthreads();
-    pc = *plan;
-    have = pc.fill_from != 0;
   }
+  __syncthreads();
+  Piece pc = *plan;
+  bool have = pc.fill_from != 0;
   const float inv_cap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
   const float lscale = a.scale * ka.k_scale * (a.softcap > 0.f ? inv_cap : kLog2e);
 
@@ -462,45 +501,45 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
       cp_async_commit();
     }
   };
-  if (have) prologue(pc);
+  if (!have) return;
+  prologue(pc);
+  int cur = 0;
 
-  while (have) {
-    // ---- q of head g as B fragments in f16, scaled by a power of two
-    uint32_t bq[UNITS][8][2];
+  while (true) {
+    // ---- q of head g as B fragments in f16, scaled by a power of two: every
+    // warp finds the head's largest magnitude and writes its share for the CTA
     float fq;  // the logit factor of head g
     {
       const uint16_t* qp =
           a.q + (static_cast<size_t>(pc.qrow) * a.Hq + pc.kvh * G + (g < G ? g : 0)) * D + t * 32;
-      uint4 raw[UNITS][4];
-      uint32_t top = 0;  // largest magnitude, as bf16 bits
+      uint4 raw[UNITS * 4];
+      uint32_t top2 = 0;
 #pragma unroll
-      for (int u = 0; u < UNITS; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          raw[u][i] = (g < G) ? __ldg(reinterpret_cast<const uint4*>(qp + u * kUnitChannels) + i)
-                              : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t w[4] = {raw[u][i].x, raw[u][i].y, raw[u][i].z, raw[u][i].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-        }
+      for (int i = 0; i < UNITS * 4; ++i) {
+        raw[i] = (g < G) ? __ldg(reinterpret_cast<const uint4*>(
+                               qp + (i >> 2) * kUnitChannels + (i & 3) * 8))
+                         : make_uint4(0u, 0u, 0u, 0u);
+        top2 = __vmaxu2(__vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu),
+                        __vmaxu2(__vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu), top2));
+      }
+      uint32_t top = max(top2 & 0xffffu, top2 >> 16);  // as bf16 bits
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int e = min(max(254 - static_cast<int>(top >> 7), 1), 253);
       const float down = __uint_as_float(static_cast<uint32_t>(e) << 23);
       fq = lscale * __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
 #pragma unroll
-      for (int u = 0; u < UNITS; ++u)
+      for (int i = 0; i < UNITS * 4; ++i) {
+        if (i % NW != warp) continue;
+        float f[8];
+        unpack8(raw[i], f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float f[8];
-          unpack8(raw[u][i], f);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            bq[u][i * 2 + k][0] = pack_f16x2(f[k * 4] * down, f[k * 4 + 1] * down);
-            bq[u][i * 2 + k][1] = pack_f16x2(f[k * 4 + 2] * down, f[k * 4 + 3] * down);
-          }
-        }
+        for (int k = 0; k < 2; ++k)
+          bq[(i * 2 + k) * 32 + lane] =
+              make_uint2(pack_f16x2(f[k * 4] * down, f[k * 4 + 1] * down),
+                         pack_f16x2(f[k * 4 + 2] * down, f[k * 4 + 3] * down));
+      }
+      __syncthreads();
     }
     const float f0 = __shfl_sync(0xffffffffu, fq, 8 * t);
     const float f1 = __shfl_sync(0xffffffffu, fq, 8 * t + 4);
@@ -551,13 +590,9 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
       }
     }
 
-    Piece nx;
-    bool have_next = false;
     if constexpr (LINE) {
-      have_next = iter.next(nx, true);
-      if (have_next) prologue(nx);
+      if (threadIdx.x == 0) next_piece(plan + (cur ^ 1));
     }
-
     // ---- the warps' states merged in warp order: (max, sum) first, from which
     // every warp takes the factor of its own O, then the sum of the scaled O
     // states through shared memory (a warp without tiles holds zeros)
@@ -570,7 +605,14 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
       ml[warp * 8 + 2 * t + 1] = make_float2(m[1], l[1]);
     }
     __syncthreads();
-    if constexpr (!LINE) pc = *plan;  // not kept in registers over the loop
+    bool have_next = false;
+    if constexpr (LINE) {
+      // the next piece's first tiles, before this piece is merged
+      const Piece nx = plan[cur ^ 1];
+      have_next = nx.fill_from != 0;
+      if (have_next) prologue(nx);
+    }
+    pc = plan[cur];  // not kept in registers over the loop
     const bool split = pc.npieces > 1;
     const size_t head0 = static_cast<size_t>(pc.qrow) * a.Hq + pc.kvh * G;
     const int slot = min(pc.slot, a.num_splits - 1);
@@ -750,7 +792,8 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
     }
     if (!have_next) break;
     __syncthreads();  // the states' shared memory is free again
-    if constexpr (LINE) pc = nx;
+    cur ^= 1;
+    pc = plan[cur];
   }
   cp_async_wait<0>();
 }
@@ -762,8 +805,7 @@ cudaError_t launch_t(const Kv4DecodeArgs& a, int grid, cudaStream_t stream) {
   static_assert(S::kSmem <= 232448 / CTAS - 1024, "shared memory of a CTA");
   const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), S::kSmem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, NW * 32, S::kSmem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(kern, grid, NW * 32, S::kSmem, stream, a);
 }
 
 template <int D, int NW, int STAGES, int CTAS>

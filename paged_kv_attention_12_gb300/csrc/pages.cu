@@ -107,31 +107,45 @@ __global__ void __launch_bounds__(256) ref_blocks_kernel(const RefArgs a) {
 // hole's is id - rank(id), rank(id) the live ids below it: one prefix count
 // gives both.
 //
-// One cluster of kPlanCtas CTAs: the ids are cut into contiguous ranges, one
-// per warp; each warp counts its live ids with ballots, the CTAs exchange
-// their totals through distributed shared memory, and a second pass over the
-// range (in L1 by then) writes the lists.  Every id is read and written by
-// its own warp only until the last phase, so new_refcounts may be refcounts.
-constexpr int kPlanCtas = 8;
+// One cluster of CTAS CTAs: the ids are cut into contiguous ranges, one per
+// warp; each warp counts its live ids with ballots, the CTAs exchange their
+// totals through distributed shared memory, and a second pass over the range
+// (the first kKeep steps of it in registers) writes the lists.  Every id is
+// read and written by its own warp only until the last phase, so
+// new_refcounts may be refcounts.  One CTA does without the cluster's barriers
+// and is taken while its registers hold all the ids (PLAN_US).
 constexpr int kPlanWarps = 32;
+constexpr int kKeep = 8;
+constexpr int kPlanOne = kPlanWarps * 32 * kKeep;  // ids one CTA keeps in registers
 
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanWarps * 32)
-    compact_plan_kernel(const PlanArgs a) {
-  __shared__ int cta_total[kPlanCtas];  // every CTA's live ids (written by each CTA everywhere)
+template <int CTAS>
+__global__ void __launch_bounds__(kPlanWarps * 32) compact_plan_kernel(const PlanArgs a) {
+  __shared__ int cta_total[CTAS];  // every CTA's live ids (written by each CTA everywhere)
   __shared__ int warp_total[kPlanWarps];
-  __shared__ int moves_total;           // CTA 0's is the cluster's
+  __shared__ int moves_total;      // CTA 0's is the cluster's
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = static_cast<int>(cluster.block_rank());
+  auto sync = [&]() {
+    if constexpr (CTAS > 1)
+      cluster.sync();
+    else
+      __syncthreads();
+  };
+  auto of = [&](int* p, int rank) {
+    if constexpr (CTAS > 1)
+      return cluster.map_shared_rank(p, rank);
+    else
+      return p;
+  };
+  const int rank = CTAS > 1 ? static_cast<int>(cluster.block_rank()) : 0;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int per_warp =
-      ((a.num_blocks + kPlanCtas * kPlanWarps - 1) / (kPlanCtas * kPlanWarps) + 31) / 32 * 32;
+      ((a.num_blocks + CTAS * kPlanWarps - 1) / (CTAS * kPlanWarps) + 31) / 32 * 32;
   const long long first = static_cast<long long>(rank * kPlanWarps + warp) * per_warp;
   const int lo = static_cast<int>(min(first, static_cast<long long>(a.num_blocks)));
   const int hi = static_cast<int>(min(first + per_warp, static_cast<long long>(a.num_blocks)));
   if (threadIdx.x == 0) moves_total = 0;
 
   // the first kKeep steps' counts stay in registers for the second pass
-  constexpr int kKeep = 8;
   int ref[kKeep];
   int count = 0;
 #pragma unroll
@@ -159,12 +173,12 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanWarps *
     warp_total[lane] = incl - v;
     const int all = __shfl_sync(0xffffffffu, incl, 31);
     // lane r stores this CTA's total into CTA r's array
-    if (lane < kPlanCtas) *cluster.map_shared_rank(&cta_total[rank], lane) = all;
+    if (lane < CTAS) *of(&cta_total[rank], lane) = all;
   }
-  cluster.sync();
+  sync();
   int live = 0, below = 0;
 #pragma unroll
-  for (int r = 0; r < kPlanCtas; ++r) {
+  for (int r = 0; r < CTAS; ++r) {
     if (r < rank) below += cta_total[r];
     live += cta_total[r];
   }
@@ -198,28 +212,29 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanWarps *
     const int i = base + lane;
     place(i, i < hi ? a.refcounts[i] : 0);
   }
-  if (lane == 0 && movers > 0) atomicAdd(cluster.map_shared_rank(&moves_total, 0), movers);
-  cluster.sync();  // the lists and the count are complete
-  const int n = *cluster.map_shared_rank(&moves_total, 0);
+  if (lane == 0 && movers > 0) atomicAdd(of(&moves_total, 0), movers);
+  sync();  // the lists and the count are complete
+  const int n = *of(&moves_total, 0);
   const int tid = rank * kPlanWarps * 32 + threadIdx.x;
-  for (int j = tid; j < n; j += kPlanCtas * kPlanWarps * 32) {
+  for (int j = tid; j < n; j += CTAS * kPlanWarps * 32) {
     const int src = a.moves[2 + 2 * j], dst = a.moves[3 + 2 * j];
     a.remap[src] = dst;
     a.new_refcounts[dst] = a.refcounts[src];
     a.new_refcounts[src] = 0;
   }
-  for (int i = 2 + 2 * n + tid; i < 2 + a.num_blocks; i += kPlanCtas * kPlanWarps * 32)
+  for (int i = 2 + 2 * n + tid; i < 2 + a.num_blocks; i += CTAS * kPlanWarps * 32)
     a.moves[i] = -1;
   if (tid == 0) {
     a.moves[0] = n;
     a.moves[1] = live;
   }
-  cluster.sync();  // CTA 0's shared memory stays until every CTA has read the count
+  if constexpr (CTAS > 1)
+    cluster.sync();  // CTA 0's shared memory stays until every CTA has read the count
 }
 
 int copy_grid(long long warps, int sm_count) {
   const long long want = (warps + 7) / 8;
-  const long long cap = static_cast<long long>(sm_count > 0 ? sm_count : 1) * 8;
+  const long long cap = static_cast<long long>(sm_count > 0 ? sm_count : 1) * 32;
   return static_cast<int>(want < 1 ? 1 : (want < cap ? want : cap));
 }
 
@@ -244,8 +259,22 @@ cudaError_t launch_ref_blocks(const RefArgs& a, int sm_count, cudaStream_t strea
 }
 
 cudaError_t launch_compact_plan(const PlanArgs& a, cudaStream_t stream) {
-  compact_plan_kernel<<<kPlanCtas, kPlanWarps * 32, 0, stream>>>(a);
-  return cudaGetLastError();
+  if (a.num_blocks <= kPlanOne) {
+    compact_plan_kernel<1><<<1, kPlanWarps * 32, 0, stream>>>(a);
+    return cudaGetLastError();
+  }
+  constexpr int kCtas = 8;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kCtas);
+  cfg.blockDim = dim3(kPlanWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = kCtas;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, compact_plan_kernel<kCtas>, a);
 }
 
 }  // namespace pka
