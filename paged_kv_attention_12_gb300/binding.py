@@ -357,9 +357,9 @@ def paged_kv_append_rope(q, k_new, v_new, k_pool, v_pool, slot_mapping, position
     rd = d if rotary_dim is None else int(rotary_dim)
     st = lib().paged_kv_append_rope(
         _ptr(q), k_new.data_ptr(), v_new.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), nb,
-        q.shape[1] if q is not None else 0, hkv, bs, d, slot_mapping.data_ptr(),
-        _ptr(positions), slot_mapping.shape[0], _ptr(q_norm_weight), _ptr(k_norm_weight),
-        1 if v_norm else 0, float(eps), float(rope_theta), rd, _ptr(err), _stream(stream))
+        q.shape[1] if q is not None else 0, hkv, bs, d, slot_mapping.data_ptr(), _ptr(positions),
+        slot_mapping.shape[0], _ptr(q_norm_weight), _ptr(k_norm_weight), 1 if v_norm else 0,
+        float(eps), float(rope_theta), rd, _ptr(err), _stream(stream))
     _check("paged_kv_append_rope", st)
 
 
@@ -367,7 +367,7 @@ def paged_kv_append_rope(q, k_new, v_new, k_pool, v_pool, slot_mapping, position
 # These check their tensors (device, type, layout, shape) before the call and
 # raise ValueError; they run on the tensors' device, on its current stream
 # unless one is given.  A decode step makes these calls for every layer, so the
-# checks build no text unless they fail.
+# checks are plain comparisons, and build no text unless one fails.
 def _refuse(t, name: str, want: str):
     raise ValueError(f"{name}: {want} is wanted, got {t.dtype} {list(t.shape)} with strides "
                      f"{t.stride()} on {t.device}")
@@ -377,15 +377,11 @@ def _dims(*shape) -> str:
     return "".join(f"[{x}]" for x in shape)
 
 
-def _fits(t, dtype, device, shape) -> bool:
-    """Whether t is a contiguous tensor of ``dtype`` and ``shape`` on ``device``."""
-    return t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()
-
-
-def _tensor(t, name: str, dtype, device, shape=None) -> None:
-    """Refuses what is no contiguous tensor of ``dtype`` on ``device`` (and ``shape``)."""
-    if not _fits(t, dtype, device, t.shape if shape is None else shape):
-        _refuse(t, name, f"contiguous {dtype} {'' if shape is None else _dims(*shape)} on {device}")
+def _tensor(t, name: str, dtype, device, shape) -> None:
+    """Refuses what is no contiguous tensor of ``dtype`` and ``shape`` on ``device``."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
+    _refuse(t, name, f"contiguous {dtype} {_dims(*shape)} on {device}")
 
 
 def _cuda_device(t, name: str):
@@ -394,31 +390,22 @@ def _cuda_device(t, name: str):
     return t.device
 
 
-def _err(err, device) -> Optional[int]:
+def _err(err, device) -> int:
     import torch
-    if err is None:
-        return None
-    _tensor(err, "err", torch.int32, device)
-    if err.numel() < 1:
-        _refuse(err, "err", "at least one int32")
+    _tensor(err, "err", torch.int32, device, (max(1, err.numel()),))
     return err.data_ptr()
 
 
-def _run_on(device, stream, name: str, *args) -> None:
-    """Calls the library function ``name`` with ``args`` and the stream, with
-    ``device`` current."""
+def _elsewhere(device) -> bool:
+    """Whether ``device`` is not the current one (the library launches there)."""
     import torch
-    fn = getattr(lib(), name)
-    idx = device.index
-    if idx == torch._C._cuda_getDevice():
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(idx) if stream is None
-                else stream.cuda_stream)
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(idx) if stream is None
-                    else stream.cuda_stream)
-    if st != PKA_OK:
-        raise PagedAttnError(name, st)
+    return device.index != torch._C._cuda_getDevice()
+
+
+def _raw_stream(device, stream):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None \
+        else stream.cuda_stream
 
 
 class Kv4Pool:
@@ -477,8 +464,14 @@ def paged_kv4_append(k_new, v_new, pool: Kv4Pool, slot_mapping, err=None, stream
     dev, T = pool.device, slot_mapping.shape[0]
     ks, vs = _token_rows(k_new, "k_new", T, pool), _token_rows(v_new, "v_new", T, pool)
     _tensor(slot_mapping, "slot_mapping", torch.int32, dev, (T,))
-    _run_on(dev, stream, "paged_kv4_append", k_new.data_ptr(), v_new.data_ptr(), ks, vs, pool._ref,
-            slot_mapping.data_ptr(), T, _err(err, dev))
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return paged_kv4_append(k_new, v_new, pool, slot_mapping, err, stream)
+    st = lib().paged_kv4_append(
+        k_new.data_ptr(), v_new.data_ptr(), ks, vs, pool._ref, slot_mapping.data_ptr(), T, None if
+        err is None else _err(err, dev), _raw_stream(dev, stream))
+    if st != PKA_OK:
+        raise PagedAttnError("paged_kv4_append", st)
 
 
 def paged_kv4_expand(pool: Kv4Pool, k_pool, v_pool, src_blocks, dst_blocks=None, err=None,
@@ -491,12 +484,18 @@ def paged_kv4_expand(pool: Kv4Pool, k_pool, v_pool, src_blocks, dst_blocks=None,
     shape = (k_pool.shape[0], pool.num_kv_heads, 16, pool.head_dim)
     _tensor(k_pool, "k_pool", torch.bfloat16, dev, shape)
     _tensor(v_pool, "v_pool", torch.bfloat16, dev, shape)
-    _tensor(src_blocks, "src_blocks", torch.int32, dev)
+    _tensor(src_blocks, "src_blocks", torch.int32, dev, src_blocks.shape)
     if dst_blocks is not None:
         _tensor(dst_blocks, "dst_blocks", torch.int32, dev, src_blocks.shape)
     dst = PkaKvPool(k_pool.data_ptr(), v_pool.data_ptr(), *shape)
-    _run_on(dev, stream, "paged_kv4_expand", pool._ref, ctypes.byref(dst), src_blocks.data_ptr(),
-            _ptr(dst_blocks), src_blocks.numel(), _err(err, dev))
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return paged_kv4_expand(pool, k_pool, v_pool, src_blocks, dst_blocks, err, stream)
+    st = lib().paged_kv4_expand(
+        pool._ref, ctypes.byref(dst), src_blocks.data_ptr(), _ptr(dst_blocks), src_blocks.numel(),
+        None if err is None else _err(err, dev), _raw_stream(dev, stream))
+    if st != PKA_OK:
+        raise PagedAttnError("paged_kv4_expand", st)
 
 
 def paged_kv4_decode_attn_ws_bytes(B, Hq, Hkv, D, max_seq_len, window=0) -> int:
@@ -512,16 +511,32 @@ def paged_kv4_decode_attn_ws(q, out, pool: Kv4Pool, block_tables, seq_lens, max_
     import torch
     dev = pool.device
     shape = B, Hq, _ = (seq_lens.shape[0], q.shape[1], pool.head_dim)
-    _tensor(q, "q", torch.bfloat16, dev, shape)
-    _tensor(out, "out", torch.bfloat16, dev, shape)
     width = block_tables.shape[-1]
-    _tensor(block_tables, "block_tables", torch.int32, dev, (B, width))
-    _tensor(seq_lens, "seq_lens", torch.int32, dev, (B,))
-    _tensor(workspace, "workspace", workspace.dtype, dev)
-    par = PkaAttnParams(scale, softcap, window, _err(err, dev))
-    _run_on(dev, stream, "paged_kv4_decode_attn_ws", q.data_ptr(), out.data_ptr(), pool._ref,
-            block_tables.data_ptr(), width, seq_lens.data_ptr(), B, Hq, int(max_seq_len),
-            ctypes.byref(par), workspace.data_ptr(), workspace.nbytes)
+    if not (q.dtype is torch.bfloat16 and out.dtype is torch.bfloat16 and
+            block_tables.dtype is torch.int32 and seq_lens.dtype is torch.int32 and
+            q.shape == shape and out.shape == shape and block_tables.shape == (B, width) and
+            seq_lens.dim() == 1 and
+            dev == q.device == out.device == block_tables.device == seq_lens.device ==
+            workspace.device and
+            q.is_contiguous() and out.is_contiguous() and block_tables.is_contiguous() and
+            seq_lens.is_contiguous() and workspace.is_contiguous()):
+        _tensor(q, "q", torch.bfloat16, dev, shape)
+        _tensor(out, "out", torch.bfloat16, dev, shape)
+        _tensor(block_tables, "block_tables", torch.int32, dev, (B, width))
+        _tensor(seq_lens, "seq_lens", torch.int32, dev, (B,))
+        _tensor(workspace, "workspace", workspace.dtype, dev, workspace.shape)
+    par = PkaAttnParams(scale, softcap, window, None if err is None else _err(err, dev))
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return paged_kv4_decode_attn_ws(
+                q, out, pool, block_tables, seq_lens, max_seq_len, workspace, scale=scale,
+                softcap=softcap, window=window, err=err, stream=stream)
+    st = lib().paged_kv4_decode_attn_ws(
+        q.data_ptr(), out.data_ptr(), pool._ref, block_tables.data_ptr(), width,
+        seq_lens.data_ptr(), B, Hq, int(max_seq_len), ctypes.byref(par), workspace.data_ptr(),
+        workspace.nbytes, _raw_stream(dev, stream))
+    if st != PKA_OK:
+        raise PagedAttnError("paged_kv4_decode_attn_ws", st)
 
 
 def paged_kv_ref_blocks(block_tables, seq_lens, refcounts, delta: int, err=None, stream=None):
@@ -534,8 +549,14 @@ def paged_kv_ref_blocks(block_tables, seq_lens, refcounts, delta: int, err=None,
     _tensor(seq_lens, "seq_lens", torch.int32, dev, (B,))
     n = refcounts.shape[0]
     _tensor(refcounts, "refcounts", torch.int32, dev, (n,))
-    _run_on(dev, stream, "paged_kv_ref_blocks", block_tables.data_ptr(), width,
-            seq_lens.data_ptr(), B, n, int(delta), refcounts.data_ptr(), _err(err, dev))
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return paged_kv_ref_blocks(block_tables, seq_lens, refcounts, delta, err, stream)
+    st = lib().paged_kv_ref_blocks(
+        block_tables.data_ptr(), width, seq_lens.data_ptr(), B, n, int(delta), refcounts.data_ptr(),
+        None if err is None else _err(err, dev), _raw_stream(dev, stream))
+    if st != PKA_OK:
+        raise PagedAttnError("paged_kv_ref_blocks", st)
 
 
 def _pool_list(pools):
@@ -558,8 +579,14 @@ def paged_kv_copy_blocks(pools, src, dst, err=None, stream=None):
     pairs = src.shape[0]
     _tensor(src, "src", torch.int32, dev, (pairs,))
     _tensor(dst, "dst", torch.int32, dev, (pairs,))
-    _run_on(dev, stream, "paged_kv_copy_blocks", ptrs, len(ptrs), n, nbytes, src.data_ptr(),
-            dst.data_ptr(), pairs, _err(err, dev))
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return paged_kv_copy_blocks(pools, src, dst, err, stream)
+    st = lib().paged_kv_copy_blocks(
+        ptrs, len(ptrs), n, nbytes, src.data_ptr(), dst.data_ptr(), pairs, None if err is None else
+        _err(err, dev), _raw_stream(dev, stream))
+    if st != PKA_OK:
+        raise PagedAttnError("paged_kv_copy_blocks", st)
 
 
 def paged_kv_compact(pools, refcounts, block_tables, seq_lens, new_refcounts, new_tables, remap,
@@ -578,9 +605,17 @@ def paged_kv_compact(pools, refcounts, block_tables, seq_lens, new_refcounts, ne
     _tensor(block_tables, "block_tables", i32, dev, (B, width))
     _tensor(new_tables, "new_tables", i32, dev, (B, width))
     _tensor(seq_lens, "seq_lens", i32, dev, (B,))
-    _run_on(dev, stream, "paged_kv_compact", ptrs, len(ptrs), n, nbytes, refcounts.data_ptr(),
-            new_refcounts.data_ptr(), block_tables.data_ptr(), new_tables.data_ptr(), width,
-            seq_lens.data_ptr(), B, remap.data_ptr(), moves.data_ptr(), _err(err, dev))
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return paged_kv_compact(pools, refcounts, block_tables, seq_lens, new_refcounts,
+                                    new_tables, remap, moves, err, stream)
+    st = lib().paged_kv_compact(
+        ptrs, len(ptrs), n, nbytes, refcounts.data_ptr(), new_refcounts.data_ptr(),
+        block_tables.data_ptr(), new_tables.data_ptr(), width, seq_lens.data_ptr(), B,
+        remap.data_ptr(), moves.data_ptr(), None if err is None else _err(err, dev),
+        _raw_stream(dev, stream))
+    if st != PKA_OK:
+        raise PagedAttnError("paged_kv_compact", st)
 
 
 # ------------------------------------------------------------ batch runners

@@ -176,6 +176,8 @@ struct Kv4DecodeArgs {
   float k_scale, v_scale;
   int32_t most_parts;  // set by the launcher: CTAs / Hkv
   float even_share;    // and Hkv / CTAs
+  int32_t max_tiles;   // 16-key tiles of the longest segment max_seq_len allows
+  int32_t whole;       // set by the launcher: no segment is cut
 };
 
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, int head_dim, int sms, cudaStream_t stream);

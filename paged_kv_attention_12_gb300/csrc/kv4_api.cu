@@ -47,10 +47,6 @@ int kv4_layout(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_seq_le
   return PKA_OK;
 }
 
-// A batch whose segments fit one per CTA and are at most this many work units
-// longer than the split's chunk streams unsplit.
-constexpr int32_t kKv4DirectSlack = 24;
-
 int check_pools(void* const* pools, int32_t num_pools, int32_t num_blocks, int64_t block_bytes) {
   if (num_pools < 0 || num_blocks <= 0 || block_bytes <= 0) return PKA_ERR_SHAPE;
   if (block_bytes % 16 != 0 || block_bytes > (int64_t(1) << 40)) return PKA_ERR_SHAPE;
@@ -218,7 +214,6 @@ int paged_kv4_decode_attn_ws(const void* q, void* out, const pka_kv4_pool* kv,
   a.base.window = params->window;
   a.base.num_splits = L.S;
   a.base.split_blocks = L.C;
-  a.base.direct_slack = kKv4DirectSlack;
   a.base.seg_counters = reinterpret_cast<int32_t*>(ws);
   a.base.partial_o = reinterpret_cast<float*>(ws + L.cnt_bytes);
   a.base.partial_lse = reinterpret_cast<float*>(ws + L.cnt_bytes + L.o_bytes);
@@ -226,6 +221,8 @@ int paged_kv4_decode_attn_ws(const void* q, void* out, const pka_kv4_pool* kv,
   a.v4 = static_cast<const uint8_t*>(kv->v);
   a.k_scale = kv->k_scale;
   a.v_scale = kv->v_scale;
+  a.max_tiles = (max_seq_len + 15) / 16;
+  if (params->window > 0) a.max_tiles = std::min(a.max_tiles, (params->window - 1) / 16 + 2);
   const int sms = pka::device_sm_count();
   if (sms <= 0) return PKA_ERR_CUDA;
   const cudaError_t e =

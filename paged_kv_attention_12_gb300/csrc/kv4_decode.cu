@@ -43,7 +43,13 @@ namespace pka {
 
 namespace {
 
-// The shortest piece worth a merge, in tiles.
+// When no segment can be longer than this many tiles per warp, none is cut: a
+// merge through global memory costs about 3.5 us.  (B = 8, Hkv = 2, G = 4, us
+// a call in a stream of them, whole / cut: D = 128, 640 tokens 6.8 / 9.1, 1280
+// tokens 8.8 / 9.4, 1600 tokens 10.4 / 9.3; D = 256, 640 tokens 8.7 / 9.4, 800
+// tokens 10.3 / 9.4.)
+constexpr int kWholePerWarp = 5;
+// Else the shortest piece, in tiles.
 constexpr int kMinPiece = 16;
 
 // A line piece's fixed cost, in tiles.
@@ -433,7 +439,25 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
     *to = p;
     *line = it;
   };
-  if (warp == 0) {
+  if (!LINE && ka.whole) {
+    // no segment is long enough to be cut: piece c is segment c
+    if (threadIdx.x == 0) {
+      Piece p{};
+      p.fill_from = static_cast<int>(blockIdx.x) < a.batch * a.Hkv;
+      if (p.fill_from != 0) {
+        p.b = static_cast<int>(blockIdx.x) / a.Hkv;
+        p.kvh = static_cast<int>(blockIdx.x) - p.b * a.Hkv;
+        const ReqGeo geo = geo_of_len(a, slen[p.b]);
+        p.j0 = geo.jlo;
+        p.ntiles = geo.nb;
+        p.t_lo = geo.t_lo;
+        p.pos = geo.pos;
+        p.qrow = p.b;
+        p.npieces = 1;
+      }
+      *plan = p;
+    }
+  } else if (warp == 0) {
     if constexpr (LINE) {
       LineIter it;
       it.init(a, slen, lane, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
@@ -813,6 +837,7 @@ cudaError_t launch_d(Kv4DecodeArgs a, int sms, cudaStream_t stream) {
   const int grid = sms * CTAS;
   a.most_parts = grid / a.base.Hkv;
   a.even_share = static_cast<float>(a.base.Hkv) / grid;
+  a.whole = a.max_tiles <= kWholePerWarp * NW;
   const bool line = static_cast<int64_t>(a.base.batch) * a.base.Hkv > grid || a.base.batch > kLens;
   if (a.base.softcap > 0.f)
     return line ? launch_t<D, NW, STAGES, CTAS, true, true>(a, grid, stream)
