@@ -447,9 +447,14 @@ int paged_kv4_expand(const pka_kv4_pool* kv, const pka_kv_pool* dst, const int32
  * rounded to f16; bf16 out).  Arguments, masks and errors as there; any group
  * of 1 to 8 query heads per KV head.  A table id outside the pool reads as
  * zeros and ORs PKA_DEVERR_BAD_TABLE into params->err.
+ * One launch: segments (request, KV head) of at most 5 tiles of 16 keys per
+ * warp of a CTA (80 at D = 128, 40 at D = 256) stream whole; longer ones are
+ * cut into pieces, at most 32 each, whose fp32 partials the last piece to
+ * arrive merges in piece order (the same bits every time).
  * workspace: at least paged_kv4_decode_attn_ws_bytes() bytes, 16-byte
- * aligned: B * Hkv int32 arrival counters (padded to 16 bytes), then the
- * partials.  Counters zero before the first call, left zero by every call.
+ * aligned: 1024 bytes of arrival counters, then the partials.  The first 1024
+ * bytes must be zero before the first call and are left zero by every call, so
+ * calls of any sizes can use one workspace (of the largest size) in turn.
  * Calls sharing one workspace must not overlap on the GPU. */
 size_t paged_kv4_decode_attn_ws_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D,
                                       int32_t max_seq_len, int32_t window);

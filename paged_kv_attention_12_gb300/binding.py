@@ -562,17 +562,18 @@ def paged_kv_ref_blocks(block_tables, seq_lens, refcounts, delta: int, err=None,
 def _pool_list(pools):
     """The pools' device pointers as a C array, their blocks and bytes per block."""
     first = pools[0]
-    dev, n, nbytes = _cuda_device(first, "pools"), first.shape[0], first.nbytes
+    dev, shape, dtype = _cuda_device(first, "pools"), first.shape, first.dtype
     for p in pools:
-        if p.device != dev or not p.is_contiguous() or p.shape[0] != n or p.nbytes != nbytes:
-            _refuse(p, "pools", f"a contiguous tensor of {n} blocks, {nbytes} bytes, on {dev}")
+        if p.shape != shape or p.dtype is not dtype or p.device != dev or not p.is_contiguous():
+            _refuse(p, "pools", f"contiguous {dtype} {_dims(*shape)} on {dev}")
+    n = shape[0]
     return ((ctypes.c_void_p * len(pools))(*[p.data_ptr() for p in pools]), n,
-            nbytes // max(n, 1), dev)
+            first.nbytes // max(n, 1), dev)
 
 
 def paged_kv_copy_blocks(pools, src, dst, err=None, stream=None):
     """Copy block ``src[i]`` to block ``dst[i]`` (int32) in each of ``pools``
-    (tensors [num_blocks][...], of equal block size: K and V of every layer).
+    (tensors [num_blocks][...] of one shape and type: K and V of every layer).
     The destinations must be distinct and none of them a source."""
     import torch
     ptrs, n, nbytes, dev = _pool_list(pools)

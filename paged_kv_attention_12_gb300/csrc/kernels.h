@@ -168,7 +168,10 @@ struct Kv4ExpandArgs {
 cudaError_t launch_kv4_expand(const Kv4ExpandArgs& a, int sm_count, cudaStream_t stream);
 
 // Split-K decode over a 4-bit cache with the combine fused in.  base: q, out,
-// partials, counters, tables and sizes as for launch_decode (k and v unused).
+// partials, tables and sizes as for launch_decode (k and v unused);
+// seg_counters: one counter per CTA.
+constexpr int kKv4MaxCtas = 256;
+constexpr size_t kKv4CounterBytes = kKv4MaxCtas * sizeof(int32_t);
 struct Kv4DecodeArgs {
   DecodeArgs base;
   const uint8_t* k4;

@@ -29,22 +29,30 @@ int check_kv4_pointers(const pka_kv4_pool* kv) {
   return aligned16(kv->k) && aligned16(kv->v) ? PKA_OK : PKA_ERR_ALIGN;
 }
 
-// Workspace of the decode: arrival counters first (where a call with other
-// sizes finds its own), then partial outputs and partial LSEs.
+// Workspace of the decode: a fixed area of arrival counters (one per CTA, for
+// the cut segment whose first piece the CTA has), then partial outputs and
+// partial LSEs.  The counters lie in the same place whatever the sizes are, so
+// that calls of all sizes can share a workspace one after another.
 struct Kv4Layout {
-  int32_t S, C;
-  size_t cnt_bytes, o_bytes, lse_bytes;
-  size_t total() const { return cnt_bytes + o_bytes + lse_bytes; }
+  int32_t S, C;  // partial slots per (request, query head); shortest piece in tiles
+  size_t o_bytes, lse_bytes;
+  size_t total() const { return pka::kKv4CounterBytes + o_bytes + lse_bytes; }
 };
 
-int kv4_layout(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_seq_len,
-               int32_t window, Kv4Layout* L) {
-  const int st = paged_decode_splitk_plan(B, Hkv, max_seq_len, 16, window, 0, &L->S, &L->C);
-  if (st != PKA_OK) return st;
-  L->cnt_bytes = (static_cast<size_t>(B) * Hkv * sizeof(int32_t) + 15) / 16 * 16;
-  L->o_bytes = static_cast<size_t>(B) * Hq * L->S * D * sizeof(float);
-  L->lse_bytes = (static_cast<size_t>(B) * Hq * L->S * sizeof(float) + 15) / 16 * 16;
-  return PKA_OK;
+int32_t kv4_max_tiles(int32_t max_seq_len, int32_t window) {
+  const int32_t full = max_seq_len / 16 + (max_seq_len % 16 != 0);
+  return window > 0 ? std::min(full, (window - 1) / 16 + 2) : full;
+}
+
+Kv4Layout kv4_layout(int32_t B, int32_t Hq, int32_t D, int32_t max_seq_len, int32_t window) {
+  Kv4Layout L;
+  const int32_t T = kv4_max_tiles(max_seq_len, window);
+  // at least four tiles a piece, and at most 32 pieces of a segment
+  L.C = std::max(4, (T + 30) / 31);
+  L.S = (T + L.C - 1) / L.C + 1;
+  L.o_bytes = static_cast<size_t>(B) * Hq * L.S * D * sizeof(float);
+  L.lse_bytes = (static_cast<size_t>(B) * Hq * L.S * sizeof(float) + 15) / 16 * 16;
+  return L;
 }
 
 int check_pools(void* const* pools, int32_t num_pools, int32_t num_blocks, int64_t block_bytes) {
@@ -159,10 +167,8 @@ int paged_kv4_expand(const pka_kv4_pool* kv, const pka_kv_pool* dst, const int32
 
 size_t paged_kv4_decode_attn_ws_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D,
                                       int32_t max_seq_len, int32_t window) {
-  if (B <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0) return 0;
-  Kv4Layout L;
-  if (kv4_layout(B, Hq, Hkv, D, max_seq_len, window, &L) != PKA_OK) return 0;
-  return L.total();
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || max_seq_len < 0) return 0;
+  return kv4_layout(B, Hq, D, max_seq_len, window).total();
 }
 
 int paged_kv4_decode_attn_ws(const void* q, void* out, const pka_kv4_pool* kv,
@@ -170,9 +176,7 @@ int paged_kv4_decode_attn_ws(const void* q, void* out, const pka_kv4_pool* kv,
                              const int32_t* seq_lens, int32_t B, int32_t Hq,
                              int32_t max_seq_len, const pka_attn_params* params,
                              void* workspace, size_t workspace_bytes, void* stream) {
-  if (q == nullptr || out == nullptr || kv == nullptr || block_tables == nullptr ||
-      seq_lens == nullptr || params == nullptr || workspace == nullptr)
-    return PKA_ERR_NULL;
+  if (kv == nullptr || params == nullptr) return PKA_ERR_NULL;
   int st = check_kv4_sizes(kv);
   if (st != PKA_OK) return st;
   if (B < 0 || Hq <= 0 || max_blocks <= 0 || max_seq_len < 0 || Hq % kv->num_kv_heads != 0)
@@ -183,13 +187,14 @@ int paged_kv4_decode_attn_ws(const void* q, void* out, const pka_kv4_pool* kv,
   if (max_blocks > 0x7fffffff / 16) return PKA_ERR_SHAPE;
   if (Hq / kv->num_kv_heads > 8) return PKA_ERR_UNSUPPORTED;
   if (!std::isfinite(params->scale) || std::isnan(params->softcap)) return PKA_ERR_SHAPE;
+  if (B == 0) return PKA_OK;
+  if (q == nullptr || out == nullptr || block_tables == nullptr || seq_lens == nullptr ||
+      workspace == nullptr)
+    return PKA_ERR_NULL;
   st = check_kv4_pointers(kv);
   if (st != PKA_OK) return st;
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return PKA_ERR_ALIGN;
-  if (B == 0) return PKA_OK;
-  Kv4Layout L;
-  st = kv4_layout(B, Hq, kv->num_kv_heads, kv->head_dim, max_seq_len, params->window, &L);
-  if (st != PKA_OK) return st;
+  const Kv4Layout L = kv4_layout(B, Hq, kv->head_dim, max_seq_len, params->window);
   if (workspace_bytes < L.total()) return PKA_ERR_WORKSPACE;
   // the work line (visible blocks and a fixed cost of 16 units per segment) in
   // the kernels' 32-bit arithmetic
@@ -215,14 +220,13 @@ int paged_kv4_decode_attn_ws(const void* q, void* out, const pka_kv4_pool* kv,
   a.base.num_splits = L.S;
   a.base.split_blocks = L.C;
   a.base.seg_counters = reinterpret_cast<int32_t*>(ws);
-  a.base.partial_o = reinterpret_cast<float*>(ws + L.cnt_bytes);
-  a.base.partial_lse = reinterpret_cast<float*>(ws + L.cnt_bytes + L.o_bytes);
+  a.base.partial_o = reinterpret_cast<float*>(ws + pka::kKv4CounterBytes);
+  a.base.partial_lse = reinterpret_cast<float*>(ws + pka::kKv4CounterBytes + L.o_bytes);
   a.k4 = static_cast<const uint8_t*>(kv->k);
   a.v4 = static_cast<const uint8_t*>(kv->v);
   a.k_scale = kv->k_scale;
   a.v_scale = kv->v_scale;
-  a.max_tiles = (max_seq_len + 15) / 16;
-  if (params->window > 0) a.max_tiles = std::min(a.max_tiles, (params->window - 1) / 16 + 2);
+  a.max_tiles = kv4_max_tiles(max_seq_len, params->window);
   const int sms = pka::device_sm_count();
   if (sms <= 0) return PKA_ERR_CUDA;
   const cudaError_t e =

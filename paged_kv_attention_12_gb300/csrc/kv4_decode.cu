@@ -639,7 +639,8 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
     pc = plan[cur];  // not kept in registers over the loop
     const bool split = pc.npieces > 1;
     const size_t head0 = static_cast<size_t>(pc.qrow) * a.Hq + pc.kvh * G;
-    const int slot = min(pc.slot, a.num_splits - 1);
+    // (a row longer than max_seq_len may have more pieces than slots: reported)
+    const bool has_slot = pc.slot < a.num_splits;
     // lane (g, t) takes warps g and g + 8
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -659,8 +660,8 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
                                        __fdividef(ka.v_scale, den);
       // P carries a factor 2^kShift, the same in every piece; a NaN sum keeps
       // its weight, so that the merge of the pieces passes it on
-      if (split && warp == 0 && g == 0 && 2 * t + j < G)
-        __stcg(a.partial_lse + (head0 + 2 * t + j) * a.num_splits + slot,
+      if (split && has_slot && warp == 0 && g == 0 && 2 * t + j < G)
+        __stcg(a.partial_lse + (head0 + 2 * t + j) * a.num_splits + pc.slot,
                den == 0.f ? -INFINITY : (isnan(den) ? M : M + log2f(den)) * kLn2);
 #pragma unroll
       for (int u = 0; u < UNITS; ++u)
@@ -709,11 +710,11 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
       const int h = 2 * (il & 3) + ij;
       const int d0 = iu * kUnitChannels + (il >> 2) * 16 + ii * 4;
       if (item >= S::kFrags || h >= G) continue;
-      if (split)
+      if (split && has_slot)
         __stcg(reinterpret_cast<float4*>(a.partial_o +
-                                         ((head0 + h) * a.num_splits + slot) * D + d0),
+                                         ((head0 + h) * a.num_splits + pc.slot) * D + d0),
                y[k]);
-      else
+      else if (!split)
         *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + (head0 + h) * D + d0) =
             make_uint2(pack_bf16x2(y[k].x, y[k].y), pack_bf16x2(y[k].z, y[k].w));
     }
@@ -724,9 +725,11 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
       if (threadIdx.x == 0) {
         if (pc.npieces > a.num_splits) report(a.err, PKA_DEVERR_SEQ_LEN);
         int last = 0;
-        if (pc.slot < a.num_splits) {
+        if (has_slot) {
           fence_acq_rel_gpu();
-          int32_t* counter = a.seg_counters + pc.b * a.Hkv + pc.kvh;
+          // the counter of the CTA that has the segment's first piece (which
+          // is the last segment of that CTA's share: no other uses it)
+          int32_t* counter = a.seg_counters + blockIdx.x - pc.slot;
           last = atomicAdd(counter, 1) == np - 1;
           fence_acq_rel_gpu();
           if (last) *counter = 0;
@@ -834,7 +837,7 @@ cudaError_t launch_t(const Kv4DecodeArgs& a, int grid, cudaStream_t stream) {
 
 template <int D, int NW, int STAGES, int CTAS>
 cudaError_t launch_d(Kv4DecodeArgs a, int sms, cudaStream_t stream) {
-  const int grid = sms * CTAS;
+  const int grid = sms * CTAS < kKv4MaxCtas ? sms * CTAS : kKv4MaxCtas;
   a.most_parts = grid / a.base.Hkv;
   a.even_share = static_cast<float>(a.base.Hkv) / grid;
   a.whole = a.max_tiles <= kWholePerWarp * NW;

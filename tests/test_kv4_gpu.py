@@ -358,7 +358,7 @@ def test_decode_same_bits_every_time_and_wherever():
     ws = workspace(c)
     for _ in range(3):
         assert torch.equal(decode(c, ws=ws), first)
-    assert not ws[:4 * len(c["lens"]) * 2].any()
+    assert not ws[:1024].any()                         # the counters
     perm = torch.randperm(c["pool"].num_blocks, generator=torch.Generator().manual_seed(0))
     inv = torch.argsort(perm)
     moved = binding.Kv4Pool(c["pool"].k[perm.to(DEV)].contiguous(),
@@ -384,6 +384,35 @@ def test_decode_same_bits_every_time_and_wherever():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, first)
+
+
+def test_one_workspace_for_calls_of_all_sizes():
+    """Batches of other sizes and head dimensions in turn on one workspace: each
+    gives the bits that it gives on a workspace of its own."""
+    g = np.random.default_rng(4)
+    cases = [make(g.integers(0, most, b).tolist(), 8, 2, d, seed=b, spare=2)
+             for b, d, most in ((2, 256, 5000), (70, 128, 400), (3, 128, 2500), (100, 256, 200),
+                                (9, 256, 1500))]
+    want = [decode(c) for c in cases]
+    ws = torch.zeros(max(workspace(c).numel() for c in cases), dtype=torch.uint8, device=DEV)
+    for i in (0, 1, 2, 3, 4, 3, 0, 1, 4, 2):
+        assert torch.equal(decode(cases[i], ws=ws), want[i]), i
+    for i in (1, 3):
+        check(cases[i], want[i])
+
+
+def test_rows_longer_than_max_seq_len():
+    """max_seq_len is a promise; rows that break it are reported or right."""
+    for lens, promise in (([5000, 30], 64), (np.full(90, 300).tolist(), 64)):
+        c = make(lens, 8, 2, 128, seed=1)
+        err = i32([0])
+        out = decode(c, err=err, max_len=promise, ws=workspace(c))
+        torch.cuda.synchronize()
+        if err.item() == 0:
+            check(c, out)
+        else:
+            assert err.item() == binding.DEVERR_SEQ_LEN
+        check(c, decode(c))                            # and the next call is right
 
 
 def test_offsets_past_32_bits():
