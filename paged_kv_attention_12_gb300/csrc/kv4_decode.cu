@@ -43,12 +43,11 @@ namespace pka {
 
 namespace {
 
-// When no segment can be longer than this many tiles per warp, none is cut: a
-// merge through global memory costs about 3.5 us.  (B = 8, Hkv = 2, G = 4, us
-// a call in a stream of them, whole / cut: D = 128, 640 tokens 6.8 / 9.1, 1280
-// tokens 8.8 / 9.4, 1600 tokens 10.4 / 9.3; D = 256, 640 tokens 8.7 / 9.4, 800
-// tokens 10.3 / 9.4.)
-constexpr int kWholePerWarp = 5;
+// When no segment can be longer than this many tiles, none is cut: a merge
+// through global memory costs about 3 us.  (B = 8, Hkv = 2, G = 4, us a call in
+// a stream of them, whole / cut: D = 128, 1024 tokens 7.6 / 8.3, 1280 tokens
+// 8.8 / 8.5; D = 256, 640 tokens 8.4 / 9.0, 800 tokens 10.0 / 9.0.)
+constexpr int whole_tiles(int head_dim) { return head_dim == 128 ? 72 : 40; }
 // Else the shortest piece, in tiles.
 constexpr int kMinPiece = 16;
 
@@ -73,6 +72,17 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+// Orders the CTA's partials (behind a barrier) before its arrival, and the
+// other pieces' partials before what follows the last one.
+__device__ __forceinline__ int atomic_add_acq_rel(int32_t* p, int32_t v) {
+  int32_t old;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;"
+               : "=r"(old)
+               : "l"(p), "r"(v)
+               : "memory");
+  return old;
+}
+
 // Transpose of an 8x8 matrix of 16-bit values held two per lane.
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t r;
@@ -93,7 +103,6 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-constexpr int kMaxParts = 34;  // partial slots per segment (33 at most), padded
 constexpr int kLens = 320;  // requests whose lengths a CTA keeps in shared memory
 
 template <int D, int NW_, int STAGES_>
@@ -103,8 +112,8 @@ struct Kv4Shape {
   static constexpr int kTile = UNITS * kUnitBytes;  // one block and head of K (or V)
   static constexpr int kRing = NW * STAGES * 2 * kTile;
   static constexpr int kLen = 2 * kLens * 4;
-  // the warps' (max, sum) per head, later the pieces' weights
-  static constexpr int kMl = NW * 8 * 8 > 8 * kMaxParts * 4 ? NW * 8 * 8 : 8 * kMaxParts * 4;
+  // the warps' (max, sum) per head; a thread's (max, sum) in the pieces' merge
+  static constexpr int kMl = NW * 8 * 8 + NW * 32 * 8;
   // two pieces, the line's iterator, a flag
   static constexpr int kPlan = (2 * sizeof(Piece) + sizeof(LineIter) + 4 + 15) / 16 * 16;
   static constexpr int kFrags = UNITS * 4 * 2 * 32; // float4 of a warp's O state
@@ -243,7 +252,7 @@ __device__ __forceinline__ void kv4_values(const uint8_t* tile, float (&o)[D / 1
 template <int D, int NT, bool EDGE, bool CAP>
 __device__ __forceinline__ void kv4_tiles(const uint8_t* const (&tile)[NT],
                                           const uint2* bq, float (&o)[D / 128][8][4],
-                                          float (&m)[2], float (&l)[2],
+                                          float (&m)[2], float (&l)[4],
                                           float f0, float f1, float softcap, int tok0, int t_lo,
                                           int pos, int lane) {
   constexpr int UNITS = D / kUnitChannels;
@@ -291,6 +300,7 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* const (&tile)[NT],
       alpha[j] = (mn == -INFINITY) ? 1.f : fast_exp2(m[j] - mn);
       m[j] = mn;
       l[j] *= alpha[j];
+      l[2 + j] *= alpha[j];
     }
 #pragma unroll
     for (int u = 0; u < UNITS; ++u)
@@ -309,10 +319,11 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* const (&tile)[NT],
   for (int k = 0; k < NT; ++k) {
     const float p0 = fast_exp2(x[k][0] - r0), p1 = fast_exp2(x[k][1] - r1);
     const float p2 = fast_exp2(x[k][2] - r0), p3 = fast_exp2(x[k][3] - r1);
-    l[0] += p0 + p2;
-    l[1] += p1 + p3;
     const uint32_t pb0 = movmatrix_trans(pack_f16x2(p0, p1));  // keys 2t, 2t + 1 of head g
     const uint32_t pb1 = movmatrix_trans(pack_f16x2(p2, p3));  // keys 2t + 8, 2t + 9
+    // the weights' sums, of the rounded weights as the values see them: ones
+    // times P^T, every row of it the same
+    mma_f16_16816(l, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, pb0, pb1);
     kv4_values<D, EDGE>(tile[k] + UNITS * kUnitBytes, o, pb0, pb1, keep0, keep1, lane);
   }
 }
@@ -329,31 +340,43 @@ __device__ __forceinline__ int theta_parts(float nb, float rtheta) {
   return __float_as_int(__fmaf_ru(nb, rtheta, 8388608.f)) - 0x4b000000;
 }
 
-__device__ __forceinline__ bool theta_piece(const Kv4DecodeArgs& ka, const int* slen,
-                                            const float* nbf, int lane, int cta, Piece& p) {
+// Finds piece `cta` of the plan and writes it to *plan (fill_from: whether
+// there is one); the calling warp's lanes all take part.
+__device__ __forceinline__ void theta_piece(const Kv4DecodeArgs& ka, int* slen, float* nbf,
+                                            int lane, int cta, Piece* plan) {
   const DecodeArgs& a = ka.base;
-  int itiles = 0, ilongest = 0;
-  for (int b = lane; b < a.batch; b += 32) {
-    const int nb = static_cast<int>(nbf[b]);
-    itiles += nb;
-    ilongest = max(ilongest, nb);
+  // 24 steps from the even share to twice of it, which fits whenever the
+  // segments number at most half the CTAs, then 7 up to the longest
+  const float near = __fdividef(24.f, 24.f + lane);
+  int tiles = 0, longest = 0;
+  for (int base = 0; base < a.batch; base += 32) {
+    const int b = base + lane;
+    const int len = b < a.batch ? req_len_of(a, 0, 0, a.seq_lens[b]) : 0;
+    const int nb = geo_of_len(a, len).nb;
+    slen[b] = len;
+    nbf[b] = b < a.batch ? fmaxf(static_cast<float>(nb), 0.5f) : 0.f;
+    tiles += nb;
+    longest = max(longest, nb);
   }
-  const float tiles = static_cast<float>(__reduce_add_sync(0xffffffffu, itiles));
-  const float longest = static_cast<float>(__reduce_max_sync(0xffffffffu, ilongest));
-  // from the even share (at least split_blocks, which bounds the workspace's
-  // slots, and kMinPiece tiles): 24 steps to twice of it, which fits whenever
-  // the segments number at most half the CTAs, then 7 up to the longest
+  if (lane == 0) plan->fill_from = 0;
+  __syncwarp();
+  tiles = __reduce_add_sync(0xffffffffu, tiles);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  // the even share, at least split_blocks (which bounds the workspace's slots)
+  // and kMinPiece tiles
   const float lo = fmaxf(static_cast<float>(max(a.split_blocks, kMinPiece)),
-                         tiles * ka.even_share);
-  const float hi = fmaxf(longest, 2.f * lo);
-  float rtheta = __fdividef(1.f, lane < 25 ? lo + lo * (lane * (1.f / 24.f))
-                                           : 2.f * lo + (hi - 2.f * lo) * ((lane - 24) * (1.f / 7.f)));
+                         static_cast<float>(tiles) * ka.even_share);
+  const float hi = fmaxf(static_cast<float>(longest), 2.f * lo);
+  float rtheta = lane < 25 ? __fdividef(near, lo)
+                           : __fdividef(1.f, 2.f * lo + (hi - 2.f * lo) * ((lane - 24) * (1.f / 7.f)));
   int sum = 0;
-#pragma unroll 4
-  for (int b = 0; b < a.batch; b += 4) {  // padded with zeros, which give none
-    const float4 n = *reinterpret_cast<const float4*>(nbf + b);
-    sum += theta_parts(n.x, rtheta) + theta_parts(n.y, rtheta) + theta_parts(n.z, rtheta) +
-           theta_parts(n.w, rtheta);
+  for (int base = 0; base < a.batch; base += 32) {  // padded with zeros, which give none
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      const float4 n = *reinterpret_cast<const float4*>(nbf + base + i);
+      sum += theta_parts(n.x, rtheta) + theta_parts(n.y, rtheta) + theta_parts(n.z, rtheta) +
+             theta_parts(n.w, rtheta);
+    }
   }
   if (lane == 31) {  // one piece each
     rtheta = __fdividef(0.999f, hi);
@@ -361,39 +384,37 @@ __device__ __forceinline__ bool theta_piece(const Kv4DecodeArgs& ka, const int* 
   }
   const unsigned fits = __ballot_sync(0xffffffffu, sum <= ka.most_parts);
   rtheta = __shfl_sync(0xffffffffu, rtheta, __ffs(fits) - 1);
-  // the segment of piece `cta`: pieces lie in (request, head, part) order
+  // pieces lie in (request, head, part) order: the lane whose request has
+  // piece `cta` writes it
   int before = 0;
   for (int base = 0; base < a.batch; base += 32) {
     const int b = base + lane;
-    const float nb = b < a.batch ? nbf[b] : 0.f;
-    const int k = b < a.batch ? min(theta_parts(nb, rtheta), a.num_splits) : 0;
-    const int incl = warp_incl_scan(k * a.Hkv, lane);
-    const unsigned m = __ballot_sync(0xffffffffu, cta < before + incl);
-    if (m != 0) {
-      const int src = __ffs(m) - 1;
-      const int parts = __shfl_sync(0xffffffffu, k, src);
-      const int in = cta - before - __shfl_sync(0xffffffffu, incl - k * a.Hkv, src);
+    const int parts = min(theta_parts(nbf[b], rtheta), a.num_splits);  // 0 past the batch
+    const ReqGeo geo = geo_of_len(a, slen[b]);
+    const int incl = warp_incl_scan(parts * a.Hkv, lane) + before;
+    const int in = cta - (incl - parts * a.Hkv);
+    if (in >= 0 && cta < incl) {
       const float rparts = __fdividef(1.f, static_cast<float>(parts));
-      p.b = base + src;
+      Piece p;
+      p.b = p.qrow = b;
       p.kvh = static_cast<int>((static_cast<float>(in) + 0.5f) * rparts);
       p.slot = in - p.kvh * parts;
       p.npieces = parts;
-      const ReqGeo geo = geo_of_len(a, slen[p.b]);
       // piece k starts at tile floor(k * n / parts), in fp32 and the same for
       // both pieces that meet there
       const float each = static_cast<float>(geo.nb) * rparts;
       const int t0 = min(static_cast<int>(each * p.slot), geo.nb);
-      const int t1 = p.slot + 1 == parts ? geo.nb : min(static_cast<int>(each * (p.slot + 1)), geo.nb);
+      const int t1 =
+          p.slot + 1 == parts ? geo.nb : min(static_cast<int>(each * (p.slot + 1)), geo.nb);
       p.j0 = geo.jlo + t0;
       p.ntiles = t1 - t0;
       p.t_lo = geo.t_lo;
       p.pos = geo.pos;
-      p.qrow = p.b;
-      return true;
+      p.fill_from = 1;
+      *plan = p;
     }
-    before += __shfl_sync(0xffffffffu, incl, 31);
+    before = __shfl_sync(0xffffffffu, incl, 31);
   }
-  return false;
 }
 
 // LINE: more segments than CTAs, which then take several pieces of the
@@ -422,13 +443,6 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
 
   launch_dependents();
   wait_predecessor();
-  for (int b = threadIdx.x; b < kLens; b += NW * 32) {
-    const int len = b < a.batch ? req_len_of(a, 0, 0, a.seq_lens[b]) : 0;
-    slen[b] = len;
-    nbf[b] = b < a.batch ? fmaxf(static_cast<float>(geo_of_len(a, len).nb), 0.5f) : 0.f;
-  }
-  __syncthreads();
-
   // the CTA's piece, worked out by warp 0 (fill_from: whether there is one);
   // with LINE thread 0 walks the line, one piece ahead in the other slot
   auto next_piece = [&](Piece* to) {
@@ -439,6 +453,11 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
     *to = p;
     *line = it;
   };
+  if constexpr (LINE) {
+    for (int b = threadIdx.x; b < kLenCache; b += NW * 32)
+      slen[b] = b < a.batch ? req_len_of(a, 0, 0, a.seq_lens[b]) : 0;
+    __syncthreads();
+  }
   if (!LINE && ka.whole) {
     // no segment is long enough to be cut: piece c is segment c
     if (threadIdx.x == 0) {
@@ -447,7 +466,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
       if (p.fill_from != 0) {
         p.b = static_cast<int>(blockIdx.x) / a.Hkv;
         p.kvh = static_cast<int>(blockIdx.x) - p.b * a.Hkv;
-        const ReqGeo geo = geo_of_len(a, slen[p.b]);
+        const ReqGeo geo = geo_of_len(a, req_len_of(a, 0, 0, a.seq_lens[p.b]));
         p.j0 = geo.jlo;
         p.ntiles = geo.nb;
         p.t_lo = geo.t_lo;
@@ -466,12 +485,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
         next_piece(plan);
       }
     } else {
-      Piece p;
-      const bool any = theta_piece(ka, slen, nbf, lane, static_cast<int>(blockIdx.x), p);
-      if (lane == 0) {
-        p.fill_from = any;
-        *plan = p;
-      }
+      theta_piece(ka, slen, nbf, lane, static_cast<int>(blockIdx.x), plan);
     }
   }
   __syncthreads();
@@ -573,7 +587,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
     for (int u = 0; u < UNITS; ++u)
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[u][i][0] = o[u][i][1] = o[u][i][2] = o[u][i][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float m[2] = {-INFINITY, -INFINITY}, l[4] = {0.f, 0.f, 0.f, 0.f};
 
     // Invariant: tiles n .. n + STAGES - 1 are requested, one group each (empty
     // groups behind the last).
@@ -620,10 +634,6 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
     // ---- the warps' states merged in warp order: (max, sum) first, from which
     // every warp takes the factor of its own O, then the sum of the scaled O
     // states through shared memory (a warp without tiles holds zeros)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) l[j] += __shfl_xor_sync(0xffffffffu, l[j], off);
     if (g == 0) {
       ml[warp * 8 + 2 * t] = make_float2(m[0], l[0]);
       ml[warp * 8 + 2 * t + 1] = make_float2(m[1], l[1]);
@@ -726,93 +736,95 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
         if (pc.npieces > a.num_splits) report(a.err, PKA_DEVERR_SEQ_LEN);
         int last = 0;
         if (has_slot) {
-          fence_acq_rel_gpu();
           // the counter of the CTA that has the segment's first piece (which
           // is the last segment of that CTA's share: no other uses it)
           int32_t* counter = a.seg_counters + blockIdx.x - pc.slot;
-          last = atomicAdd(counter, 1) == np - 1;
-          fence_acq_rel_gpu();
+          last = atomic_add_acq_rel(counter, 1) == np - 1;
           if (last) *counter = 0;
         }
         *flag = last;
       }
       __syncthreads();
       if (*flag != 0) {
-        // the threads of an output item take every parts-th piece each; their
-        // first eight loads are in flight while the weights are computed
+        // The threads of an output item (four columns of a head) take every
+        // parts-th piece each, up to kFlight with all loads in flight, and fold
+        // them into a state (M, den, acc); the states of an item are merged
+        // through shared memory.
         constexpr int kRow = D / 4;
-        constexpr int kFlight = 8;
+        constexpr int kFlight = D == 256 ? 4 : 8;
         const int items = G * kRow;
         const int parts = max(1, NW * 32 / items);
-        float* wts = reinterpret_cast<float*>(ml);  // [G][kMaxParts]
-        auto load = [&](int item, int s0, float4 (&x)[kFlight]) {
-          const int it = item % items;
-          const float* po =
-              a.partial_o + (head0 + it / kRow) * a.num_splits * D + it % kRow * 4;
-#pragma unroll
-          for (int k = 0; k < kFlight; ++k)
-            x[k] = __ldcg(reinterpret_cast<const float4*>(
-                po + static_cast<size_t>(min(s0 + k * parts, np - 1)) * D));
-        };
-        float4 x[kFlight];
-        if (static_cast<int>(threadIdx.x) < items * parts)
-          load(threadIdx.x, threadIdx.x / items, x);
-        if (warp < G) {
-          const float* lse = a.partial_lse + (head0 + warp) * a.num_splits;
-          const float v0 = lane < np ? __ldcg(lse + lane) : -INFINITY;
-          const float v1 = lane + 32 < np ? __ldcg(lse + lane + 32) : -INFINITY;
-          float M = fmaxf(v0, v1);
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-          if (M == -INFINITY) M = 0.f;
-          const float w0 = fast_exp2((v0 - M) * kLog2e), w1 = fast_exp2((v1 - M) * kLog2e);
-          float den = w0 + w1;
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
+        auto finish = [&](int it, const float4& acc, float den) {
           const float inv = den == 0.f ? 0.f : 1.f / den;
-          if (lane < np) wts[warp * kMaxParts + lane] = w0 * inv;
-          if (lane + 32 < np) wts[warp * kMaxParts + lane + 32] = w1 * inv;
-        }
-        __syncthreads();
-        auto store = [&](int it, const float4& acc) {
           *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + (head0 + it / kRow) * D +
                                     it % kRow * 4) =
-              make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                         pack_bf16x2(acc.z * inv, acc.w * inv));
         };
+        float2* md = ml + NW * 8;
         for (int item = threadIdx.x; item < items * parts; item += NW * 32) {
-          const int part = item / items, it = item % items;
-          if (item >= NW * 32) load(item, part, x);
+          const int part = item / items, it = item - part * items;
+          const size_t row = (head0 + it / kRow) * a.num_splits;
+          const float* po = a.partial_o + row * D + it % kRow * 4;
+          float M = -INFINITY, den = 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
           for (int s0 = part; s0 < np; s0 += kFlight * parts) {
-            if (s0 != part) load(item, s0, x);
+            float lv[kFlight];
+            float4 x[kFlight];
 #pragma unroll
             for (int k = 0; k < kFlight; ++k) {
-              if (s0 + k * parts < np) {
-                const float w = wts[it / kRow * kMaxParts + s0 + k * parts];
-                acc.x = fmaf(w, x[k].x, acc.x);
-                acc.y = fmaf(w, x[k].y, acc.y);
-                acc.z = fmaf(w, x[k].z, acc.z);
-                acc.w = fmaf(w, x[k].w, acc.w);
-              }
+              const int sk = min(s0 + k * parts, np - 1);
+              lv[k] = __ldcg(a.partial_lse + row + sk);
+              x[k] = __ldcg(reinterpret_cast<const float4*>(po + static_cast<size_t>(sk) * D));
+            }
+            float top = M;
+#pragma unroll
+            for (int k = 0; k < kFlight; ++k) {
+              if (s0 + k * parts >= np) lv[k] = -INFINITY;
+              top = fmaxf(top, lv[k]);
+            }
+            if (top == -INFINITY) continue;
+            const float r = fast_exp2((M - top) * kLog2e);  // 0 while M = -inf
+            M = top;
+            den *= r;
+            acc = make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r);
+#pragma unroll
+            for (int k = 0; k < kFlight; ++k) {
+              if (s0 + k * parts >= np) break;
+              const float w = fast_exp2((lv[k] - top) * kLog2e);
+              den += w;
+              acc.x = fmaf(w, x[k].x, acc.x);
+              acc.y = fmaf(w, x[k].y, acc.y);
+              acc.z = fmaf(w, x[k].z, acc.z);
+              acc.w = fmaf(w, x[k].w, acc.w);
             }
           }
-          if (parts > 1)
+          if (parts > 1) {
             st[item] = acc;
-          else
-            store(it, acc);
+            md[item] = make_float2(M, den);
+          } else {
+            finish(it, acc, den);
+          }
         }
         if (parts > 1) {
           __syncthreads();
           for (int it = threadIdx.x; it < items; it += NW * 32) {
-            float4 acc = st[it];
-            for (int k = 1; k < parts; ++k) {
+            float M = -INFINITY;
+            for (int k = 0; k < parts; ++k) M = fmaxf(M, md[k * items + it].x);
+            float den = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < parts; ++k) {
+              const float2 v = md[k * items + it];
               const float4 z = st[k * items + it];
-              acc.x += z.x;
-              acc.y += z.y;
-              acc.z += z.z;
-              acc.w += z.w;
+              const float w = v.x == -INFINITY ? 0.f : fast_exp2((v.x - M) * kLog2e);
+              den = fmaf(w, v.y, den);
+              acc.x = fmaf(w, z.x, acc.x);
+              acc.y = fmaf(w, z.y, acc.y);
+              acc.z = fmaf(w, z.z, acc.z);
+              acc.w = fmaf(w, z.w, acc.w);
             }
-            store(it, acc);
+            finish(it, acc, den);
           }
         }
       }
@@ -840,7 +852,7 @@ cudaError_t launch_d(Kv4DecodeArgs a, int sms, cudaStream_t stream) {
   const int grid = sms * CTAS < kKv4MaxCtas ? sms * CTAS : kKv4MaxCtas;
   a.most_parts = grid / a.base.Hkv;
   a.even_share = static_cast<float>(a.base.Hkv) / grid;
-  a.whole = a.max_tiles <= kWholePerWarp * NW;
+  a.whole = a.max_tiles <= whole_tiles(D);
   const bool line = static_cast<int64_t>(a.base.batch) * a.base.Hkv > grid || a.base.batch > kLens;
   if (a.base.softcap > 0.f)
     return line ? launch_t<D, NW, STAGES, CTAS, true, true>(a, grid, stream)
