@@ -447,12 +447,11 @@ int paged_kv4_expand(const pka_kv4_pool* kv, const pka_kv_pool* dst, const int32
  * rounded to f16; bf16 out).  Arguments, masks and errors as there; any group
  * of 1 to 8 query heads per KV head.  A table id outside the pool reads as
  * zeros and ORs PKA_DEVERR_BAD_TABLE into params->err.
- * One launch: segments (request, KV head) of at most 5 tiles of 16 keys per
- * warp of a CTA (80 at D = 128, 40 at D = 256) stream whole; longer ones are
- * cut into pieces, at most 32 each, whose fp32 partials the last piece to
+ * One launch: short segments (request, KV head) stream whole; longer ones are
+ * cut into pieces, at most 30 each, whose fp32 partials the last piece to
  * arrive merges in piece order (the same bits every time).
  * workspace: at least paged_kv4_decode_attn_ws_bytes() bytes, 16-byte
- * aligned: 1024 bytes of arrival counters, then the partials.  The first 1024
+ * aligned: 2048 bytes of arrival counters, then the partials.  The first 2048
  * bytes must be zero before the first call and are left zero by every call, so
  * calls of any sizes can use one workspace (of the largest size) in turn.
  * Calls sharing one workspace must not overlap on the GPU. */

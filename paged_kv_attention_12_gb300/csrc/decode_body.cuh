@@ -207,9 +207,7 @@ constexpr int kLenCache = 128;
 // Enumerates the pieces of one pipeline.  Every lane of a warp runs it in
 // lockstep (it uses warp scans), and every warp of the pipeline sees the
 // same sequence.
-// kCost: the fixed cost of a piece (kPieceCost in the bf16 kernels).
-template <int kCost>
-struct PieceIterT {
+struct PieceIter {
   const DecodeArgs* a;
   const int* slen;  // req_len of the first min(B, kLenCache) requests (shared memory)
   int vcta, vgrid;  // this pipeline's index and the number of pipelines
@@ -225,7 +223,7 @@ struct PieceIterT {
   ReqGeo geo;
   bool done;
 
-  __device__ static int units(int nb) { return nb > 0 ? nb + kCost : 0; }
+  __device__ static int units(int nb) { return nb > 0 ? nb + kPieceCost : 0; }
   __device__ int len_of(int bb) const { return bb < kLenCache ? slen[bb] : req_len(*a, bb); }
 
   __device__ void init(const DecodeArgs& args, const int* slen_, int lane, int vcta_, int vgrid_) {
@@ -336,7 +334,7 @@ struct PieceIterT {
         const int n = geo.nb;
         const int u = units(n);
         const int seg = A.Hkv * prefix + kvh * u;       // segment start
-        const int s0 = seg + (n > 0 ? kCost : 0);  // unit of its first tile
+        const int s0 = seg + (n > 0 ? kPieceCost : 0);  // unit of its first tile
         const bool before = (n > 0 ? s0 + n : seg + 1) <= lo;  // wholly before this chunk
         const bool after = !last && seg >= hi;
         if (after) {
@@ -381,7 +379,6 @@ struct PieceIterT {
     return true;
   }
 };
-using PieceIter = PieceIterT<kPieceCost>;
 
 }  // namespace
 

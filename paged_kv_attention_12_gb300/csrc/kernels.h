@@ -169,9 +169,10 @@ cudaError_t launch_kv4_expand(const Kv4ExpandArgs& a, int sm_count, cudaStream_t
 
 // Split-K decode over a 4-bit cache with the combine fused in.  base: q, out,
 // partials, tables and sizes as for launch_decode (k and v unused);
-// seg_counters: one counter per CTA.
-constexpr int kKv4MaxCtas = 256;
-constexpr size_t kKv4CounterBytes = kKv4MaxCtas * sizeof(int32_t);
+// seg_counters: one counter per piece beyond one each of the segments, which
+// number at most kKv4MaxExtra.
+constexpr int kKv4MaxExtra = 512;
+constexpr size_t kKv4CounterBytes = kKv4MaxExtra * sizeof(int32_t);
 struct Kv4DecodeArgs {
   DecodeArgs base;
   const uint8_t* k4;

@@ -29,10 +29,9 @@ int check_kv4_pointers(const pka_kv4_pool* kv) {
   return aligned16(kv->k) && aligned16(kv->v) ? PKA_OK : PKA_ERR_ALIGN;
 }
 
-// Workspace of the decode: a fixed area of arrival counters (one per CTA, for
-// the cut segment whose first piece the CTA has), then partial outputs and
-// partial LSEs.  The counters lie in the same place whatever the sizes are, so
-// that calls of all sizes can share a workspace one after another.
+// Workspace of the decode: a fixed area of arrival counters, then partial
+// outputs and partial LSEs.  The counters lie in the same place whatever the
+// sizes are, so that calls of all sizes can share a workspace in turn.
 struct Kv4Layout {
   int32_t S, C;  // partial slots per (request, query head); shortest piece in tiles
   size_t o_bytes, lse_bytes;
@@ -47,8 +46,8 @@ int32_t kv4_max_tiles(int32_t max_seq_len, int32_t window) {
 Kv4Layout kv4_layout(int32_t B, int32_t Hq, int32_t D, int32_t max_seq_len, int32_t window) {
   Kv4Layout L;
   const int32_t T = kv4_max_tiles(max_seq_len, window);
-  // at least four tiles a piece, and at most 32 pieces of a segment
-  L.C = std::max(4, (T + 30) / 31);
+  // at least four tiles a piece, and at most 30 pieces of a segment
+  L.C = std::max(4, (T + 28) / 29);
   L.S = (T + L.C - 1) / L.C + 1;
   L.o_bytes = static_cast<size_t>(B) * Hq * L.S * D * sizeof(float);
   L.lse_bytes = (static_cast<size_t>(B) * Hq * L.S * sizeof(float) + 15) / 16 * 16;

@@ -36,6 +36,8 @@
 // P = 2^(x - m + kShift) lies in (0, 2^15]: f16 (11 bits, the only rounding
 // of P), of use down to 2^-32 of the largest weight; the sums are fp32 over
 // the unrounded values.
+#include <algorithm>
+
 #include "decode_body.cuh"
 #include "kv4.cuh"
 
@@ -48,12 +50,10 @@ namespace {
 // a stream of them, whole / cut: D = 128, 1024 tokens 7.6 / 8.3, 1280 tokens
 // 8.8 / 8.5; D = 256, 640 tokens 8.4 / 9.0, 800 tokens 10.0 / 9.0.)
 constexpr int whole_tiles(int head_dim) { return head_dim == 128 ? 72 : 40; }
+// The same for the small CTAs of large batches.
+constexpr int kSmallWhole = 24;
 // Else the shortest piece, in tiles.
 constexpr int kMinPiece = 16;
-
-// A line piece's fixed cost, in tiles.
-constexpr int kLinePieceCost = 16;
-using LineIter = PieceIterT<kLinePieceCost>;
 
 constexpr float kGrow = 7.f;
 constexpr float kShift = 8.f;
@@ -103,27 +103,30 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-constexpr int kLens = 320;  // requests whose lengths a CTA keeps in shared memory
-
-template <int D, int NW_, int STAGES_>
+// A CTA of NW warps with STAGES tiles in flight each, CTAS of them per SM; PW
+// warps of it work the plan out; LENS: requests whose lengths it has room for.
+template <int D, int NW_, int STAGES_, int CTAS_, int PW_, int LENS_>
 struct Kv4Shape {
-  static constexpr int NW = NW_, STAGES = STAGES_;
+  static constexpr int NW = NW_, STAGES = STAGES_, CTAS = CTAS_, PW = PW_, LENS = LENS_;
+  static constexpr int kMaxBatch = LENS - 4 * PW;   // (a warp's share of them is a multiple of 4)
   static constexpr int UNITS = D / kUnitChannels;
   static constexpr int kTile = UNITS * kUnitBytes;  // one block and head of K (or V)
-  static constexpr int kRing = NW * STAGES * 2 * kTile;
-  static constexpr int kLen = 2 * kLens * 4;
-  // the warps' (max, sum) per head; a thread's (max, sum) in the pieces' merge
-  static constexpr int kMl = NW * 8 * 8 + NW * 32 * 8;
-  // two pieces, the line's iterator, a flag
-  static constexpr int kPlan = (2 * sizeof(Piece) + sizeof(LineIter) + 4 + 15) / 16 * 16;
   static constexpr int kFrags = UNITS * 4 * 2 * 32; // float4 of a warp's O state
   static constexpr int kItems = (kFrags + NW * 32 - 1) / (NW * 32);
-  // the warps' O states are merged kRound warps at a time
-  static constexpr int kRounds = (D == 256 && NW > 8) ? 2 : 1;
-  static constexpr int kRound = NW / kRounds;
-  static_assert(NW % kRounds == 0, "equal rounds");
-  static constexpr int kQ = UNITS * 8 * 32 * 8;     // q as B fragments
-  static constexpr int kSmem = kRing + kLen + kMl + kPlan + kQ + kRound * kFrags * 16;
+  // Shared memory: the warps' rings, into which each warp's O state goes at the
+  // end and then the threads' states of the pieces' merge; lengths and tiles of
+  // the requests; the plan's sums; the warps' (max, sum) per head; the piece and
+  // a flag; q as B fragments.
+  static constexpr int kWarpRing = STAGES * 2 * kTile;
+  static constexpr int kLen = NW * kWarpRing;
+  static constexpr int kScr = kLen + 2 * LENS * 4;
+  static constexpr int kMl = kScr + PW * 32 * 4 + (PW + 1) / 2 * 16;
+  static constexpr int kPlan = kMl + NW * 8 * 8;
+  static constexpr int kQ = kPlan + (sizeof(Piece) + 4 + 15) / 16 * 16;
+  static constexpr int kSmem = kQ + UNITS * 8 * 32 * 8;
+  static_assert(NW <= 16 && LENS % 4 == 0, "");
+  static_assert(kWarpRing >= kFrags * 16 && kLen >= NW * 32 * (16 + 8), "the states fit the rings");
+  static_assert(kSmem <= 232448 / CTAS - 1024, "shared memory of a CTA");
 };
 
 // The four A registers of K's k-step S (0..7) of a unit: words of row g and
@@ -328,29 +331,44 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* const (&tile)[NT],
   }
 }
 
-// Pieces when the segments (request, KV head) number at most the CTAs: one
-// piece per CTA, so that no CTA pays a piece's fixed cost twice.  theta is the
-// smallest of 32 lengths with sum over segments of ceil(n / theta) <= CTAs;
-// segment n gets that many pieces of equal length (one: its output is written
-// without partials).  One warp of every CTA computes the plan, the same in all
-// of them; nbf holds the segments' tiles (an empty one counts a half, so that
-// it gets a piece of its own).
+// The plan: one piece per CTA, so that no CTA pays a piece's fixed cost twice.
+// theta is the smallest of 32 lengths with sum over segments (request, KV head)
+// of ceil(n / theta) <= CTAs; segment n gets that many pieces of equal length
+// (one: its output is written without partials).  Every CTA computes the same
+// plan from the lengths: each warp sums its share of the requests for all 32
+// lengths, one per lane.  nbf holds the segments' tiles (an empty one counts a
+// half, so that it gets a piece of its own).
 __device__ __forceinline__ int theta_parts(float nb, float rtheta) {
   // 2^23 + ceil(nb * rtheta), rounded up
   return __float_as_int(__fmaf_ru(nb, rtheta, 8388608.f)) - 0x4b000000;
 }
 
-// Finds piece `cta` of the plan and writes it to *plan (fill_from: whether
-// there is one); the calling warp's lanes all take part.
-__device__ __forceinline__ void theta_piece(const Kv4DecodeArgs& ka, int* slen, float* nbf,
-                                            int lane, int cta, Piece* plan) {
+// Finds piece `cta` and writes it to *plan (fill_from: whether there is one).
+// The first PW warps take part; the caller's barrier makes the result visible.
+template <typename S>
+__device__ __forceinline__ void theta_piece(const Kv4DecodeArgs& ka, uint8_t* smem, int cta,
+                                            Piece* plan) {
+  constexpr int PW = S::PW;
   const DecodeArgs& a = ka.base;
+  int* slen = reinterpret_cast<int*>(smem + S::kLen);
+  float* nbf = reinterpret_cast<float*>(slen + S::LENS);
+  int* sums = reinterpret_cast<int*>(smem + S::kScr);    // [PW][32]
+  int2* red = reinterpret_cast<int2*>(sums + PW * 32);  // [PW]
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int share = ((a.batch + PW - 1) / PW + 3) / 4 * 4;  // requests of a warp
   // 24 steps from the even share to twice of it, which fits whenever the
-  // segments number at most half the CTAs, then 7 up to the longest
+  // segments number at most half the CTAs, then 6 up to the longest, then one
+  // piece each, which always fits
   const float near = __fdividef(24.f, 24.f + lane);
   int tiles = 0, longest = 0;
-  for (int base = 0; base < a.batch; base += 32) {
-    const int b = base + lane;
+  auto sync = [&]() {
+    if constexpr (PW == 1)
+      __syncwarp();
+    else
+      named_sync(1, PW * 32);
+  };
+#pragma unroll 4
+  for (int b = threadIdx.x; b < PW * share; b += PW * 32) {
     const int len = b < a.batch ? req_len_of(a, 0, 0, a.seq_lens[b]) : 0;
     const int nb = geo_of_len(a, len).nb;
     slen[b] = len;
@@ -358,10 +376,16 @@ __device__ __forceinline__ void theta_piece(const Kv4DecodeArgs& ka, int* slen, 
     tiles += nb;
     longest = max(longest, nb);
   }
-  if (lane == 0) plan->fill_from = 0;
-  __syncwarp();
   tiles = __reduce_add_sync(0xffffffffu, tiles);
   longest = __reduce_max_sync(0xffffffffu, longest);
+  if (threadIdx.x == 0) plan->fill_from = 0;
+  if (PW > 1 && lane == 0) red[warp] = make_int2(tiles, longest);
+  sync();
+  if constexpr (PW > 1) {
+    const int2 r = lane < PW ? red[lane] : make_int2(0, 0);
+    tiles = __reduce_add_sync(0xffffffffu, r.x);
+    longest = __reduce_max_sync(0xffffffffu, r.y);
+  }
   // the even share, at least split_blocks (which bounds the workspace's slots)
   // and kMinPiece tiles
   const float lo = fmaxf(static_cast<float>(max(a.split_blocks, kMinPiece)),
@@ -369,27 +393,39 @@ __device__ __forceinline__ void theta_piece(const Kv4DecodeArgs& ka, int* slen, 
   const float hi = fmaxf(static_cast<float>(longest), 2.f * lo);
   float rtheta = lane < 25 ? __fdividef(near, lo)
                            : __fdividef(1.f, 2.f * lo + (hi - 2.f * lo) * ((lane - 24) * (1.f / 7.f)));
+  if (lane == 31) rtheta = __fdividef(0.999f, hi);
+  auto parts_of = [&](float nb) { return min(theta_parts(nb, rtheta), a.num_splits); };
   int sum = 0;
-  for (int base = 0; base < a.batch; base += 32) {  // padded with zeros, which give none
-#pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-      const float4 n = *reinterpret_cast<const float4*>(nbf + base + i);
-      sum += theta_parts(n.x, rtheta) + theta_parts(n.y, rtheta) + theta_parts(n.z, rtheta) +
-             theta_parts(n.w, rtheta);
-    }
+#pragma unroll 4
+  for (int i = 0; i < share; i += 4) {  // (padded with zeros, which give none)
+    const float4 n = *reinterpret_cast<const float4*>(nbf + warp * share + i);
+    sum += parts_of(n.x) + parts_of(n.y) + parts_of(n.z) + parts_of(n.w);
   }
-  if (lane == 31) {  // one piece each
-    rtheta = __fdividef(0.999f, hi);
+  if constexpr (PW > 1) {
+    sums[warp * 32 + lane] = sum;
+    sync();
+    if (warp != 0) return;
     sum = 0;
+#pragma unroll
+    for (int w = 0; w < PW; ++w) sum += sums[w * 32 + lane];
   }
-  const unsigned fits = __ballot_sync(0xffffffffu, sum <= ka.most_parts);
-  rtheta = __shfl_sync(0xffffffffu, rtheta, __ffs(fits) - 1);
-  // pieces lie in (request, head, part) order: the lane whose request has
-  // piece `cta` writes it
-  int before = 0;
-  for (int base = 0; base < a.batch; base += 32) {
-    const int b = base + lane;
-    const int parts = min(theta_parts(nbf[b], rtheta), a.num_splits);  // 0 past the batch
+  const int chosen = __ffs(__ballot_sync(0xffffffffu, sum <= ka.most_parts)) - 1;
+  rtheta = __shfl_sync(0xffffffffu, rtheta, chosen);
+  // pieces lie in (request, head, part) order: the share that has piece `cta`,
+  // then in it the lane whose request has it
+  int w = 0, before = 0;
+  if constexpr (PW > 1) {
+    const int mine = lane < PW ? sums[lane * 32 + chosen] * a.Hkv : 0;
+    const int upto = warp_incl_scan(mine, lane);
+    const unsigned m = __ballot_sync(0xffffffffu, cta < upto);
+    if (m == 0) return;
+    w = __ffs(m) - 1;
+    before = __shfl_sync(0xffffffffu, upto - mine, w);
+  }
+  for (int i = 0; i < share; i += 32) {
+    const bool in_share = i + lane < share;
+    const int b = w * share + (in_share ? i + lane : 0);
+    const int parts = in_share ? parts_of(nbf[b]) : 0;
     const ReqGeo geo = geo_of_len(a, slen[b]);
     const int incl = warp_incl_scan(parts * a.Hkv, lane) + before;
     const int in = cta - (incl - parts * a.Hkv);
@@ -417,55 +453,33 @@ __device__ __forceinline__ void theta_piece(const Kv4DecodeArgs& ka, int* slen, 
   }
 }
 
-// LINE: more segments than CTAs, which then take several pieces of the
-// split-K line each; else one piece per CTA.
-template <int D, int NW, int STAGES, int CTAS, bool CAP, bool LINE>
-__global__ void __launch_bounds__(NW * 32, CTAS)
+template <int D, typename S, bool CAP>
+__global__ void __launch_bounds__(S::NW * 32, S::CTAS)
     kv4_decode_kernel(const __grid_constant__ Kv4DecodeArgs ka) {
-  using S = Kv4Shape<D, NW, STAGES>;
-  constexpr int UNITS = S::UNITS;
+  constexpr int UNITS = S::UNITS, NW = S::NW, STAGES = S::STAGES;
   extern __shared__ __align__(128) uint8_t smem[];
   const DecodeArgs& a = ka.base;
   const int G = a.Hq / a.Hkv;
-  int* slen = reinterpret_cast<int*>(smem + S::kRing);
-  float* nbf = reinterpret_cast<float*>(slen + kLens);
-  float2* ml = reinterpret_cast<float2*>(smem + S::kRing + S::kLen);  // [NW][8]
-  Piece* plan = reinterpret_cast<Piece*>(smem + S::kRing + S::kLen + S::kMl);  // [2]
-  LineIter* line = reinterpret_cast<LineIter*>(plan + 2);
-  volatile int* flag = reinterpret_cast<int*>(line + 1);
-  uint2* bq = reinterpret_cast<uint2*>(smem + S::kRing + S::kLen + S::kMl + S::kPlan);  // [UNITS][8][32]
-  float4* st = reinterpret_cast<float4*>(smem + S::kRing + S::kLen + S::kMl + S::kPlan +
-                                         S::kQ);  // [kRound][kFrags]
+  float2* ml = reinterpret_cast<float2*>(smem + S::kMl);  // [NW][8]
+  Piece* plan = reinterpret_cast<Piece*>(smem + S::kPlan);
+  volatile int* flag = reinterpret_cast<int*>(plan + 1);
+  uint2* bq = reinterpret_cast<uint2*>(smem + S::kQ);      // [UNITS][8][32]
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  uint8_t* ring = smem + warp * STAGES * 2 * S::kTile;
+  uint8_t* ring = smem + warp * S::kWarpRing;
   const uint32_t ring_addr = smem_u32(ring);
+  const int cta = static_cast<int>(blockIdx.x);
 
   launch_dependents();
   wait_predecessor();
-  // the CTA's piece, worked out by warp 0 (fill_from: whether there is one);
-  // with LINE thread 0 walks the line, one piece ahead in the other slot
-  auto next_piece = [&](Piece* to) {
-    LineIter it = *line;
-    Piece p{};
-    const bool any = it.next(p, true);
-    p.fill_from = any;
-    *to = p;
-    *line = it;
-  };
-  if constexpr (LINE) {
-    for (int b = threadIdx.x; b < kLenCache; b += NW * 32)
-      slen[b] = b < a.batch ? req_len_of(a, 0, 0, a.seq_lens[b]) : 0;
-    __syncthreads();
-  }
-  if (!LINE && ka.whole) {
-    // no segment is long enough to be cut: piece c is segment c
+  if (ka.whole) {
+    // no segment is cut: piece c is segment c
     if (threadIdx.x == 0) {
       Piece p{};
-      p.fill_from = static_cast<int>(blockIdx.x) < a.batch * a.Hkv;
+      p.fill_from = cta < a.batch * a.Hkv;
       if (p.fill_from != 0) {
-        p.b = static_cast<int>(blockIdx.x) / a.Hkv;
-        p.kvh = static_cast<int>(blockIdx.x) - p.b * a.Hkv;
+        p.b = cta / a.Hkv;
+        p.kvh = cta - p.b * a.Hkv;
         const ReqGeo geo = geo_of_len(a, req_len_of(a, 0, 0, a.seq_lens[p.b]));
         p.j0 = geo.jlo;
         p.ntiles = geo.nb;
@@ -476,31 +490,23 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
       }
       *plan = p;
     }
-  } else if (warp == 0) {
-    if constexpr (LINE) {
-      LineIter it;
-      it.init(a, slen, lane, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
-      if (lane == 0) {
-        *line = it;
-        next_piece(plan);
-      }
-    } else {
-      theta_piece(ka, slen, nbf, lane, static_cast<int>(blockIdx.x), plan);
-    }
+  } else if (warp < S::PW) {
+    theta_piece<S>(ka, smem, cta, plan);
   }
   __syncthreads();
   Piece pc = *plan;
-  bool have = pc.fill_from != 0;
+  if (pc.fill_from == 0) return;
   const float inv_cap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
   const float lscale = a.scale * ka.k_scale * (a.softcap > 0.f ? inv_cap : kLog2e);
 
-  int first = 0, mine = 0;  // this warp's tiles of the piece: first .. first + mine - 1
-  int ids = 0;              // block ids of its tiles base .. base + 31, one per lane
-  auto load_ids = [&](const Piece& P, int base) {
+  // this warp's tiles of the piece: first .. first + mine - 1
+  const int first = pc.ntiles * warp / NW, mine = pc.ntiles * (warp + 1) / NW - first;
+  int ids = 0;  // block ids of its tiles base .. base + 31, one per lane
+  auto load_ids = [&](int base) {
     const int i = base + lane;
     int id = -1;
     if (i < mine) {
-      id = a.tables[static_cast<size_t>(P.b) * a.max_blocks + P.j0 + first + i];
+      id = a.tables[static_cast<size_t>(pc.b) * a.max_blocks + pc.j0 + first + i];
       if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.num_blocks)) {
         report(a.err, PKA_DEVERR_BAD_TABLE);
         id = -1;
@@ -508,12 +514,12 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
     }
     return id;
   };
-  // requests the warp's tile n of piece P (its id in lane n % 32 of ids)
-  auto issue = [&](const Piece& P, int n) {
+  // requests the warp's tile n (its id in lane n % 32 of ids)
+  auto issue = [&](int n) {
     const int id = __shfl_sync(0xffffffffu, ids, n & 31);
     const uint32_t bytes = id >= 0 ? 16u : 0u;  // a bad id reads as zeros
     const long long off =
-        (static_cast<long long>(max(id, 0)) * a.Hkv + P.kvh) * S::kTile;
+        (static_cast<long long>(max(id, 0)) * a.Hkv + pc.kvh) * S::kTile;
     const uint32_t dst = ring_addr + (n % STAGES) * 2 * S::kTile;
 #pragma unroll
     for (int c = 0; c < S::kTile / 512; ++c) {
@@ -529,343 +535,324 @@ __global__ void __launch_bounds__(NW * 32, CTAS)
       cp_async16(dst + (v ? S::kTile : 0) + c, (v ? ka.v4 : ka.k4) + off + c, bytes);
     }
   };
-  auto prologue = [&](const Piece& P) {
-    first = P.ntiles * warp / NW;
-    mine = P.ntiles * (warp + 1) / NW - first;
-    ids = load_ids(P, 0);
+  ids = load_ids(0);
 #pragma unroll
-    for (int n = 0; n < STAGES; ++n) {
-      if (n < mine) issue(P, n);
-      cp_async_commit();
+  for (int n = 0; n < STAGES; ++n) {
+    if (n < mine) issue(n);
+    cp_async_commit();
+  }
+
+  // ---- q of head g as B fragments in f16, scaled by a power of two: every
+  // warp finds the head's largest magnitude and writes its share for the CTA
+  float fq;  // the logit factor of head g
+  {
+    const uint16_t* qp =
+        a.q + (static_cast<size_t>(pc.qrow) * a.Hq + pc.kvh * G + (g < G ? g : 0)) * D + t * 32;
+    uint4 raw[UNITS * 4];
+    uint32_t top2 = 0;
+#pragma unroll
+    for (int i = 0; i < UNITS * 4; ++i) {
+      raw[i] = (g < G) ? __ldg(reinterpret_cast<const uint4*>(
+                             qp + (i >> 2) * kUnitChannels + (i & 3) * 8))
+                       : make_uint4(0u, 0u, 0u, 0u);
+      top2 = __vmaxu2(__vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu),
+                      __vmaxu2(__vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu), top2));
     }
+    uint32_t top = max(top2 & 0xffffu, top2 >> 16);  // as bf16 bits
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int e = min(max(254 - static_cast<int>(top >> 7), 1), 253);
+    const float down = __uint_as_float(static_cast<uint32_t>(e) << 23);
+    fq = lscale * __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < UNITS * 4; ++i) {
+      if (i % NW != warp) continue;
+      float f[8];
+      unpack8(raw[i], f);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        bq[(i * 2 + k) * 32 + lane] =
+            make_uint2(pack_f16x2(f[k * 4] * down, f[k * 4 + 1] * down),
+                       pack_f16x2(f[k * 4 + 2] * down, f[k * 4 + 3] * down));
+    }
+    __syncthreads();
+  }
+  const float f0 = __shfl_sync(0xffffffffu, fq, 8 * t);
+  const float f1 = __shfl_sync(0xffffffffu, fq, 8 * t + 4);
+
+  float o[UNITS][8][4];
+#pragma unroll
+  for (int u = 0; u < UNITS; ++u)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[u][i][0] = o[u][i][1] = o[u][i][2] = o[u][i][3] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[4] = {0.f, 0.f, 0.f, 0.f};
+
+  // Invariant: tiles n .. n + STAGES - 1 are requested, one group each (empty
+  // groups behind the last).
+  const int count = mine, tok_first = (pc.j0 + first) * kBlockSize;
+  int n = 0;
+  auto is_edge = [&](int k) {
+    const int tok0 = tok_first + k * kBlockSize;
+    return tok0 < pc.t_lo || tok0 + kBlockSize - 1 > pc.pos;
   };
-  if (!have) return;
-  prologue(pc);
-  int cur = 0;
-
-  while (true) {
-    // ---- q of head g as B fragments in f16, scaled by a power of two: every
-    // warp finds the head's largest magnitude and writes its share for the CTA
-    float fq;  // the logit factor of head g
-    {
-      const uint16_t* qp =
-          a.q + (static_cast<size_t>(pc.qrow) * a.Hq + pc.kvh * G + (g < G ? g : 0)) * D + t * 32;
-      uint4 raw[UNITS * 4];
-      uint32_t top2 = 0;
-#pragma unroll
-      for (int i = 0; i < UNITS * 4; ++i) {
-        raw[i] = (g < G) ? __ldg(reinterpret_cast<const uint4*>(
-                               qp + (i >> 2) * kUnitChannels + (i & 3) * 8))
-                         : make_uint4(0u, 0u, 0u, 0u);
-        top2 = __vmaxu2(__vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu),
-                        __vmaxu2(__vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu), top2));
-      }
-      uint32_t top = max(top2 & 0xffffu, top2 >> 16);  // as bf16 bits
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int e = min(max(254 - static_cast<int>(top >> 7), 1), 253);
-      const float down = __uint_as_float(static_cast<uint32_t>(e) << 23);
-      fq = lscale * __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-#pragma unroll
-      for (int i = 0; i < UNITS * 4; ++i) {
-        if (i % NW != warp) continue;
-        float f[8];
-        unpack8(raw[i], f);
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          bq[(i * 2 + k) * 32 + lane] =
-              make_uint2(pack_f16x2(f[k * 4] * down, f[k * 4 + 1] * down),
-                         pack_f16x2(f[k * 4 + 2] * down, f[k * 4 + 3] * down));
-      }
-      __syncthreads();
+  auto refill = [&](int k) {  // the slot of tile k is free
+    const int ahead = k + STAGES;
+    if (ahead < count) {
+      if ((ahead & 31) == 0) ids = load_ids(ahead);
+      issue(ahead);
     }
-    const float f0 = __shfl_sync(0xffffffffu, fq, 8 * t);
-    const float f1 = __shfl_sync(0xffffffffu, fq, 8 * t + 4);
+    cp_async_commit();
+  };
+  while (n < count) {
+    const uint8_t* t0 = ring + (n % STAGES) * 2 * S::kTile;
+    if (n + 1 < count && !is_edge(n) && !is_edge(n + 1)) {
+      cp_async_wait<STAGES - 2>();
+      __syncwarp();  // every lane's part of the tiles has landed
+      const uint8_t* const tiles[2] = {t0, ring + ((n + 1) % STAGES) * 2 * S::kTile};
+      kv4_tiles<D, 2, false, CAP>(tiles, bq, o, m, l, f0, f1, a.softcap, 0, 0, 0, lane);
+      __syncwarp();
+      refill(n);
+      refill(n + 1);
+      n += 2;
+    } else {
+      cp_async_wait<STAGES - 1>();
+      __syncwarp();
+      const uint8_t* const tiles[1] = {t0};
+      kv4_tiles<D, 1, true, CAP>(tiles, bq, o, m, l, f0, f1, a.softcap,
+                                 tok_first + n * kBlockSize, pc.t_lo, pc.pos, lane);
+      __syncwarp();
+      refill(n);
+      ++n;
+    }
+  }
 
-    float o[UNITS][8][4];
+  // ---- the warps' states merged in warp order: (max, sum) first, from which
+  // every warp takes the factor of its own O, then the sum of the scaled O
+  // states through shared memory (a warp without tiles holds zeros)
+  if (g == 0) {
+    ml[warp * 8 + 2 * t] = make_float2(m[0], l[0]);
+    ml[warp * 8 + 2 * t + 1] = make_float2(m[1], l[1]);
+  }
+  __syncthreads();
+  pc = *plan;  // not kept in registers over the loop
+  const bool split = pc.npieces > 1;
+  const size_t head0 = static_cast<size_t>(pc.qrow) * a.Hq + pc.kvh * G;
+  // (a row longer than max_seq_len may have more pieces than slots: reported)
+  const bool has_slot = pc.slot < a.num_splits;
+  // lane (g, t) takes warps g and g + 8
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const float2 none = make_float2(-INFINITY, 0.f);
+    const float2 v0 = g < NW ? ml[g * 8 + 2 * t + j] : none;
+    const float2 v1 = g + 8 < NW ? ml[(g + 8) * 8 + 2 * t + j] : none;
+    float M = fmaxf(v0.x, v1.x);
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    if (M == -INFINITY) M = 0.f;
+    float den = ((v0.x == -INFINITY) ? 1.f : fast_exp2(v0.x - M)) * v0.y +
+                ((v1.x == -INFINITY) ? 1.f : fast_exp2(v1.x - M)) * v1.y;
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
+    const float f = den == 0.f ? 0.f
+                               : ((m[j] == -INFINITY) ? 1.f : fast_exp2(m[j] - M)) *
+                                     __fdividef(ka.v_scale, den);
+    // P carries a factor 2^kShift, the same in every piece; a NaN sum keeps
+    // its weight, so that the merge of the pieces passes it on
+    if (split && has_slot && warp == 0 && g == 0 && 2 * t + j < G)
+      __stcg(a.partial_lse + (head0 + 2 * t + j) * a.num_splits + pc.slot,
+             den == 0.f ? -INFINITY : (isnan(den) ? M : M + log2f(den)) * kLn2);
 #pragma unroll
     for (int u = 0; u < UNITS; ++u)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[u][i][0] = o[u][i][1] = o[u][i][2] = o[u][i][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[4] = {0.f, 0.f, 0.f, 0.f};
-
-    // Invariant: tiles n .. n + STAGES - 1 are requested, one group each (empty
-    // groups behind the last).
-    const int count = mine, tok_first = (pc.j0 + first) * kBlockSize;
-    int n = 0;
-    auto is_edge = [&](int k) {
-      const int tok0 = tok_first + k * kBlockSize;
-      return tok0 < pc.t_lo || tok0 + kBlockSize - 1 > pc.pos;
-    };
-    auto refill = [&](int k) {  // the slot of tile k is free
-      const int ahead = k + STAGES;
-      if (ahead < count) {
-        if ((ahead & 31) == 0) ids = load_ids(pc, ahead);
-        issue(pc, ahead);
+      for (int i = 0; i < 8; ++i) {
+        o[u][i][j] *= f;
+        o[u][i][2 + j] *= f;
       }
-      cp_async_commit();
-    };
-    while (n < count) {
-      const uint8_t* t0 = ring + (n % STAGES) * 2 * S::kTile;
-      if (n + 1 < count && !is_edge(n) && !is_edge(n + 1)) {
-        cp_async_wait<STAGES - 2>();
-        __syncwarp();  // every lane's part of the tiles has landed
-        const uint8_t* const tiles[2] = {t0, ring + ((n + 1) % STAGES) * 2 * S::kTile};
-        kv4_tiles<D, 2, false, CAP>(tiles, bq, o, m, l, f0, f1, a.softcap, 0, 0, 0, lane);
-        __syncwarp();
-        refill(n);
-        refill(n + 1);
-        n += 2;
-      } else {
-        cp_async_wait<STAGES - 1>();
-        __syncwarp();
-        const uint8_t* const tiles[1] = {t0};
-        kv4_tiles<D, 1, true, CAP>(tiles, bq, o, m, l, f0, f1, a.softcap,
-                                   tok_first + n * kBlockSize, pc.t_lo, pc.pos, lane);
-        __syncwarp();
-        refill(n);
-        ++n;
+  }
+  auto state = [&](int w, int item) {
+    return reinterpret_cast<const float4*>(smem + w * S::kWarpRing) + item;
+  };
+  if (2 * t < G) {
+    float4* row = reinterpret_cast<float4*>(ring) + lane;  // every tile of it is consumed
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          row[((u * 4 + i) * 2 + j) * 32] =
+              make_float4(o[u][2 * i][j], o[u][2 * i][2 + j], o[u][2 * i + 1][j],
+                          o[u][2 * i + 1][2 + j]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < S::kItems; ++k) {
+    const int item = threadIdx.x + k * NW * 32;
+    const int il = item & 31, ij = (item >> 5) & 1, ii = (item >> 6) & 3, iu = item >> 8;
+    const int h = 2 * (il & 3) + ij;
+    const int d0 = iu * kUnitChannels + (il >> 2) * 16 + ii * 4;
+    if (item >= S::kFrags || h >= G) continue;
+    float4 y = *state(0, item);
+#pragma unroll
+    for (int w = 1; w < NW; ++w) {
+      const float4 x = *state(w, item);
+      y.x += x.x;
+      y.y += x.y;
+      y.z += x.z;
+      y.w += x.w;
+    }
+    if (split && has_slot)
+      __stcg(reinterpret_cast<float4*>(a.partial_o +
+                                       ((head0 + h) * a.num_splits + pc.slot) * D + d0),
+             y);
+    else if (!split)
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + (head0 + h) * D + d0) =
+          make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+  }
+  if (split) {
+    // ---- the piece that arrives last at its segment merges the partials
+    const int np = min(pc.npieces, a.num_splits);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      if (pc.npieces > a.num_splits) report(a.err, PKA_DEVERR_SEQ_LEN);
+      int last = 0;
+      if (has_slot) {
+        // the segment's counter: the pieces beyond one each of the segments
+        // before it, a number that every cut segment raises
+        int32_t* counter = a.seg_counters + (cta - pc.slot) - (pc.b * a.Hkv + pc.kvh);
+        last = atomic_add_acq_rel(counter, 1) == np - 1;
+        if (last) *counter = 0;
       }
-    }
-
-    if constexpr (LINE) {
-      if (threadIdx.x == 0) next_piece(plan + (cur ^ 1));
-    }
-    // ---- the warps' states merged in warp order: (max, sum) first, from which
-    // every warp takes the factor of its own O, then the sum of the scaled O
-    // states through shared memory (a warp without tiles holds zeros)
-    if (g == 0) {
-      ml[warp * 8 + 2 * t] = make_float2(m[0], l[0]);
-      ml[warp * 8 + 2 * t + 1] = make_float2(m[1], l[1]);
+      *flag = last;
     }
     __syncthreads();
-    bool have_next = false;
-    if constexpr (LINE) {
-      // the next piece's first tiles, before this piece is merged
-      const Piece nx = plan[cur ^ 1];
-      have_next = nx.fill_from != 0;
-      if (have_next) prologue(nx);
-    }
-    pc = plan[cur];  // not kept in registers over the loop
-    const bool split = pc.npieces > 1;
-    const size_t head0 = static_cast<size_t>(pc.qrow) * a.Hq + pc.kvh * G;
-    // (a row longer than max_seq_len may have more pieces than slots: reported)
-    const bool has_slot = pc.slot < a.num_splits;
-    // lane (g, t) takes warps g and g + 8
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float2 none = make_float2(-INFINITY, 0.f);
-      const float2 v0 = g < NW ? ml[g * 8 + 2 * t + j] : none;
-      const float2 v1 = g + 8 < NW ? ml[(g + 8) * 8 + 2 * t + j] : none;
-      float M = fmaxf(v0.x, v1.x);
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-      if (M == -INFINITY) M = 0.f;
-      float den = ((v0.x == -INFINITY) ? 1.f : fast_exp2(v0.x - M)) * v0.y +
-                  ((v1.x == -INFINITY) ? 1.f : fast_exp2(v1.x - M)) * v1.y;
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
-      const float f = den == 0.f ? 0.f
-                                 : ((m[j] == -INFINITY) ? 1.f : fast_exp2(m[j] - M)) *
-                                       __fdividef(ka.v_scale, den);
-      // P carries a factor 2^kShift, the same in every piece; a NaN sum keeps
-      // its weight, so that the merge of the pieces passes it on
-      if (split && has_slot && warp == 0 && g == 0 && 2 * t + j < G)
-        __stcg(a.partial_lse + (head0 + 2 * t + j) * a.num_splits + pc.slot,
-               den == 0.f ? -INFINITY : (isnan(den) ? M : M + log2f(den)) * kLn2);
-#pragma unroll
-      for (int u = 0; u < UNITS; ++u)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          o[u][i][j] *= f;
-          o[u][i][2 + j] *= f;
-        }
-    }
-    float4 y[S::kItems];
-#pragma unroll
-    for (int r = 0; r < S::kRounds; ++r) {
-      if (r > 0) __syncthreads();  // the last round's states are read
-      if (warp / S::kRound == r && 2 * t < G) {
-        float4* row = st + (warp - r * S::kRound) * S::kFrags + lane;
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              row[((u * 4 + i) * 2 + j) * 32] =
-                  make_float4(o[u][2 * i][j], o[u][2 * i][2 + j], o[u][2 * i + 1][j],
-                              o[u][2 * i + 1][2 + j]);
-      }
-      __syncthreads();
-#pragma unroll
-      for (int k = 0; k < S::kItems; ++k) {
-        const int item = threadIdx.x + k * NW * 32;
-        if (item >= S::kFrags || 2 * (item & 3) + ((item >> 5) & 1) >= G) continue;
-        if (r == 0) y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < S::kRound; ++w) {
-          const float4 x = st[w * S::kFrags + item];
-          y[k].x += x.x;
-          y[k].y += x.y;
-          y[k].z += x.z;
-          y[k].w += x.w;
-        }
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < S::kItems; ++k) {
-      const int item = threadIdx.x + k * NW * 32;
-      const int il = item & 31, ij = (item >> 5) & 1, ii = (item >> 6) & 3, iu = item >> 8;
-      const int h = 2 * (il & 3) + ij;
-      const int d0 = iu * kUnitChannels + (il >> 2) * 16 + ii * 4;
-      if (item >= S::kFrags || h >= G) continue;
-      if (split && has_slot)
-        __stcg(reinterpret_cast<float4*>(a.partial_o +
-                                         ((head0 + h) * a.num_splits + pc.slot) * D + d0),
-               y[k]);
-      else if (!split)
-        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + (head0 + h) * D + d0) =
-            make_uint2(pack_bf16x2(y[k].x, y[k].y), pack_bf16x2(y[k].z, y[k].w));
-    }
-    if (split) {
-      // ---- the piece that arrives last at its segment merges the partials
-      const int np = min(pc.npieces, a.num_splits);
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        if (pc.npieces > a.num_splits) report(a.err, PKA_DEVERR_SEQ_LEN);
-        int last = 0;
-        if (has_slot) {
-          // the counter of the CTA that has the segment's first piece (which
-          // is the last segment of that CTA's share: no other uses it)
-          int32_t* counter = a.seg_counters + blockIdx.x - pc.slot;
-          last = atomic_add_acq_rel(counter, 1) == np - 1;
-          if (last) *counter = 0;
-        }
-        *flag = last;
-      }
-      __syncthreads();
-      if (*flag != 0) {
-        // The threads of an output item (four columns of a head) take every
-        // parts-th piece each, up to kFlight with all loads in flight, and fold
-        // them into a state (M, den, acc); the states of an item are merged
-        // through shared memory.
-        constexpr int kRow = D / 4;
-        constexpr int kFlight = D == 256 ? 4 : 8;
-        const int items = G * kRow;
-        const int parts = max(1, NW * 32 / items);
-        auto finish = [&](int it, const float4& acc, float den) {
-          const float inv = den == 0.f ? 0.f : 1.f / den;
-          *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + (head0 + it / kRow) * D +
-                                    it % kRow * 4) =
-              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
-                         pack_bf16x2(acc.z * inv, acc.w * inv));
-        };
-        float2* md = ml + NW * 8;
-        for (int item = threadIdx.x; item < items * parts; item += NW * 32) {
-          const int part = item / items, it = item - part * items;
-          const size_t row = (head0 + it / kRow) * a.num_splits;
-          const float* po = a.partial_o + row * D + it % kRow * 4;
-          float M = -INFINITY, den = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (*flag != 0) {
+      // The threads of an output item (four columns of a head) take every
+      // parts-th piece each, up to kFlight with all loads in flight, and fold
+      // them into a state (M, den, acc); the states of an item are merged
+      // through shared memory.
+      constexpr int kRow = D / 4;
+      constexpr int kFlight = D == 256 ? 4 : 8;
+      const int items = G * kRow;
+      const int parts = max(1, NW * 32 / items);
+      auto finish = [&](int it, const float4& acc, float den) {
+        const float inv = den == 0.f ? 0.f : 1.f / den;
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + (head0 + it / kRow) * D +
+                                  it % kRow * 4) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                       pack_bf16x2(acc.z * inv, acc.w * inv));
+      };
+      float4* st = reinterpret_cast<float4*>(smem);           // [NW * 32]
+      float2* md = reinterpret_cast<float2*>(st + NW * 32);  // [NW * 32]
+      for (int item = threadIdx.x; item < items * parts; item += NW * 32) {
+        const int part = item / items, it = item - part * items;
+        const size_t row = (head0 + it / kRow) * a.num_splits;
+        const float* po = a.partial_o + row * D + it % kRow * 4;
+        float M = -INFINITY, den = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-          for (int s0 = part; s0 < np; s0 += kFlight * parts) {
-            float lv[kFlight];
-            float4 x[kFlight];
+        for (int s0 = part; s0 < np; s0 += kFlight * parts) {
+          float lv[kFlight];
+          float4 x[kFlight];
 #pragma unroll
-            for (int k = 0; k < kFlight; ++k) {
-              const int sk = min(s0 + k * parts, np - 1);
-              lv[k] = __ldcg(a.partial_lse + row + sk);
-              x[k] = __ldcg(reinterpret_cast<const float4*>(po + static_cast<size_t>(sk) * D));
-            }
-            float top = M;
-#pragma unroll
-            for (int k = 0; k < kFlight; ++k) {
-              if (s0 + k * parts >= np) lv[k] = -INFINITY;
-              top = fmaxf(top, lv[k]);
-            }
-            if (top == -INFINITY) continue;
-            const float r = fast_exp2((M - top) * kLog2e);  // 0 while M = -inf
-            M = top;
-            den *= r;
-            acc = make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r);
-#pragma unroll
-            for (int k = 0; k < kFlight; ++k) {
-              if (s0 + k * parts >= np) break;
-              const float w = fast_exp2((lv[k] - top) * kLog2e);
-              den += w;
-              acc.x = fmaf(w, x[k].x, acc.x);
-              acc.y = fmaf(w, x[k].y, acc.y);
-              acc.z = fmaf(w, x[k].z, acc.z);
-              acc.w = fmaf(w, x[k].w, acc.w);
-            }
+          for (int k = 0; k < kFlight; ++k) {
+            const int sk = min(s0 + k * parts, np - 1);
+            lv[k] = __ldcg(a.partial_lse + row + sk);
+            x[k] = __ldcg(reinterpret_cast<const float4*>(po + static_cast<size_t>(sk) * D));
           }
-          if (parts > 1) {
-            st[item] = acc;
-            md[item] = make_float2(M, den);
-          } else {
-            finish(it, acc, den);
+          float top = M;
+#pragma unroll
+          for (int k = 0; k < kFlight; ++k) {
+            if (s0 + k * parts >= np) lv[k] = -INFINITY;
+            top = fmaxf(top, lv[k]);
+          }
+          if (top == -INFINITY) continue;
+          const float r = fast_exp2((M - top) * kLog2e);  // 0 while M = -inf
+          M = top;
+          den *= r;
+          acc = make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r);
+#pragma unroll
+          for (int k = 0; k < kFlight; ++k) {
+            if (s0 + k * parts >= np) break;
+            const float w = fast_exp2((lv[k] - top) * kLog2e);
+            den += w;
+            acc.x = fmaf(w, x[k].x, acc.x);
+            acc.y = fmaf(w, x[k].y, acc.y);
+            acc.z = fmaf(w, x[k].z, acc.z);
+            acc.w = fmaf(w, x[k].w, acc.w);
           }
         }
         if (parts > 1) {
-          __syncthreads();
-          for (int it = threadIdx.x; it < items; it += NW * 32) {
-            float M = -INFINITY;
-            for (int k = 0; k < parts; ++k) M = fmaxf(M, md[k * items + it].x);
-            float den = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = 0; k < parts; ++k) {
-              const float2 v = md[k * items + it];
-              const float4 z = st[k * items + it];
-              const float w = v.x == -INFINITY ? 0.f : fast_exp2((v.x - M) * kLog2e);
-              den = fmaf(w, v.y, den);
-              acc.x = fmaf(w, z.x, acc.x);
-              acc.y = fmaf(w, z.y, acc.y);
-              acc.z = fmaf(w, z.z, acc.z);
-              acc.w = fmaf(w, z.w, acc.w);
-            }
-            finish(it, acc, den);
+          st[item] = acc;
+          md[item] = make_float2(M, den);
+        } else {
+          finish(it, acc, den);
+        }
+      }
+      if (parts > 1) {
+        __syncthreads();
+        for (int it = threadIdx.x; it < items; it += NW * 32) {
+          float M = -INFINITY;
+          for (int k = 0; k < parts; ++k) M = fmaxf(M, md[k * items + it].x);
+          float den = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int k = 0; k < parts; ++k) {
+            const float2 v = md[k * items + it];
+            const float4 z = st[k * items + it];
+            const float w = v.x == -INFINITY ? 0.f : fast_exp2((v.x - M) * kLog2e);
+            den = fmaf(w, v.y, den);
+            acc.x = fmaf(w, z.x, acc.x);
+            acc.y = fmaf(w, z.y, acc.y);
+            acc.z = fmaf(w, z.z, acc.z);
+            acc.w = fmaf(w, z.w, acc.w);
           }
+          finish(it, acc, den);
         }
       }
     }
-    if (!have_next) break;
-    __syncthreads();  // the states' shared memory is free again
-    cur ^= 1;
-    pc = plan[cur];
   }
   cp_async_wait<0>();
 }
 
-template <int D, int NW, int STAGES, int CTAS, bool CAP, bool LINE>
-cudaError_t launch_t(const Kv4DecodeArgs& a, int grid, cudaStream_t stream) {
-  using S = Kv4Shape<D, NW, STAGES>;
-  auto kern = kv4_decode_kernel<D, NW, STAGES, CTAS, CAP, LINE>;
-  static_assert(S::kSmem <= 232448 / CTAS - 1024, "shared memory of a CTA");
-  const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), S::kSmem);
-  if (e != cudaSuccess) return e;
-  return launch_overlapped(kern, grid, NW * 32, S::kSmem, stream, a);
-}
-
-template <int D, int NW, int STAGES, int CTAS>
-cudaError_t launch_d(Kv4DecodeArgs a, int sms, cudaStream_t stream) {
-  const int grid = sms * CTAS < kKv4MaxCtas ? sms * CTAS : kKv4MaxCtas;
+template <int D, typename S>
+cudaError_t launch_t(Kv4DecodeArgs a, int grid, cudaStream_t stream) {
   a.most_parts = grid / a.base.Hkv;
   a.even_share = static_cast<float>(a.base.Hkv) / grid;
-  a.whole = a.max_tiles <= whole_tiles(D);
-  const bool line = static_cast<int64_t>(a.base.batch) * a.base.Hkv > grid || a.base.batch > kLens;
-  if (a.base.softcap > 0.f)
-    return line ? launch_t<D, NW, STAGES, CTAS, true, true>(a, grid, stream)
-                : launch_t<D, NW, STAGES, CTAS, true, false>(a, grid, stream);
-  return line ? launch_t<D, NW, STAGES, CTAS, false, true>(a, grid, stream)
-              : launch_t<D, NW, STAGES, CTAS, false, false>(a, grid, stream);
+  auto kern = a.base.softcap > 0.f ? kv4_decode_kernel<D, S, true> : kv4_decode_kernel<D, S, false>;
+  const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), S::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(kern, grid, S::NW * 32, S::kSmem, stream, a);
+}
+
+// Up to one segment per SM: CTAs that fill an SM, one piece each.  More
+// segments than that: small CTAs, several to an SM, which the hardware hands
+// out as others end, so that one's fixed costs pass behind another's loads; as
+// many pieces as run at once, or some more than there are segments, to cut the
+// long ones.  Batches beyond the plan's shared memory are not cut.
+template <int D, typename Big, typename Small>
+cudaError_t launch_d(Kv4DecodeArgs a, int sms, cudaStream_t stream) {
+  const int64_t segments = static_cast<int64_t>(a.base.batch) * a.base.Hkv;
+  const int big = std::min(sms, kKv4MaxExtra);
+  if (segments <= big && a.base.batch <= Big::kMaxBatch) {
+    a.whole = a.max_tiles <= whole_tiles(D);
+    return launch_t<D, Big>(a, big, stream);
+  }
+  const int count = static_cast<int>(segments);
+  a.whole = a.base.batch > Small::kMaxBatch || a.max_tiles <= kSmallWhole;
+  if (a.whole) return launch_t<D, Small>(a, count, stream);
+  const int extra = std::min(kKv4MaxExtra, std::max(Small::CTAS * sms - count, kKv4MaxExtra / 2));
+  return launch_t<D, Small>(a, count + extra, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, int head_dim, int sms, cudaStream_t stream) {
-  if (head_dim == 128) return launch_d<128, 16, 4, 1>(a, sms, stream);
-  if (head_dim == 256) return launch_d<256, 8, 4, 1>(a, sms, stream);
+  if (head_dim == 128)
+    return launch_d<128, Kv4Shape<128, 16, 4, 1, 1, 224>, Kv4Shape<128, 4, 4, 4, 4, 720>>(a, sms,
+                                                                                         stream);
+  if (head_dim == 256)
+    return launch_d<256, Kv4Shape<256, 8, 4, 1, 1, 224>, Kv4Shape<256, 2, 4, 4, 2, 720>>(a, sms,
+                                                                                        stream);
   return cudaErrorInvalidValue;
 }
 

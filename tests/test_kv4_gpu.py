@@ -358,7 +358,7 @@ def test_decode_same_bits_every_time_and_wherever():
     ws = workspace(c)
     for _ in range(3):
         assert torch.equal(decode(c, ws=ws), first)
-    assert not ws[:1024].any()                         # the counters
+    assert not ws[:2048].any()                         # the counters
     perm = torch.randperm(c["pool"].num_blocks, generator=torch.Generator().manual_seed(0))
     inv = torch.argsort(perm)
     moved = binding.Kv4Pool(c["pool"].k[perm.to(DEV)].contiguous(),
