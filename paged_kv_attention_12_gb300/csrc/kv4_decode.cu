@@ -6,16 +6,25 @@
 // arithmetic per byte is 3.6 times that of the bf16 decode: the design keeps
 // the conversion short and every other cost off the path.
 //
-// Work.  The split-K line of the bf16 decode (PieceIter: segments of
-// (request, KV head) cut into equal chunks, one per CTA), one persistent CTA
-// of NW warps per SM.  Warp w of a CTA takes tiles w, w + NW, ... of a piece
-// (a tile: 16 keys of one head, K and V).
+// Work.  A segment is one (request, KV head), a tile 16 keys of it (K and V).
+// Segments stream whole or are cut into pieces of equal length (theta_piece),
+// one piece per CTA; a CTA of NW warps gives each warp a run of the piece's
+// tiles and merges the warps' states in shared memory.  Few segments run on CTAs
+// that fill an SM (16 warps at D = 128, 8 at 256), more of them on CTAs of a
+// half or a quarter of that: uniform batches of 608 segments reach 4.4 TB/s
+// (1680 tokens, D = 128) to 5.4 TB/s (6720 tokens) that way.
 //
 // Loads.  Every warp streams its own tiles: cp.async, 16 bytes a lane, into
 // its own ring of STAGES tiles in shared memory, so no other warp is waited
-// for inside a piece; the next piece's first tiles are requested before the
-// current piece is merged.  (Streaming random 1152-byte units: 5.6 TB/s with
-// cp.async against 4.9 TB/s with one bulk copy per unit.)
+// for inside a piece.  Streaming random 1152-byte units: 5.6 TB/s with cp.async
+// against 4.9 TB/s with one bulk copy per unit.  Four tiles a warp in flight; five
+// or six were no faster (4 x 32..131 K keys 43.3, 44.5, 45.1 us).
+//
+// What bounds it: HBM.  With long segments a tile takes an SM 55 ns (D = 128)
+// or 110 ns (D = 256), 6.4 TB/s over the GPU, 94% of a plain copy, at 2.8 and
+// 2.3 of 4 instructions a cycle.  Around that lie about 4 us from the launch to
+// the first tiles, 1.5 us for the warps' merge and, where segments are cut, 3 us
+// for the merge through global memory.
 //
 // Arithmetic per tile and warp: S^T = K q^T and O^T += V^T P^T with m16n8k16
 // f16 MMAs (keys or channels on M, the G <= 8 query heads on N).  Codes go
@@ -51,7 +60,9 @@ namespace {
 // 8.8 / 8.5; D = 256, 640 tokens 8.4 / 9.0, 800 tokens 10.0 / 9.0.)
 constexpr int whole_tiles(int head_dim) { return head_dim == 128 ? 72 : 40; }
 // The same for the small CTAs of large batches.
-constexpr int kSmallWhole = 24;
+constexpr int kSmallWhole = 60;
+// Pieces beyond one for each segment, when the segments are more than run at once.
+constexpr int kMoreThan = 64;
 // Else the shortest piece, in tiles.
 constexpr int kMinPiece = 16;
 
@@ -815,44 +826,48 @@ __global__ void __launch_bounds__(S::NW * 32, S::CTAS)
 }
 
 template <int D, typename S>
-cudaError_t launch_t(Kv4DecodeArgs a, int grid, cudaStream_t stream) {
-  a.most_parts = grid / a.base.Hkv;
+cudaError_t launch_t(Kv4DecodeArgs a, int64_t grid, cudaStream_t stream) {
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  a.most_parts = static_cast<int>(grid / a.base.Hkv);
   a.even_share = static_cast<float>(a.base.Hkv) / grid;
   auto kern = a.base.softcap > 0.f ? kv4_decode_kernel<D, S, true> : kv4_decode_kernel<D, S, false>;
   const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), S::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(kern, grid, S::NW * 32, S::kSmem, stream, a);
+  return launch_overlapped(kern, static_cast<int>(grid), S::NW * 32, S::kSmem, stream, a);
 }
 
-// Up to one segment per SM: CTAs that fill an SM, one piece each.  More
-// segments than that: small CTAs, several to an SM, which the hardware hands
-// out as others end, so that one's fixed costs pass behind another's loads; as
-// many pieces as run at once, or some more than there are segments, to cut the
-// long ones.  Batches beyond the plan's shared memory are not cut.
-template <int D, typename Big, typename Small>
-cudaError_t launch_d(Kv4DecodeArgs a, int sms, cudaStream_t stream) {
+// Few segments: CTAs that fill an SM.  More segments than SMs: two or four
+// smaller CTAs to an SM, so that most segments stay whole and one CTA's fixed
+// costs pass behind another's loads; more than run at once: the hardware hands
+// the CTAs out as others end.  The pieces number at most the CTAs that run at
+// once, or some more than the segments, to cut the long ones.  Batches beyond
+// the plan's shared memory are not cut.
+template <int D, typename S>
+cudaError_t launch_s(Kv4DecodeArgs a, int64_t segments, int sms, int whole, cudaStream_t stream) {
+  a.whole = a.base.batch > S::kMaxBatch || a.max_tiles <= whole;
+  if (a.whole) return launch_t<D, S>(a, segments, stream);
+  const int64_t at_once = S::CTAS * sms;
+  const int64_t pieces = S::CTAS < 4 ? at_once : std::max(at_once, segments + kMoreThan);
+  return launch_t<D, S>(a, std::min<int64_t>(pieces, segments + kKv4MaxExtra), stream);
+}
+
+template <int D, typename Big, typename Mid, typename Small>
+cudaError_t launch_d(const Kv4DecodeArgs& a, int sms, cudaStream_t stream) {
   const int64_t segments = static_cast<int64_t>(a.base.batch) * a.base.Hkv;
-  const int big = std::min(sms, kKv4MaxExtra);
-  if (segments <= big && a.base.batch <= Big::kMaxBatch) {
-    a.whole = a.max_tiles <= whole_tiles(D);
-    return launch_t<D, Big>(a, big, stream);
-  }
-  const int count = static_cast<int>(segments);
-  a.whole = a.base.batch > Small::kMaxBatch || a.max_tiles <= kSmallWhole;
-  if (a.whole) return launch_t<D, Small>(a, count, stream);
-  const int extra = std::min(kKv4MaxExtra, std::max(Small::CTAS * sms - count, kKv4MaxExtra / 2));
-  return launch_t<D, Small>(a, count + extra, stream);
+  if (segments <= sms) return launch_s<D, Big>(a, segments, sms, whole_tiles(D), stream);
+  if (segments <= 2 * sms) return launch_s<D, Mid>(a, segments, sms, whole_tiles(D) / 2, stream);
+  return launch_s<D, Small>(a, segments, sms, kSmallWhole, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, int head_dim, int sms, cudaStream_t stream) {
   if (head_dim == 128)
-    return launch_d<128, Kv4Shape<128, 16, 4, 1, 1, 224>, Kv4Shape<128, 4, 4, 4, 4, 720>>(a, sms,
-                                                                                         stream);
+    return launch_d<128, Kv4Shape<128, 16, 4, 1, 1, 224>, Kv4Shape<128, 8, 4, 2, 4, 400>,
+                    Kv4Shape<128, 4, 4, 4, 4, 720>>(a, sms, stream);
   if (head_dim == 256)
-    return launch_d<256, Kv4Shape<256, 8, 4, 1, 1, 224>, Kv4Shape<256, 2, 4, 4, 2, 720>>(a, sms,
-                                                                                        stream);
+    return launch_d<256, Kv4Shape<256, 8, 4, 1, 1, 224>, Kv4Shape<256, 4, 4, 2, 4, 400>,
+                    Kv4Shape<256, 2, 4, 4, 2, 720>>(a, sms, stream);
   return cudaErrorInvalidValue;
 }
 
