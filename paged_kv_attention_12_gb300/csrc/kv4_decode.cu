@@ -43,8 +43,8 @@
 // share; it moves (and O is rescaled) only when a logit exceeds it by more
 // than kGrow, so most tiles need one vote instead of a maximum over the warp.
 // P = 2^(x - m + kShift) lies in (0, 2^15]: f16 (11 bits, the only rounding
-// of P), of use down to 2^-32 of the largest weight; the sums are fp32 over
-// the unrounded values.
+// of P), of use down to 2^-32 of the largest weight.  The weights' sums are
+// taken over the rounded values, in fp32 on the tensor cores.
 #include <algorithm>
 
 #include "decode_body.cuh"

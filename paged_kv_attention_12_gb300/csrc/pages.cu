@@ -18,7 +18,9 @@ constexpr int kCopyChunk = 32 * 16 * kCopyUnroll;  // bytes a warp copies per it
 
 // One warp per (pair, pool, 2 KB chunk of the block), the chunk's loads in
 // flight together.  The pairs come from src / dst, or, for a compaction, from
-// its list of moves (whose length only the device knows).
+// its list of moves (whose length only the device knows).  Bound by HBM: 12000
+// moves in four pools of 16 KB blocks, 1.57 GB, 242 us with 32 CTAs per SM
+// (258 with 8: the hardware evens the SMs out), 6.5 TB/s, 96% of a plain copy.
 __global__ void __launch_bounds__(256) copy_blocks_kernel(const __grid_constant__ CopyArgs a) {
   const int lane = threadIdx.x & 31;
   const long long gthread = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
@@ -113,7 +115,8 @@ __global__ void __launch_bounds__(256) ref_blocks_kernel(const RefArgs a) {
 // (the first kKeep steps of it in registers) writes the lists.  Every id is
 // read and written by its own warp only until the last phase, so
 // new_refcounts may be refcounts.  One CTA does without the cluster's barriers
-// and is taken while its registers hold all the ids (PLAN_US).
+// and is taken while its registers hold all the ids (one CTA / eight: 2048 ids
+// 3.7 / 4.8 us, 65536 ids 42 / 8.2 us, a launch in a stream of them).
 constexpr int kPlanWarps = 32;
 constexpr int kKeep = 8;
 constexpr int kPlanOne = kPlanWarps * 32 * kKeep;  // ids one CTA keeps in registers
@@ -145,6 +148,9 @@ __global__ void __launch_bounds__(kPlanWarps * 32) compact_plan_kernel(const Pla
   const int hi = static_cast<int>(min(first + per_warp, static_cast<long long>(a.num_blocks)));
   if (threadIdx.x == 0) moves_total = 0;
 
+  // a CTA's shared memory may be written by the others once it has started:
+  // arrive now, wait before the first such write
+  if constexpr (CTAS > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   // the first kKeep steps' counts stay in registers for the second pass
   int ref[kKeep];
   int count = 0;
@@ -162,6 +168,7 @@ __global__ void __launch_bounds__(kPlanWarps * 32) compact_plan_kernel(const Pla
   }
   if (lane == 0) warp_total[warp] = count;
   __syncthreads();
+  if constexpr (CTAS > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   if (warp == 0) {
     const int v = warp_total[lane];
     int incl = v;

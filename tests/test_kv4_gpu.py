@@ -47,6 +47,18 @@ def random_pool(nb, hkv, D, seed, ks=KS, vs=VS):
     return binding.Kv4Pool(out[0], out[1], ks, vs)
 
 
+def byte_pool(nb, hkv, D, seed, ks=KS, vs=VS):
+    """A full pool of random codes, with scales from 0.25 to 4: quick to make."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    out = []
+    for _ in range(2):
+        p = torch.randint(0, 256, (nb, hkv, D // 128, 1152), generator=g, device=DEV,
+                          dtype=torch.uint8)
+        p[..., 1024:] = p[..., 1024:] % 33 + 0x28
+        out.append(p)
+    return binding.Kv4Pool(out[0], out[1], ks, vs)
+
+
 # ---------------------------------------------------------------- write
 @pytest.mark.parametrize("D,hkv,T,wide", [(128, 1, 1, 0), (128, 3, 33, 5), (256, 2, 700, 0),
                                           (256, 8, 17, 3), (128, 4, 1025, 1)])
@@ -155,13 +167,13 @@ def test_expand_bad_ids():
 
 # ---------------------------------------------------------------- decode
 def make(lens, hq, hkv, D, *, seed=0, spare=5, qmag=1.0, scale=None, window=0, softcap=0.0,
-         poison=True):
+         poison=True, pool_of=random_pool):
     """A decode call over a random pool; with poison, slots behind a row's end
     hold NaN scales and so do unused blocks."""
     rng = np.random.default_rng(seed + 77)
     nbs = [-(-n // 16) for n in lens]
     nb = sum(nbs) + spare
-    pool = random_pool(nb, hkv, D, seed)
+    pool = pool_of(nb, hkv, D, seed)
     perm = rng.permutation(nb)
     width = max(nbs + [1]) + 1
     table = np.full((len(lens), width), -1, np.int64)
@@ -284,6 +296,28 @@ def test_decode_many_short_requests():
     check(c, decode(c))
 
 
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("B,hkv,lo,hi", [
+    (152, 1, 0, 900),      # as many segments as SMs
+    (153, 1, 0, 1500),     # one more: two CTAs to an SM
+    (60, 5, 700, 1400),    # 300 segments, some cut
+    (77, 4, 0, 1300),      # 308: four to an SM
+    (150, 8, 0, 700),      # 1200: more than run at once
+    (760, 1, 0, 1000),     # more requests than a plan holds
+    (40, 8, 1, 150)])      # short ones, whole
+def test_decode_batches_of_many_segments(D, B, hkv, lo, hi):
+    g = np.random.default_rng(B + hkv)
+    lens = g.integers(lo, hi, B)
+    lens[g.integers(0, B)] = 5 * hi                    # one long request among them
+    c = make(lens.tolist(), hkv, hkv, D, seed=B, pool_of=byte_pool, poison=False)
+    err = i32([0])
+    out = decode(c, err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    check(c, out)
+    assert torch.equal(decode(c), out)
+
+
 @pytest.mark.parametrize("scale,qmag", [(0.0, 1.0), (-0.1, 1.0), (1.0, 4.0), (1e-3, 1e4),
                                         (3e4, 1e-6)])
 def test_decode_scales_and_query_ranges(scale, qmag):
@@ -390,7 +424,7 @@ def test_one_workspace_for_calls_of_all_sizes():
     """Batches of other sizes and head dimensions in turn on one workspace: each
     gives the bits that it gives on a workspace of its own."""
     g = np.random.default_rng(4)
-    cases = [make(g.integers(0, most, b).tolist(), 8, 2, d, seed=b, spare=2)
+    cases = [make(g.integers(0, most, b).tolist(), 8, 2, d, seed=b, spare=2, pool_of=byte_pool)
              for b, d, most in ((2, 256, 5000), (70, 128, 400), (3, 128, 2500), (100, 256, 200),
                                 (9, 256, 1500))]
     want = [decode(c) for c in cases]
@@ -403,8 +437,9 @@ def test_one_workspace_for_calls_of_all_sizes():
 
 def test_rows_longer_than_max_seq_len():
     """max_seq_len is a promise; rows that break it are reported or right."""
-    for lens, promise in (([5000, 30], 64), (np.full(90, 300).tolist(), 64)):
-        c = make(lens, 8, 2, 128, seed=1)
+    for lens, promise in (([5000, 30], 64), ([12000, 30], 2000), ([900] * 90, 64),
+                          ([9000] * 2 + [100] * 100, 1500)):
+        c = make(lens, 8, 2, 128, seed=1, pool_of=byte_pool, poison=False)
         err = i32([0])
         out = decode(c, err=err, max_len=promise, ws=workspace(c))
         torch.cuda.synchronize()
