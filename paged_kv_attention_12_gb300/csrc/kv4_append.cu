@@ -136,7 +136,7 @@ cudaError_t launch_kv4_expand(const Kv4ExpandArgs& a, int sm_count, cudaStream_t
   if (a.n == 0) return cudaSuccess;
   const long long warps =
       2LL * a.n * a.Hkv * (a.head_dim / kUnitChannels);
-  kv4_expand_kernel<<<grid_for((warps + 7) / 8, sm_count, 8), 256, 0, stream>>>(a);
+  kv4_expand_kernel<<<grid_for((warps + 7) / 8, sm_count, 64), 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -18,11 +18,11 @@
 // its own ring of STAGES tiles in shared memory, so no other warp is waited
 // for inside a piece.  Streaming random 1152-byte units: 5.6 TB/s with cp.async
 // against 4.9 TB/s with one bulk copy per unit.  Four tiles a warp in flight; five
-// or six were no faster (4 x 32..131 K keys 43.3, 44.5, 45.1 us).
+// or six were slower (4 x 32..131 K keys: 43.3, 44.5, 45.1 us).
 //
 // What bounds it: HBM.  With long segments a tile takes an SM 55 ns (D = 128)
-// or 110 ns (D = 256), 6.4 TB/s over the GPU, 94% of a plain copy, at 2.8 and
-// 2.3 of 4 instructions a cycle.  Around that lie about 4 us from the launch to
+// or 110 ns (D = 256), 6.4 TB/s over the GPU, 94% of a plain copy, at 300 and
+// 490 instructions and 2.8 and 2.3 of 4 a cycle.  Around that lie about 4 us from the launch to
 // the first tiles, 1.5 us for the warps' merge and, where segments are cut, 3 us
 // for the merge through global memory.
 //
@@ -75,6 +75,16 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same from zero.
+__device__ __forceinline__ void mma_f16_16816_first(float (&d)[4], uint32_t a0, uint32_t a1,
+                                                    uint32_t a2, uint32_t a3, uint32_t b0,
+                                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -142,17 +152,21 @@ struct Kv4Shape {
 
 // The four A registers of K's k-step S (0..7) of a unit: words of row g and
 // row g + 8, scaled.
-template <int S>
+template <int S, bool FIRST>
 __device__ __forceinline__ void k_step(float (&acc)[4], const uint4& r0, const uint4& r1,
                                        const uint32_t (&s0)[2], const uint32_t (&s1)[2],
                                        uint32_t b0, uint32_t b1) {
   constexpr int B = (S & 1) * 2;
   const uint32_t w0 = (S / 2 == 0) ? r0.x : (S / 2 == 1) ? r0.y : (S / 2 == 2) ? r0.z : r0.w;
   const uint32_t w1 = (S / 2 == 0) ? r1.x : (S / 2 == 1) ? r1.y : (S / 2 == 2) ? r1.z : r1.w;
-  mma_f16_16816(acc, f16x2_mul(e2m1x2_to_f16x2<B>(w0), s0[S / 4]),
-                f16x2_mul(e2m1x2_to_f16x2<B>(w1), s1[S / 4]),
-                f16x2_mul(e2m1x2_to_f16x2<B + 1>(w0), s0[S / 4]),
-                f16x2_mul(e2m1x2_to_f16x2<B + 1>(w1), s1[S / 4]), b0, b1);
+  const uint32_t a0 = f16x2_mul(e2m1x2_to_f16x2<B>(w0), s0[S / 4]);
+  const uint32_t a1 = f16x2_mul(e2m1x2_to_f16x2<B>(w1), s1[S / 4]);
+  const uint32_t a2 = f16x2_mul(e2m1x2_to_f16x2<B + 1>(w0), s0[S / 4]);
+  const uint32_t a3 = f16x2_mul(e2m1x2_to_f16x2<B + 1>(w1), s1[S / 4]);
+  if constexpr (FIRST)
+    mma_f16_16816_first(acc, a0, a1, a2, a3, b0, b1);
+  else
+    mma_f16_16816(acc, a0, a1, a2, a3, b0, b1);
 }
 
 // M-tile of byte B of a V word: channels 2B and 2B + 1 of the word.
@@ -172,13 +186,10 @@ __device__ __forceinline__ void v_step(float (&o)[4], uint32_t lo0, uint32_t hi0
 template <int D, int NT>
 __device__ __forceinline__ void kv4_scores(const uint8_t* const (&tile)[NT], const uint2* bq,
                                            float (&x)[NT][4], int lane) {
-  float s[NT][2][4];
+  constexpr int UNITS = D / kUnitChannels;
+  float s[UNITS][NT][4];  // one chain of MMAs per unit and tile
 #pragma unroll
-  for (int k = 0; k < NT; ++k)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s[k][0][i] = s[k][1][i] = 0.f;
-#pragma unroll
-  for (int u = 0; u < D / kUnitChannels; ++u) {
+  for (int u = 0; u < UNITS; ++u) {
     uint4 r0[NT], r1[NT];
     uint32_t s0[NT][2], s1[NT][2];
 #pragma unroll
@@ -201,7 +212,7 @@ __device__ __forceinline__ void kv4_scores(const uint8_t* const (&tile)[NT], con
   {                                                                                     \
     const uint2 b = q[(K_) * 32];                                                       \
     _Pragma("unroll") for (int k = 0; k < NT; ++k)                                      \
-        k_step<K_>(s[k][(K_) & 1], r0[k], r1[k], s0[k], s1[k], b.x, b.y);               \
+        k_step<K_, (K_) == 0>(s[u][k], r0[k], r1[k], s0[k], s1[k], b.x, b.y);           \
   }
     PKA_KV4_STEP(0)
     PKA_KV4_STEP(1)
@@ -216,7 +227,7 @@ __device__ __forceinline__ void kv4_scores(const uint8_t* const (&tile)[NT], con
 #pragma unroll
   for (int k = 0; k < NT; ++k)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[k][i] = s[k][0][i] + s[k][1][i];
+    for (int i = 0; i < 4; ++i) x[k][i] = UNITS == 1 ? s[0][k][i] : s[0][k][i] + s[UNITS - 1][k][i];
 }
 
 // O^T += V^T P^T of one tile.  The lane holds group g of every unit for keys
