@@ -449,7 +449,9 @@ int paged_kv4_expand(const pka_kv4_pool* kv, const pka_kv_pool* dst, const int32
  * zeros and ORs PKA_DEVERR_BAD_TABLE into params->err.
  * One launch: short segments (request, KV head) stream whole; longer ones are
  * cut into pieces, at most 30 each, whose fp32 partials the last piece to
- * arrive merges in piece order (the same bits every time).
+ * arrive merges in a fixed order (the same bits every time).  max_seq_len
+ * sizes the pieces; rows that are longer all the same are computed, more
+ * slowly.
  * workspace: at least paged_kv4_decode_attn_ws_bytes() bytes, 16-byte
  * aligned: 2048 bytes of arrival counters, then the partials.  The first 2048
  * bytes must be zero before the first call and are left zero by every call, so

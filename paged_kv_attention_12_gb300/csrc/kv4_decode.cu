@@ -659,8 +659,6 @@ __global__ void __launch_bounds__(S::NW * 32, S::CTAS)
   pc = *plan;  // not kept in registers over the loop
   const bool split = pc.npieces > 1;
   const size_t head0 = static_cast<size_t>(pc.qrow) * a.Hq + pc.kvh * G;
-  // (a row longer than max_seq_len may have more pieces than slots: reported)
-  const bool has_slot = pc.slot < a.num_splits;
   // lane (g, t) takes warps g and g + 8
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -680,7 +678,7 @@ __global__ void __launch_bounds__(S::NW * 32, S::CTAS)
                                      __fdividef(ka.v_scale, den);
     // P carries a factor 2^kShift, the same in every piece; a NaN sum keeps
     // its weight, so that the merge of the pieces passes it on
-    if (split && has_slot && warp == 0 && g == 0 && 2 * t + j < G)
+    if (split && warp == 0 && g == 0 && 2 * t + j < G)
       __stcg(a.partial_lse + (head0 + 2 * t + j) * a.num_splits + pc.slot,
              den == 0.f ? -INFINITY : (isnan(den) ? M : M + log2f(den)) * kLn2);
 #pragma unroll
@@ -723,28 +721,24 @@ __global__ void __launch_bounds__(S::NW * 32, S::CTAS)
       y.z += x.z;
       y.w += x.w;
     }
-    if (split && has_slot)
+    if (split)
       __stcg(reinterpret_cast<float4*>(a.partial_o +
                                        ((head0 + h) * a.num_splits + pc.slot) * D + d0),
              y);
-    else if (!split)
+    else
       *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + (head0 + h) * D + d0) =
           make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
   }
   if (split) {
     // ---- the piece that arrives last at its segment merges the partials
-    const int np = min(pc.npieces, a.num_splits);
+    const int np = pc.npieces;
     __syncthreads();
     if (threadIdx.x == 0) {
-      if (pc.npieces > a.num_splits) report(a.err, PKA_DEVERR_SEQ_LEN);
-      int last = 0;
-      if (has_slot) {
-        // the segment's counter: the pieces beyond one each of the segments
-        // before it, a number that every cut segment raises
-        int32_t* counter = a.seg_counters + (cta - pc.slot) - (pc.b * a.Hkv + pc.kvh);
-        last = atomic_add_acq_rel(counter, 1) == np - 1;
-        if (last) *counter = 0;
-      }
+      // the segment's counter: the pieces beyond one each of the segments
+      // before it, a number that every cut segment raises
+      int32_t* counter = a.seg_counters + (cta - pc.slot) - (pc.b * a.Hkv + pc.kvh);
+      const bool last = atomic_add_acq_rel(counter, 1) == np - 1;
+      if (last) *counter = 0;
       *flag = last;
     }
     __syncthreads();
