@@ -26,32 +26,6 @@
 
 namespace pka {
 
-// Launches that may start while their predecessor in the stream drains: the
-// kernel waits for it (its writes included) before it touches memory, so only
-// launch latency overlaps (about 0.6 us a call in a stream of decodes).
-__device__ __forceinline__ void launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_predecessor() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
-template <typename Args>
-cudaError_t launch_overlapped(void (*kernel)(Args), int grid, int threads, int smem,
-                              cudaStream_t stream, const Args& args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args);
-}
-
 constexpr int kUnitChannels = 128;
 constexpr int kUnitCodes = 1024;
 constexpr int kUnitBytes = 1152;

@@ -4,6 +4,7 @@
 // bytes they move: a value is 2 bytes in bf16 and 0.5625 in the pool.
 #include "kv4.cuh"
 #include "kernels.h"
+#include "overlap.cuh"
 
 namespace pka {
 
@@ -13,11 +14,13 @@ namespace {
 // 32 bytes of one token's group of 16 channels and writes 8 code bytes and a
 // scale.  Tokens that follow one another in a block make whole 32-byte sectors
 // of the stores: a K unit holds a token's groups side by side, a V unit a
-// group's tokens.  8192 tokens x 4 heads x 128: 6.6 us for 21.5 MB (3.2 us of
+// group's tokens.  8192 tokens x 4 heads x 128: 6.4 us for 21.5 MB (3.2 us of
 // HBM); bound by the arithmetic, about 200 instructions a group (a division per
 // value made it 9.8 us, 8-byte V stores of one token 10.5 us).
 __global__ void __launch_bounds__(256, 4)
     kv4_append_kernel(const __grid_constant__ Kv4AppendArgs a) {
+  launch_dependents();
+  wait_predecessor();
   const int lane = threadIdx.x & 31;
   const int units = a.head_dim / kUnitChannels;
   const int per_quad = 2 * a.Hkv * units;
@@ -128,14 +131,15 @@ cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int sm_count, cudaStream_t
   if (a.T == 0) return cudaSuccess;
   const long long warps =
       (static_cast<long long>(a.T) + 3) / 4 * 2 * a.Hkv * (a.head_dim / kUnitChannels);
-  kv4_append_kernel<<<grid_for((warps + 7) / 8, sm_count, 16), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(kv4_append_kernel, grid_for((warps + 7) / 8, sm_count, 16), 256, 0,
+                           stream, a);
 }
 
 cudaError_t launch_kv4_expand(const Kv4ExpandArgs& a, int sm_count, cudaStream_t stream) {
   if (a.n == 0) return cudaSuccess;
   const long long warps =
       2LL * a.n * a.Hkv * (a.head_dim / kUnitChannels);
+  // a plain launch: overlapped, 128 blocks took 3.1 us instead of 2.3
   kv4_expand_kernel<<<grid_for((warps + 7) / 8, sm_count, 64), 256, 0, stream>>>(a);
   return cudaGetLastError();
 }

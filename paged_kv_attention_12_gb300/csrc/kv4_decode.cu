@@ -49,6 +49,7 @@
 
 #include "decode_body.cuh"
 #include "kv4.cuh"
+#include "overlap.cuh"
 
 namespace pka {
 

@@ -5,6 +5,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "overlap.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -19,9 +20,11 @@ constexpr int kCopyChunk = 32 * 16 * kCopyUnroll;  // bytes a warp copies per it
 // One warp per (pair, pool, 2 KB chunk of the block), the chunk's loads in
 // flight together.  The pairs come from src / dst, or, for a compaction, from
 // its list of moves (whose length only the device knows).  Bound by HBM: 12000
-// moves in four pools of 16 KB blocks, 1.57 GB, 242 us with 32 CTAs per SM
+// moves in four pools of 16 KB blocks, 1.57 GB, 240 us with 32 CTAs per SM
 // (258 with 8: the hardware evens the SMs out), 6.5 TB/s, 96% of a plain copy.
 __global__ void __launch_bounds__(256) copy_blocks_kernel(const __grid_constant__ CopyArgs a) {
+  launch_dependents();
+  wait_predecessor();
   const int lane = threadIdx.x & 31;
   const long long gthread = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
   // the tables of a compaction: entries of a row's used part follow their
@@ -80,6 +83,8 @@ __global__ void __launch_bounds__(256) copy_blocks_kernel(const __grid_constant_
 // One thread per table entry.  Integer atomics: the counts do not depend on
 // their order.
 __global__ void __launch_bounds__(256) ref_blocks_kernel(const RefArgs a) {
+  launch_dependents();
+  wait_predecessor();
   const long long entries = static_cast<long long>(a.batch) * a.max_blocks;
   for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < entries;
        i += static_cast<long long>(gridDim.x) * blockDim.x) {
@@ -122,7 +127,7 @@ constexpr int kKeep = 8;
 constexpr int kPlanOne = kPlanWarps * 32 * kKeep;  // ids one CTA keeps in registers
 
 template <int CTAS>
-__global__ void __launch_bounds__(kPlanWarps * 32) compact_plan_kernel(const PlanArgs a) {
+__global__ void __launch_bounds__(kPlanWarps * 32, 1) compact_plan_kernel(const PlanArgs a) {
   __shared__ int cta_total[CTAS];  // every CTA's live ids (written by each CTA everywhere)
   __shared__ int warp_total[kPlanWarps];
   __shared__ int moves_total;      // CTA 0's is the cluster's
@@ -146,6 +151,8 @@ __global__ void __launch_bounds__(kPlanWarps * 32) compact_plan_kernel(const Pla
   const long long first = static_cast<long long>(rank * kPlanWarps + warp) * per_warp;
   const int lo = static_cast<int>(min(first, static_cast<long long>(a.num_blocks)));
   const int hi = static_cast<int>(min(first + per_warp, static_cast<long long>(a.num_blocks)));
+  launch_dependents();
+  wait_predecessor();
   if (threadIdx.x == 0) moves_total = 0;
 
   // a CTA's shared memory may be written by the others once it has started:
@@ -255,33 +262,21 @@ cudaError_t launch_copy_blocks(const CopyArgs& a, int max_pairs, int sm_count,
     const long long tw = (static_cast<long long>(a.batch) * a.max_blocks + 31) / 32;
     if (tw > warps) warps = tw;
   }
-  copy_blocks_kernel<<<copy_grid(warps, sm_count), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(copy_blocks_kernel, copy_grid(warps, sm_count), 256, 0, stream, a);
 }
 
 cudaError_t launch_ref_blocks(const RefArgs& a, int sm_count, cudaStream_t stream) {
   const long long entries = static_cast<long long>(a.batch) * a.max_blocks;
-  ref_blocks_kernel<<<copy_grid((entries + 31) / 32, sm_count), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(ref_blocks_kernel, copy_grid((entries + 31) / 32, sm_count), 256, 0,
+                           stream, a);
 }
 
 cudaError_t launch_compact_plan(const PlanArgs& a, cudaStream_t stream) {
-  if (a.num_blocks <= kPlanOne) {
-    compact_plan_kernel<1><<<1, kPlanWarps * 32, 0, stream>>>(a);
-    return cudaGetLastError();
-  }
   constexpr int kCtas = 8;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kCtas);
-  cfg.blockDim = dim3(kPlanWarps * 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = kCtas;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, compact_plan_kernel<kCtas>, a);
+  return a.num_blocks <= kPlanOne
+             ? launch_overlapped(compact_plan_kernel<1>, 1, kPlanWarps * 32, 0, stream, a)
+             : launch_overlapped(compact_plan_kernel<kCtas>, kCtas, kPlanWarps * 32, 0, stream, a,
+                                 kCtas);
 }
 
 }  // namespace pka
