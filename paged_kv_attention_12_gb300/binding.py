@@ -357,9 +357,9 @@ def paged_kv_append_rope(q, k_new, v_new, k_pool, v_pool, slot_mapping, position
     rd = d if rotary_dim is None else int(rotary_dim)
     st = lib().paged_kv_append_rope(
         _ptr(q), k_new.data_ptr(), v_new.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), nb,
-        q.shape[1] if q is not None else 0, hkv, bs, d, slot_mapping.data_ptr(), _ptr(positions),
-        slot_mapping.shape[0], _ptr(q_norm_weight), _ptr(k_norm_weight), 1 if v_norm else 0,
-        float(eps), float(rope_theta), rd, _ptr(err), _stream(stream))
+        q.shape[1] if q is not None else 0, hkv, bs, d, slot_mapping.data_ptr(),
+        _ptr(positions), slot_mapping.shape[0], _ptr(q_norm_weight), _ptr(k_norm_weight),
+        1 if v_norm else 0, float(eps), float(rope_theta), rd, _ptr(err), _stream(stream))
     _check("paged_kv_append_rope", st)
 
 
@@ -560,7 +560,7 @@ def paged_kv_ref_blocks(block_tables, seq_lens, refcounts, delta: int, err=None,
 
 
 def _pool_list(pools):
-    """The pools' device pointers as a C array, their blocks and bytes per block."""
+    """The pools' device pointers as a C array, their blocks, bytes per block and device."""
     first = pools[0]
     dev, shape, dtype = _cuda_device(first, "pools"), first.shape, first.dtype
     for p in pools:
@@ -576,6 +576,8 @@ def paged_kv_copy_blocks(pools, src, dst, err=None, stream=None):
     (tensors [num_blocks][...] of one shape and type: K and V of every layer).
     The destinations must be distinct and none of them a source."""
     import torch
+    if not pools:
+        return
     ptrs, n, nbytes, dev = _pool_list(pools)
     pairs = src.shape[0]
     _tensor(src, "src", torch.int32, dev, (pairs,))
@@ -595,9 +597,11 @@ def paged_kv_compact(pools, refcounts, block_tables, seq_lens, new_refcounts, ne
     """Move the live blocks (``refcounts`` > 0) of every pool to ids 0, 1, ...
     and give the new counts, tables, the map old id -> new id and the moves
     (int32 [2 + num_blocks]: their number, the live blocks, then pairs).
-    ``new_refcounts`` and ``new_tables`` may be the old ones."""
+    ``new_refcounts`` and ``new_tables`` may be the old ones.  Without pools
+    only the plan and the tables are worked out."""
     import torch
-    ptrs, n, nbytes, dev = _pool_list(pools)
+    ptrs, n, nbytes, dev = _pool_list(pools) if pools else \
+        (None, refcounts.shape[0], 0, _cuda_device(refcounts, "refcounts"))
     i32, B, width = torch.int32, seq_lens.shape[0], block_tables.shape[-1]
     _tensor(refcounts, "refcounts", i32, dev, (n,))
     _tensor(new_refcounts, "new_refcounts", i32, dev, (n,))
@@ -611,7 +615,7 @@ def paged_kv_compact(pools, refcounts, block_tables, seq_lens, new_refcounts, ne
             return paged_kv_compact(pools, refcounts, block_tables, seq_lens, new_refcounts,
                                     new_tables, remap, moves, err, stream)
     st = lib().paged_kv_compact(
-        ptrs, len(ptrs), n, nbytes, refcounts.data_ptr(), new_refcounts.data_ptr(),
+        ptrs, len(pools), n, nbytes, refcounts.data_ptr(), new_refcounts.data_ptr(),
         block_tables.data_ptr(), new_tables.data_ptr(), width, seq_lens.data_ptr(), B,
         remap.data_ptr(), moves.data_ptr(), None if err is None else _err(err, dev),
         _raw_stream(dev, stream))

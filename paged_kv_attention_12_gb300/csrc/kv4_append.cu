@@ -37,11 +37,11 @@ __global__ void __launch_bounds__(256, 4)
     if (t >= a.T) continue;
     const bool is_v = in >= a.Hkv * units;
     const int hu = is_v ? in - a.Hkv * units : in;  // head * units + unit
-    const int s = __ldg(a.slot_mapping + t);
+    const int s = a.slot_mapping[t];
     const uint4* src = reinterpret_cast<const uint4*>(
         (is_v ? a.v_new + t * a.v_stride : a.k_new + t * a.k_stride) + hu * kUnitChannels +
         g8 * 16);
-    const uint4 in0 = __ldg(src), in1 = __ldg(src + 1);
+    const uint4 in0 = src[0], in1 = src[1];
     if (s < 0) continue;
     const int blk = s / kBlockSize, tok = s % kBlockSize;
     if (blk >= a.num_blocks) {

@@ -575,8 +575,8 @@ __global__ void __launch_bounds__(S::NW * 32, S::CTAS)
     uint32_t top2 = 0;
 #pragma unroll
     for (int i = 0; i < UNITS * 4; ++i) {
-      raw[i] = (g < G) ? __ldg(reinterpret_cast<const uint4*>(
-                             qp + (i >> 2) * kUnitChannels + (i & 3) * 8))
+      raw[i] = (g < G) ? *reinterpret_cast<const uint4*>(
+                             qp + (i >> 2) * kUnitChannels + (i & 3) * 8)
                        : make_uint4(0u, 0u, 0u, 0u);
       top2 = __vmaxu2(__vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu),
                       __vmaxu2(__vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu), top2));

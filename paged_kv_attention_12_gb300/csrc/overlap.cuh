@@ -1,7 +1,9 @@
 // Launches that may start while their predecessor in the stream drains
 // (programmatic dependent launch): the kernel waits for it, its writes
 // included, before it touches memory, so only the launch latency overlaps:
-// 0.4 to 0.7 us a call in a stream of them.
+// 0.4 to 0.7 us a call in a stream of them.  Such a kernel may not read through
+// the non-coherent path (ld.global.nc): what the predecessor writes changes
+// during its life.
 #pragma once
 
 #include <cuda_runtime.h>

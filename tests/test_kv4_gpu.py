@@ -476,6 +476,64 @@ def test_offsets_past_32_bits():
 
 
 # ---------------------------------------------------------------- together
+def test_a_stream_of_steps_sees_its_own_writes():
+    """Decode steps in a row without a wait, each with lengths, slots, rows and
+    queries that the kernels right before it wrote: the same bits as step by
+    step with a wait between the kernels, eagerly and in a replayed graph."""
+    D, hkv, Hq, B, steps = 128, 2, 8, 3, 24
+    ks, vs = (torch.stack([rows((B, hkv, D), 100 * i + j) for i in range(steps)])
+              for j in (1, 2))
+    qs = torch.stack([rows((B, Hq, D), 100 * i + 3) for i in range(steps)])
+    table = i32(np.arange(B * 4).reshape(B, 4))
+    pool = binding.Kv4Pool.zeros(B * 4, hkv, D, KS, VS, device=DEV)
+    start, first = i32([5, 0, 14]), table[:, 0] * 16
+    lens, slots, at = start.clone(), start + first, torch.zeros(1, dtype=torch.int64, device=DEV)
+    k, v, q = torch.zeros_like(ks[0]), torch.zeros_like(ks[0]), torch.zeros_like(qs[0])
+    out = torch.zeros((steps, B, Hq, D), dtype=torch.bfloat16, device=DEV)
+    nbytes = binding.paged_kv4_decode_attn_ws_bytes(B, Hq, hkv, D, 64)
+    ws = torch.zeros(nbytes, dtype=torch.uint8, device=DEV)
+
+    def reset():
+        pool.k.zero_()
+        pool.v.zero_()
+        lens.copy_(start)
+        slots.copy_(start + first)
+        at.zero_()
+        out.zero_()
+        torch.cuda.synchronize()
+
+    def run(wait):
+        for i in range(steps):
+            for src, dst in ((ks, k), (vs, v), (qs, q)):
+                torch.index_select(src, 0, at, out=dst.unsqueeze(0))
+                wait()
+            binding.paged_kv4_append(k, v, pool, slots)
+            wait()
+            lens.add_(1)
+            wait()
+            binding.paged_kv4_decode_attn_ws(q, out[i], pool, table, lens, 64, ws, scale=0.1)
+            wait()
+            slots.add_(1)
+            at.add_(1)
+            wait()
+
+    reset()
+    run(torch.cuda.synchronize)
+    want = out.clone()
+    assert torch.isfinite(want).all() and want[-1].any()
+    reset()
+    run(lambda: None)
+    assert torch.equal(out, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(lambda: None)
+    for _ in range(2):
+        reset()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
 def test_prompt_decode_fork_and_compact_together():
     """A prompt written to a 4-bit cache and attended by the prefill kernel over
     its expanded blocks, decoded, forked with its last block copied, the parent

@@ -153,3 +153,80 @@ def test_plan_alone():
                             None, s)
     torch.cuda.synchronize()
     assert st == 0 and nt.tolist() == [[0, 39, 40]]
+
+
+def test_no_pools_in_python():
+    """The binding with an empty list: a copy does nothing, a compaction plans."""
+    n = 70
+    refs = torch.zeros(n, dtype=torch.int32, device=DEV)
+    refs[50:] = 2
+    t, lens = i32([[69, 50, -1]]), i32([20])
+    nr, nt, rm = torch.zeros_like(refs), torch.zeros_like(t), torch.zeros_like(refs)
+    mv = torch.zeros(n + 2, dtype=torch.int32, device=DEV)
+    binding.paged_kv_copy_blocks([], i32([0]), i32([1]))
+    binding.paged_kv_compact([], refs, t, lens, nr, nt, rm, mv)
+    moves, k, remap, counts, tables = oracle.compact(refs.tolist(), t.tolist(), [20])
+    assert mv[:2].tolist() == [len(moves), k] == [20, 20]
+    assert np.array_equal(rm.cpu().numpy(), remap) and np.array_equal(nr.cpu().numpy(), counts)
+    assert nt.tolist() == tables.tolist()
+
+
+def test_pools_past_32_bits():
+    """Blocks beyond 4 GiB of a pool are copied and moved where they are."""
+    nbytes = 1 << 20
+    n = 4 * 1024 + 24
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("needs 8 GiB of free device memory")
+    pool = torch.zeros((n, nbytes), dtype=torch.uint8, device=DEV)
+    pool[n - 1] = 7
+    pool[3] = 5
+    binding.paged_kv_copy_blocks([pool], i32([n - 1, 3]), i32([n - 9, n - 2]))
+    assert (pool[n - 9] == 7).all() and (pool[n - 2] == 5).all() and not pool[n - 8:n - 2].any()
+    refs = torch.zeros(n, dtype=torch.int32, device=DEV)
+    refs[[n - 9, n - 2]] = 1
+    nr, rm = torch.zeros_like(refs), torch.zeros_like(refs)
+    mv = torch.zeros(n + 2, dtype=torch.int32, device=DEV)
+    none = torch.zeros((0, 1), dtype=torch.int32, device=DEV)
+    binding.paged_kv_compact([pool], refs, none, i32([]), nr, none, rm, mv)
+    assert mv[:6].tolist() == [2, 2, n - 2, 0, n - 9, 1]
+    assert (pool[0] == 5).all() and (pool[1] == 7).all() and not pool[2].any()
+
+
+def test_captured_beside_another_stream():
+    """A graph in which the operations follow events of another stream and
+    kernels of other programs: every replay sees what they wrote before it."""
+    n, B = 500, 3
+    pool = torch.zeros((n, 64), dtype=torch.int32, device=DEV)
+    base = torch.arange(n, dtype=torch.int32, device=DEV)[:, None].expand(n, 64)
+    step, refs = i32([0]), torch.zeros(n, dtype=torch.int32, device=DEV)
+    t, lens = i32(np.arange(B * 4).reshape(B, 4) * 40 + 20), i32([64, 0, 50])
+    nr, nt, rm = torch.zeros_like(refs), torch.zeros_like(t), torch.zeros_like(refs)
+    mv, err = torch.zeros(n + 2, dtype=torch.int32, device=DEV), i32([0])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        step.add_(1)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            torch.add(base, step, out=pool)
+            binding.paged_kv_copy_blocks([pool], t[0, :1].contiguous(), t[1, :1].contiguous())
+        refs.zero_()
+        binding.paged_kv_ref_blocks(t, lens, refs, 1, err)
+        main.wait_stream(side)
+        binding.paged_kv_compact([pool], refs, t, lens, nr, nt, rm, mv, err)
+        binding.paged_kv_ref_blocks(nt, lens, nr, -1, err)
+    for k in range(1, 5):
+        graph.replay()
+        torch.cuda.synchronize()
+        ids = t.tolist()
+        live = sorted(ids[0] + ids[2])
+        holes = [i for i in range(8) if i not in live]
+        where = {i: i for i in live}
+        where.update(zip(sorted(live)[::-1], holes))
+        assert err.item() == 0 and not nr.any() and mv[:2].tolist() == [len(holes), 8]
+        assert nt.tolist() == [[where[i] for i in ids[0]], ids[1], [where[i] for i in ids[2]]]
+        for i in live:
+            assert (pool[where[i]] == i + k).all()
+        assert (pool[ids[1][0]] == ids[0][0] + k).all()
