@@ -109,6 +109,18 @@ __device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float (&q)[8]) {
   return r;
 }
 
+// v0 / step and v1 / step from the reciprocal y of step: q = v y, then
+// q + (v - q step) y, two lanes an instruction.
+__device__ __forceinline__ void markstein_x2(float v0, float v1, float y, float step, float& q0,
+                                             float& q1) {
+  asm("{\n\t.reg .b64 v, y, s, q, r;\n\t"
+      "mov.b64 v, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 s, {%5, %5};\n\t"
+      "mul.rn.f32x2 q, v, y;\n\tfma.rn.f32x2 r, q, s, v;\n\tfma.rn.f32x2 q, r, y, q;\n\t"
+      "mov.b64 {%0, %1}, q;\n\t}"
+      : "=f"(q0), "=f"(q1)
+      : "f"(v0), "f"(v1), "f"(y), "f"(-step));
+}
+
 // A group of 16 bf16 values -> 8 code bytes and the scale byte.  s6 = 6 * pool
 // scale, rounded to fp32.
 __device__ __forceinline__ uint2 quantise_group(const uint4& in0, const uint4& in1,
@@ -143,14 +155,11 @@ __device__ __forceinline__ uint2 quantise_group(const uint4& in0, const uint4& i
     float q[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float v[2];
-      bf16x2_to_f32(in[h * 4 + i], v[0], v[1]);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float q0 = __fmul_rn(v[j], y);
-        // (-0 stays -0)
-        q[2 * i + j] = copysignf(__fmaf_rn(__fmaf_rn(-q0, step, v[j]), y, q0), v[j]);
-      }
+      float v0, v1, q0, q1;
+      bf16x2_to_f32(in[h * 4 + i], v0, v1);
+      markstein_x2(v0, v1, y, step, q0, q1);
+      q[2 * i] = copysignf(q0, v0);  // (-0 stays -0)
+      q[2 * i + 1] = copysignf(q1, v1);
     }
     if (!plain) {
 #pragma unroll 1

@@ -2,6 +2,8 @@
 //
 // The format and its rounding are in kv4.cuh.  Both kernels are bound by the
 // bytes they move: a value is 2 bytes in bf16 and 0.5625 in the pool.
+#include <algorithm>
+
 #include "kv4.cuh"
 #include "kernels.h"
 #include "overlap.cuh"
@@ -10,52 +12,64 @@ namespace pka {
 
 namespace {
 
-// One warp per four tokens and 128 channels of a head, K or V; a lane takes the
-// 32 bytes of one token's group of 16 channels and writes 8 code bytes and a
-// scale.  Tokens that follow one another in a block make whole 32-byte sectors
-// of the stores: a K unit holds a token's groups side by side, a V unit a
-// group's tokens.  8192 tokens x 4 heads x 128: 6.4 us for 21.5 MB (3.2 us of
-// HBM); bound by the arithmetic, about 200 instructions a group (a division per
-// value made it 9.8 us, 8-byte V stores of one token 10.5 us).
-__global__ void __launch_bounds__(256, 4)
+// One warp per four tokens and 128 channels of a head, of K or V or (BOTH) of
+// each; a lane takes the 32 bytes of one token's group of 16 channels and writes
+// 8 code bytes and a scale.  Tokens that follow one another in a block make
+// whole 32-byte sectors of the stores: a K unit holds a token's groups side by
+// side, a V unit a group's tokens.  Grid: y the head and 128 channels (and K or
+// V), x the tokens, so that nothing is divided by sizes.  Bound by arithmetic and
+// by the time a warp waits for its rows: 8192 tokens x 4 heads x 128, 21.5 MB,
+// 4.9 us, 3.2 us of it HBM (K and V on warps of their own 5.5 us, unpaired
+// arithmetic 5.6, four CTAs per SM 6.0, a warp index divided by the heads 6.4, a
+// division per value 9.8).  32 tokens: 1.8 us, 2.2 with BOTH.
+template <bool BOTH>
+__global__ void __launch_bounds__(256, 5)
     kv4_append_kernel(const __grid_constant__ Kv4AppendArgs a) {
   launch_dependents();
   wait_predecessor();
+  constexpr int SIDES = BOTH ? 2 : 1;
   const int lane = threadIdx.x & 31;
-  const int units = a.head_dim / kUnitChannels;
-  const int per_quad = 2 * a.Hkv * units;
+  const int per = a.Hkv * (a.head_dim / kUnitChannels);  // units of a block
   const int g8 = lane & 7;
   const unsigned quads = (static_cast<unsigned>(a.T) + 3) / 4;
-  const unsigned long long total = static_cast<unsigned long long>(quads) * per_quad;
-  const unsigned wstride = gridDim.x * (blockDim.x / 32);
-  for (unsigned long long w = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; w < total;
-       w += wstride) {
-    const unsigned quad = total >> 32 ? static_cast<unsigned>(w / per_quad)
-                                      : static_cast<unsigned>(w) / per_quad;
-    const int in = static_cast<int>(w - static_cast<unsigned long long>(quad) * per_quad);
-    const long long t = static_cast<long long>(quad) * 4 + (lane >> 3);
-    if (t >= a.T) continue;
-    const bool is_v = in >= a.Hkv * units;
-    const int hu = is_v ? in - a.Hkv * units : in;  // head * units + unit
-    const int s = a.slot_mapping[t];
-    const uint4* src = reinterpret_cast<const uint4*>(
-        (is_v ? a.v_new + t * a.v_stride : a.k_new + t * a.k_stride) + hu * kUnitChannels +
-        g8 * 16);
-    const uint4 in0 = src[0], in1 = src[1];
-    if (s < 0) continue;
-    const int blk = s / kBlockSize, tok = s % kBlockSize;
-    if (blk >= a.num_blocks) {
-      if (in == 0 && g8 == 0) report(a.err, PKA_DEVERR_BAD_TABLE);
-      continue;
+  const unsigned stride = gridDim.x * (blockDim.x / 32);
+  for (int y = blockIdx.y; y < per * (3 - SIDES); y += gridDim.y) {
+    const bool second = !BOTH && y >= per;
+    const int hu = second ? y - per : y;  // head * units of a head + unit
+    const int chan = hu * kUnitChannels + g8 * 16;
+    for (unsigned quad = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; quad < quads;
+         quad += stride) {
+      const unsigned t = quad * 4 + (lane >> 3);
+      if (t >= static_cast<unsigned>(a.T)) continue;
+      const int s = a.slot_mapping[t];
+      uint4 x[SIDES][2];
+#pragma unroll
+      for (int k = 0; k < SIDES; ++k) {
+        const bool v = BOTH ? k == 1 : second;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            (v ? a.v_new + t * a.v_stride : a.k_new + t * a.k_stride) + chan);
+        x[k][0] = src[0];
+        x[k][1] = src[1];
+      }
+      if (s < 0) continue;
+      const int blk = s / kBlockSize, tok = s % kBlockSize;
+      if (blk >= a.num_blocks) {
+        if (y == 0 && g8 == 0) report(a.err, PKA_DEVERR_BAD_TABLE);
+        continue;
+      }
+      const long long at = (static_cast<long long>(blk) * per + hu) * kUnitBytes;
+#pragma unroll
+      for (int k = 0; k < SIDES; ++k) {
+        const bool v = BOTH ? k == 1 : second;
+        uint8_t* unit = (v ? a.v_pool : a.k_pool) + at;
+        uint32_t sb;
+        const uint2 codes = quantise_group(x[k][0], x[k][1], v ? a.v_scale : a.k_scale,
+                                           v ? a.v_scale6 : a.k_scale6, sb);
+        *reinterpret_cast<uint2*>(unit + (v ? v_code_offset(tok, g8) : k_code_offset(tok, g8))) =
+            codes;
+        unit[v ? v_scale_offset(tok, g8) : k_scale_offset(tok, g8)] = static_cast<uint8_t>(sb);
+      }
     }
-    uint32_t sb;
-    const uint2 codes = quantise_group(in0, in1, is_v ? a.v_scale : a.k_scale,
-                                       is_v ? a.v_scale6 : a.k_scale6, sb);
-    uint8_t* unit = (is_v ? a.v_pool : a.k_pool) +
-                    (static_cast<long long>(blk) * a.Hkv * units + hu) * kUnitBytes;
-    *reinterpret_cast<uint2*>(unit + (is_v ? v_code_offset(tok, g8) : k_code_offset(tok, g8))) =
-        codes;
-    unit[is_v ? v_scale_offset(tok, g8) : k_scale_offset(tok, g8)] = static_cast<uint8_t>(sb);
   }
 }
 
@@ -129,9 +143,14 @@ int grid_for(long long blocks, int sm_count, int per_sm) {
 
 cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int sm_count, cudaStream_t stream) {
   if (a.T == 0) return cudaSuccess;
-  const long long warps =
-      (static_cast<long long>(a.T) + 3) / 4 * 2 * a.Hkv * (a.head_dim / kUnitChannels);
-  return launch_overlapped(kv4_append_kernel, grid_for((warps + 7) / 8, sm_count, 16), 256, 0,
+  const int sms = sm_count > 0 ? sm_count : 1;
+  const int per = a.Hkv * (a.head_dim / kUnitChannels);
+  const long long x = (static_cast<long long>(a.T) + 31) / 32;
+  // K and V on one warp once there is more to do than 40 warps an SM do at once
+  const bool both = x * per * 2 > 5LL * sms;
+  const int y = std::min(both ? per : 2 * per, 65535);
+  const dim3 grid(static_cast<unsigned>(std::min(x, (16LL * sms + y - 1) / y)), y);
+  return launch_overlapped(both ? kv4_append_kernel<true> : kv4_append_kernel<false>, grid, 256, 0,
                            stream, a);
 }
 

@@ -19,10 +19,10 @@ __device__ __forceinline__ void wait_predecessor() {
 
 // cluster: CTAs per cluster (1: none).
 template <typename Args>
-cudaError_t launch_overlapped(void (*kernel)(Args), int grid, int threads, int smem,
+cudaError_t launch_overlapped(void (*kernel)(Args), dim3 grid, int threads, int smem,
                               cudaStream_t stream, const Args& args, int cluster = 1) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;

@@ -131,6 +131,22 @@ def bf16_bits(x32):
     return torch.from_numpy(np.ascontiguousarray(x32)).to(torch.bfloat16)
 
 
+def test_append_more_heads_than_a_grid_has():
+    """70000 heads of one block are the bytes of 70000 blocks of one head."""
+    H, D, slots = 70000, 128, [5, 0, 9]
+    k, v = rows((3, H, D), 1), rows((3, H, D), 2)
+    a = binding.Kv4Pool.zeros(1, H, D, KS, VS, device=DEV)
+    b = binding.Kv4Pool.zeros(H, 1, D, KS, VS, device=DEV)
+    err = i32([0])
+    binding.paged_kv4_append(k, v, a, i32(slots), err)
+    one = torch.arange(H, device=DEV, dtype=torch.int32)[None] * 16 + i32(slots)[:, None]
+    binding.paged_kv4_append(k.view(3 * H, 1, D), v.view(3 * H, 1, D), b, one.reshape(-1), err)
+    assert err.item() == 0 and a.k[0, -1].any() and a.v[0, -1].any()
+    assert torch.equal(a.k.view(-1), b.k.view(-1)) and torch.equal(a.v.view(-1), b.v.view(-1))
+    binding.paged_kv4_append(k, v, a, i32([16, -1, 15]), err)
+    assert err.item() == binding.DEVERR_BAD_TABLE
+
+
 @pytest.mark.parametrize("D,hkv,n", [(128, 1, 1), (128, 3, 37), (256, 2, 90)])
 def test_expand_bit_exact(D, hkv, n):
     pool = random_pool(n + 3, hkv, D, n)
