@@ -168,6 +168,14 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// The smaller operand, or NaN if one is NaN (fminf gives the other one, which
+// would turn a NaN logit into a finite one).
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // One step of the split-K log-sum-exp merge: folds four pieces (natural-log
 // LSE lv[u], normalised partial row x[u]) into a running state (max M,
 // denominator den, numerator acc) taken relative to M.  Pieces with

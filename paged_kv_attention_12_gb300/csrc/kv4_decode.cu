@@ -304,8 +304,9 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* const (&tile)[NT],
     for (int i = 0; i < 4; ++i) {
       float v = x[k][i] * ((i & 1) ? f1 : f0);
       if constexpr (CAP) {
-        // v = logit / cap; tanh(y) = 1 - 2 / (e^{2y} + 1), absolute error ~1e-7
-        const float e = fast_exp2(fminf(2.f * kLog2e * v, 126.f));
+        // v = logit / cap; tanh(y) = 1 - 2 / (e^{2y} + 1), absolute error ~1e-7;
+        // a NaN logit stays NaN
+        const float e = fast_exp2(min_nan(2.f * kLog2e * v, 126.f));
         v = softcap * (1.f - __fdividef(2.f, e + 1.f)) * kLog2e;
       }
       if constexpr (EDGE) v = ((i & 2) ? ok_hi : ok_lo) ? v : -INFINITY;
