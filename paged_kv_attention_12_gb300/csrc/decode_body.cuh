@@ -494,8 +494,8 @@ __device__ __forceinline__ void decode_slot(
   for (int i = 0; i < 4; ++i) {
     float v = s[i];
     if (softcap > 0.f) {
-      // tanh(y) = 1 - 2 / (e^{2y} + 1); absolute error ~1e-7
-      const float e = fast_exp2(fminf(2.f * kLog2e * (v * qscale * inv_cap), 126.f));
+      // tanh(y) = 1 - 2 / (e^{2y} + 1); absolute error ~1e-7; NaN stays NaN
+      const float e = fast_exp2(min_nan(2.f * kLog2e * (v * qscale * inv_cap), 126.f));
       v = softcap * (1.f - __fdividef(2.f, e + 1.f)) * kLog2e;
     }
     else v *= qscale;

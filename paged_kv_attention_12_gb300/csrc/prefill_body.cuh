@@ -184,9 +184,10 @@ __device__ __forceinline__ float min3f(float a, float b, float c) {
   return d;
 }
 
-// exp2-based tanh: tanh(y) = 1 - 2 / (exp(2y) + 1); absolute error ~1e-7.
+// exp2-based tanh: tanh(y) = 1 - 2 / (exp(2y) + 1); absolute error ~1e-7;
+// NaN stays NaN.
 __device__ __forceinline__ float tanh_via_exp2(float y) {
-  const float e = fast_exp2(fminf(2.f * kLog2e * y, 126.f));
+  const float e = fast_exp2(min_nan(2.f * kLog2e * y, 126.f));
   return 1.f - __fdividef(2.f, e + 1.f);
 }
 
