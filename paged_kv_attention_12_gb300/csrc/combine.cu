@@ -51,8 +51,8 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineArgs a) {
   uint16_t* dst = a.out + static_cast<size_t>(row) * D + seg * 128 + lane * 4;
   *reinterpret_cast<uint2*>(dst) =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (a.lse_out != nullptr && lane == 0 && seg == 0)
-    a.lse_out[row] = den > 0.f ? M + logf(den) : -INFINITY;
+  if (a.lse_out != nullptr && lane == 0 && seg == 0)  // (a NaN sum: NaN)
+    a.lse_out[row] = den == 0.f ? -INFINITY : M + logf(den);
 }
 
 __global__ void check_tables_kernel(const CheckArgs a) {

@@ -180,13 +180,15 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 // LSE lv[u], normalised partial row x[u]) into a running state (max M,
 // denominator den, numerator acc) taken relative to M.  Pieces with
 // lv = -inf must come with x = 0; a group of four such pieces leaves the
-// state untouched.  The split-K combine launch and the decode kernel's fused
-// combine both merge groups [0, 4), [4, 8), ... of a row's pieces with this
-// step, so the two paths give identical results.
+// state untouched; a piece with lv = NaN makes the row NaN.  The split-K
+// combine launch and the decode kernel's fused combine both merge groups
+// [0, 4), [4, 8), ... of a row's pieces with this step, so the two paths give
+// identical results.
 __device__ __forceinline__ void lse_merge4(float& M, float& den, float4& acc, const float* lv,
                                           const float4* x) {
   const float gm = fmaxf(fmaxf(lv[0], lv[1]), fmaxf(lv[2], lv[3]));
-  if (gm == -INFINITY) return;
+  // (the maximum passes over NaN, the sum does not)
+  if (gm == -INFINITY && lv[0] + lv[1] + lv[2] + lv[3] == -INFINITY) return;
   const float nm = fmaxf(M, gm);
   const float r = fast_exp2((M - nm) * 1.4426950408889634f);  // 0 while M = -inf
   den *= r;

@@ -973,12 +973,13 @@ __device__ __forceinline__ void decode_body(const DecodeArgs& a, const CUtensorM
                          orow + h * D, D * 4);
               bulk_commit();
             }
+            // (the LSE of a NaN sum is NaN: the merge may not drop the piece)
             if (t < S::TG && g == 0) {
               a.partial_lse[r0 + static_cast<size_t>(h0) * a.num_splits] =
-                  l[0] > 0.f ? (m[0] + log2f(l[0])) * kLn2 : -INFINITY;
+                  l[0] == 0.f ? -INFINITY : (m[0] + log2f(l[0])) * kLn2;
               if (h1 < G)
                 a.partial_lse[r0 + static_cast<size_t>(h1) * a.num_splits] =
-                    l[1] > 0.f ? (m[1] + log2f(l[1])) * kLn2 : -INFINITY;
+                    l[1] == 0.f ? -INFINITY : (m[1] + log2f(l[1])) * kLn2;
             }
           }
         } else {

@@ -128,6 +128,28 @@ def test_bf16_pools(D, L, n, t, softcap):
     follow_nan(bf16_batch(D, L, n, softcap), t, one_piece_paths)
 
 
+def cut_paths(b):
+    """Decode in pieces whose partial results are merged."""
+    out = torch.full_like(b.q, 7.0)
+    binding.paged_decode_attn_noalloc(b.q, out, b.k_pool, b.v_pool, b.block_tables, b.seq_lens,
+                                      b.max_seq_len, scale=b.scale, softcap=b.softcap)
+    yield "noalloc", out
+    split = binding.DecodeSplitK(b)
+    lse = torch.zeros(b.q.shape[:2], dtype=torch.float32, device=DEV)
+    yield "split-K", split.run(lse_out=lse)
+    yield "split-K LSE", lse[..., None]
+    yield "fused", binding.DecodeFused(b).run()
+    yield "mixed", binding.MixedBatch(b).run()
+
+
+@pytest.mark.parametrize("softcap", [0.0, 50.0])
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("L,t", [([90, 70], 53), ([5000, 70], 2601), ([5000, 70], 4999)])
+def test_bf16_pools_in_pieces(D, L, t, softcap):
+    """The merge drops no piece that is NaN, nor a row all of whose pieces are."""
+    follow_nan(bf16_batch(D, L, [1, 1], softcap), t, cut_paths)
+
+
 @pytest.mark.parametrize("softcap", [0.0, 50.0])
 def test_expanded_blocks(softcap):
     """A 4-bit group that held an infinity, read by a chunk over its expanded
