@@ -45,6 +45,8 @@
 // P = 2^(x - m + kShift) lies in (0, 2^15]: f16 (11 bits, the only rounding
 // of P), of use down to 2^-32 of the largest weight.  The weights' sums are
 // taken over the rounded values, in fp32 on the tensor cores.
+#include <float.h>
+
 #include <algorithm>
 
 #include "decode_body.cuh"
@@ -273,14 +275,49 @@ __device__ __forceinline__ void kv4_values(const uint8_t* tile, float (&o)[D / 1
   }
 }
 
+// x <- cap * tanh(x / cap) for a lane's log2-domain logits; in: ln 2 / cap,
+// out: cap * log2 e.  tanh(y) = 1 - 2 / (e^{2y} + 1) has an absolute error of up
+// to 7e-7, which the cap multiplies, so that it serves from |y| = 1/4 on only;
+// below it the logit is x (1 - y^2/3 + 2 y^4/15 - 17 y^6/315 + 62 y^8/2835), next
+// term under 2^-26.  The error is at most 2^-18 of the logit whatever the cap.
+// The exp2 form is left out where no logit of the warp wants it: the serving
+// layer with a cap of 50 takes 17.0 us that way, with both forms for every logit
+// 17.4 (one input set, in a graph).  NaN stays NaN.
+template <int NT>
+__device__ __forceinline__ void cap_logits(float (&x)[NT][4], float in, float out) {
+  float top = 0.f, y[NT][4];
+#pragma unroll
+  for (int k = 0; k < NT; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[k][i] = x[k][i] * in;
+      const float y2 = y[k][i] * y[k][i];
+      float p = fmaf(y2, 62.f / 2835.f, -17.f / 315.f);
+      p = fmaf(y2, p, 2.f / 15.f);
+      p = fmaf(y2, p, -1.f / 3.f);
+      x[k][i] = fmaf(x[k][i] * y2, p, x[k][i]);
+      top = fmaxf(top, fabsf(y[k][i]));
+    }
+  if (__any_sync(0xffffffffu, top >= 0.25f)) {
+#pragma unroll
+    for (int k = 0; k < NT; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float e = fast_exp2(min_nan(2.f * kLog2e * y[k][i], 126.f));
+        const float far = out * (1.f - __fdividef(2.f, e + 1.f));
+        x[k][i] = fabsf(y[k][i]) < 0.25f ? x[k][i] : far;
+      }
+  }
+}
+
 // NT tiles for one warp: scores, softmax step, values.  EDGE (NT = 1): the
 // tile holds keys outside [t_lo, pos].
 template <int D, int NT, bool EDGE, bool CAP>
 __device__ __forceinline__ void kv4_tiles(const uint8_t* const (&tile)[NT],
                                           const uint2* bq, float (&o)[D / 128][8][4],
                                           float (&m)[2], float (&l)[4],
-                                          float f0, float f1, float softcap, int tok0, int t_lo,
-                                          int pos, int lane) {
+                                          float f0, float f1, float cap_in, float cap_out,
+                                          int tok0, int t_lo, int pos, int lane) {
   constexpr int UNITS = D / kUnitChannels;
   static_assert(!EDGE || NT == 1, "an edge tile goes alone");
   const int g = lane >> 2, t = lane & 3;
@@ -297,20 +334,18 @@ __device__ __forceinline__ void kv4_tiles(const uint8_t* const (&tile)[NT],
     keep1 = (k0 + 8 >= lo && k0 + 8 <= hi ? 0xffu : 0u) |
             (k0 + 9 >= lo && k0 + 9 <= hi ? 0xff00u : 0u);
   }
+#pragma unroll
+  for (int k = 0; k < NT; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[k][i] *= (i & 1) ? f1 : f0;
+  if constexpr (CAP) cap_logits<NT>(x, cap_in, cap_out);
   float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
   for (int k = 0; k < NT; ++k) {
+    if constexpr (EDGE) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float v = x[k][i] * ((i & 1) ? f1 : f0);
-      if constexpr (CAP) {
-        // v = logit / cap; tanh(y) = 1 - 2 / (e^{2y} + 1), absolute error ~1e-7;
-        // a NaN logit stays NaN
-        const float e = fast_exp2(min_nan(2.f * kLog2e * v, 126.f));
-        v = softcap * (1.f - __fdividef(2.f, e + 1.f)) * kLog2e;
-      }
-      if constexpr (EDGE) v = ((i & 2) ? ok_hi : ok_lo) ? v : -INFINITY;
-      x[k][i] = v;
+      for (int i = 0; i < 4; ++i)
+        if (!((i & 2) ? ok_hi : ok_lo)) x[k][i] = -INFINITY;
     }
     top0 = fmaxf(top0, fmaxf(x[k][0], x[k][2]));
     top1 = fmaxf(top1, fmaxf(x[k][1], x[k][3]));
@@ -520,8 +555,10 @@ __global__ void __launch_bounds__(S::NW * 32, S::CTAS)
   __syncthreads();
   Piece pc = *plan;
   if (pc.fill_from == 0) return;
-  const float inv_cap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
-  const float lscale = a.scale * ka.k_scale * (a.softcap > 0.f ? inv_cap : kLog2e);
+  // (log2-domain logits; a cap near 0 would give an infinite factor, and NaN
+  // for a logit of 0)
+  const float lscale = a.scale * ka.k_scale * kLog2e;
+  const float cap_in = fminf(kLn2 / a.softcap, FLT_MAX), cap_out = a.softcap * kLog2e;
 
   // this warp's tiles of the piece: first .. first + mine - 1
   const int first = pc.ntiles * warp / NW, mine = pc.ntiles * (warp + 1) / NW - first;
@@ -633,7 +670,8 @@ __global__ void __launch_bounds__(S::NW * 32, S::CTAS)
       cp_async_wait<STAGES - 2>();
       __syncwarp();  // every lane's part of the tiles has landed
       const uint8_t* const tiles[2] = {t0, ring + ((n + 1) % STAGES) * 2 * S::kTile};
-      kv4_tiles<D, 2, false, CAP>(tiles, bq, o, m, l, f0, f1, a.softcap, 0, 0, 0, lane);
+      kv4_tiles<D, 2, false, CAP>(tiles, bq, o, m, l, f0, f1, cap_in, cap_out, 0, 0, 0,
+                                  lane);
       __syncwarp();
       refill(n);
       refill(n + 1);
@@ -642,7 +680,7 @@ __global__ void __launch_bounds__(S::NW * 32, S::CTAS)
       cp_async_wait<STAGES - 1>();
       __syncwarp();
       const uint8_t* const tiles[1] = {t0};
-      kv4_tiles<D, 1, true, CAP>(tiles, bq, o, m, l, f0, f1, a.softcap,
+      kv4_tiles<D, 1, true, CAP>(tiles, bq, o, m, l, f0, f1, cap_in, cap_out,
                                  tok_first + n * kBlockSize, pc.t_lo, pc.pos, lane);
       __syncwarp();
       refill(n);

@@ -1,0 +1,103 @@
+"""GPU checks of 4-bit decode at the ends of its parameters' ranges."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from paged_kv_attention_12_gb300 import _build, binding
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    _build.build()
+    binding.lib()
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device=DEV)
+
+
+def f64(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def make(lens, D, *, seed=0, ks=0.004, vs=0.002, qmag=1.0, scale=None, softcap=0.0, spare=3):
+    """A call of 8 query and 2 KV heads over random codes with e4m3 scales from
+    0.25 to 4."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    nbs = [-(-n // 16) for n in lens]
+    shape = (sum(nbs) + spare, 2, D // 128, 1152)
+    pools = []
+    for _ in range(2):
+        p = torch.randint(0, 256, shape, generator=g, device=DEV, dtype=torch.uint8)
+        p[..., 1024:] = p[..., 1024:] % 33 + 0x28
+        pools.append(p)
+    perm = np.random.default_rng(seed).permutation(shape[0])
+    table, at = np.full((len(lens), max(nbs) + 1), -1), 0
+    for b, n in enumerate(nbs):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    q = torch.randn((len(lens), 8, D), generator=torch.Generator().manual_seed(seed)) * qmag
+    return dict(pool=binding.Kv4Pool(*pools, ks, vs), table=table, lens=list(lens),
+                q=q.to(torch.bfloat16).to(DEV), scale=scale or 1 / math.sqrt(D), softcap=softcap)
+
+
+def run(c, lens=None, err=None):
+    B, hq, D = c["q"].shape
+    most = max(c["lens"])
+    n = binding.paged_kv4_decode_attn_ws_bytes(B, hq, 2, D, most)
+    ws = torch.zeros(n, dtype=torch.uint8, device=DEV)
+    out = torch.full_like(c["q"], float("nan"))
+    binding.paged_kv4_decode_attn_ws(c["q"], out, c["pool"], i32(c["table"]),
+                                     i32(c["lens"] if lens is None else lens), most, ws,
+                                     scale=c["scale"], softcap=c["softcap"], err=err)
+    torch.cuda.synchronize()
+    return out
+
+
+def check(c, out):
+    """Against fp64 attention over the values the pool holds.  The capped logit
+    moves by less than the logit does (tanh's slope is at most 1), and its own
+    rounding is relative to it, whatever the cap: at most 2^-18 of the largest
+    one (the exp2 form is taken from tanh = 0.24 on, with an absolute error of
+    tanh below 5e-7).  The logits' fp32 sums: (D + 8) 2^-23 of the sum of
+    |scale q_c k_c|; the exponential 2^-20.  Weights are rounded to f16 (2^-11,
+    below 2^-14 of the largest 2^-33 of it), outputs to bf16 (half a step: 2^-8,
+    below 2^-126 2^-134)."""
+    p = c["pool"]
+    kp = oracle.kv4_decode(p.k.cpu().numpy(), p.k_scale, False)
+    vp = oracle.kv4_decode(p.v.cpu().numpy(), p.v_scale, True)
+    q, D = f64(c["q"]), c["q"].shape[2]
+    args = (c["table"], c["lens"], c["scale"], c["softcap"], 0)
+    ref, _ = oracle.paged_decode(q, kp, vp, *args)
+    mag, _ = oracle.paged_decode(q, kp, np.abs(vp), *args)
+    s, top, small = 0.0, 0.0, np.zeros(mag.shape)
+    for b, n in enumerate(c["lens"]):
+        if n:
+            key = oracle.gather_request_kv(kp, c["table"][b], n, 16)
+            one = np.einsum("hgd,thd->hgt", q[b].reshape(2, 4, D), key) * c["scale"]
+            a = np.einsum("hgd,thd->hgt", np.abs(q[b]).reshape(2, 4, D), np.abs(key))
+            s, top = max(s, abs(c["scale"]) * a.max()), max(top, np.abs(one).max())
+            v = oracle.gather_request_kv(vp, c["table"][b], n, 16)
+            small[b] = 2.0 ** -33 * np.abs(v).sum(0).repeat(4, 0)
+    if c["softcap"] > 0:
+        top = c["softcap"] * np.tanh(top / c["softcap"])
+    delta = (D + 8) * 2.0 ** -23 * s + 2.0 ** -20 + 2.0 ** -18 * top
+    tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -134 + (2.0 ** -11 + 2 * delta) * mag + small
+    worst = float(((np.abs(f64(out) - ref) - tol) / np.abs(mag).max()).max())
+    assert worst <= 0, (worst, delta, top)             # NaN fails too
+
+
+@pytest.mark.parametrize("softcap", [1e-40, 1e-3, 5.0, 50.0, 300.0, 1e4, 1e6, 1e20, 3e38])
+@pytest.mark.parametrize("D,lens", [(128, [70, 1, 0, 300]), (256, [9000, 40])])
+def test_caps_of_every_size(D, lens, softcap):
+    """A cap far above the logits leaves them as they are, one far below makes
+    them all alike; a query of zeros averages its values."""
+    c = make(lens, D, seed=len(lens), qmag=4.0, ks=0.05, softcap=softcap)
+    c["q"][0, 3] = 0.0
+    check(c, run(c))
