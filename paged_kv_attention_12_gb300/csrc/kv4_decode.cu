@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(S::NW * 32, S::CTAS)
     for (int off = 4; off < 32; off <<= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
     const float f = den == 0.f ? 0.f
                                : ((m[j] == -INFINITY) ? 1.f : fast_exp2(m[j] - M)) *
-                                     __fdividef(ka.v_scale, den);
+                                     __fdividef(1.f, den);
     // P carries a factor 2^kShift, the same in every piece; a NaN sum keeps
     // its weight, so that the merge of the pieces passes it on
     if (split && warp == 0 && g == 0 && 2 * t + j < G)
@@ -729,6 +729,13 @@ __global__ void __launch_bounds__(S::NW * 32, S::CTAS)
         o[u][i][2 + j] *= f;
       }
   }
+  // four normalised output columns of a row: V's pool scale comes last, since a
+  // small one divided by the weights' sum would leave fp32's range
+  auto store_scaled = [&](size_t row, int d0, const float4& y) {
+    const float vs = ka.v_scale;
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + row * D + d0) =
+        make_uint2(pack_bf16x2(y.x * vs, y.y * vs), pack_bf16x2(y.z * vs, y.w * vs));
+  };
   auto state = [&](int w, int item) {
     return reinterpret_cast<const float4*>(smem + w * S::kWarpRing) + item;
   };
@@ -766,8 +773,7 @@ __global__ void __launch_bounds__(S::NW * 32, S::CTAS)
                                        ((head0 + h) * a.num_splits + pc.slot) * D + d0),
              y);
     else
-      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + (head0 + h) * D + d0) =
-          make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+      store_scaled(head0 + h, d0, y);
   }
   if (split) {
     // ---- the piece that arrives last at its segment merges the partials
@@ -793,10 +799,8 @@ __global__ void __launch_bounds__(S::NW * 32, S::CTAS)
       const int parts = max(1, NW * 32 / items);
       auto finish = [&](int it, const float4& acc, float den) {
         const float inv = den == 0.f ? 0.f : 1.f / den;
-        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + (head0 + it / kRow) * D +
-                                  it % kRow * 4) =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
-                       pack_bf16x2(acc.z * inv, acc.w * inv));
+        store_scaled(head0 + it / kRow, it % kRow * 4,
+                     make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
       };
       float4* st = reinterpret_cast<float4*>(smem);           // [NW * 32]
       float2* md = reinterpret_cast<float2*>(st + NW * 32);  // [NW * 32]

@@ -101,3 +101,15 @@ def test_caps_of_every_size(D, lens, softcap):
     c = make(lens, D, seed=len(lens), qmag=4.0, ks=0.05, softcap=softcap)
     c["q"][0, 3] = 0.0
     check(c, run(c))
+
+
+@pytest.mark.parametrize("ks,vs,qmag", [(0.004, 1.2e-38, 1.0), (0.004, 3e-34, 1.0),
+                                        (0.004, 1e36, 1.0), (1e-36, 0.002, 1e34),
+                                        (1e35, 0.002, 1e-36)])
+@pytest.mark.parametrize("D,lens", [(128, [1100, 50]), (256, [9000])])
+def test_pool_scales_of_every_size(D, lens, ks, vs, qmag):
+    """Pool scales near both ends of fp32: the output is as accurate as ever."""
+    c = make(lens, D, seed=3, ks=ks, vs=vs, qmag=qmag, scale=0.05)
+    c["pool"].v[..., :1024] &= 0x77                    # no value below 0: means are large
+    c["q"][0, 6] = 0.0                                 # every weight the same
+    check(c, run(c))
