@@ -698,6 +698,10 @@ __global__ void __launch_bounds__(S::NW * 32, S::CTAS)
   __syncthreads();
   pc = *plan;  // not kept in registers over the loop
   const bool split = pc.npieces > 1;
+  // A sum of 0 means no visible key, whose output is 0, or logits that are all
+  // -infinity, whose softmax is 0 / 0 (a piece of a cut segment leaves that to
+  // the merge).
+  const float no_sum = split || pc.ntiles == 0 ? 0.f : NAN;
   const size_t head0 = static_cast<size_t>(pc.qrow) * a.Hq + pc.kvh * G;
   // lane (g, t) takes warps g and g + 8
 #pragma unroll
@@ -713,7 +717,7 @@ __global__ void __launch_bounds__(S::NW * 32, S::CTAS)
                 ((v1.x == -INFINITY) ? 1.f : fast_exp2(v1.x - M)) * v1.y;
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
-    const float f = den == 0.f ? 0.f
+    const float f = den == 0.f ? no_sum
                                : ((m[j] == -INFINITY) ? 1.f : fast_exp2(m[j] - M)) *
                                      __fdividef(1.f, den);
     // P carries a factor 2^kShift, the same in every piece; a NaN sum keeps
@@ -798,7 +802,7 @@ __global__ void __launch_bounds__(S::NW * 32, S::CTAS)
       const int items = G * kRow;
       const int parts = max(1, NW * 32 / items);
       auto finish = [&](int it, const float4& acc, float den) {
-        const float inv = den == 0.f ? 0.f : 1.f / den;
+        const float inv = den == 0.f ? NAN : 1.f / den;  // (a cut segment has keys)
         store_scaled(head0 + it / kRow, it % kRow * 4,
                      make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
       };

@@ -113,3 +113,17 @@ def test_pool_scales_of_every_size(D, lens, ks, vs, qmag):
     c["pool"].v[..., :1024] &= 0x77                    # no value below 0: means are large
     c["q"][0, 6] = 0.0                                 # every weight the same
     check(c, run(c))
+
+
+@pytest.mark.parametrize("lens", [[40, 0, 7], [9000, 0, 7]])
+def test_query_of_minus_infinity(lens):
+    """Keys are visible but every logit is -infinity: the softmax is 0 / 0.  A
+    row without keys stays 0."""
+    c = make(lens, 128)
+    c["pool"].k[..., :1024] = 0x22                     # every code 1
+    c["q"].fill_(1.0)
+    c["q"][:, 5, 0] = -math.inf
+    out = run(c)
+    assert torch.isnan(out[0, 5]).all() and torch.isnan(out[2, 5]).all() and not out[1].any()
+    out[:, 5] = 0
+    assert torch.isfinite(out).all()
