@@ -1,4 +1,5 @@
-"""GPU checks of 4-bit decode at the ends of its parameters' ranges."""
+"""GPU checks of 4-bit decode at the ends of its parameters' ranges, and of the ids
+and lengths that it and the expansion correct."""
 import math
 
 import numpy as np
@@ -127,3 +128,40 @@ def test_query_of_minus_infinity(lens):
     assert torch.isnan(out[0, 5]).all() and torch.isnan(out[2, 5]).all() and not out[1].any()
     out[:, 5] = 0
     assert torch.isfinite(out).all()
+
+
+def test_bad_ids_read_as_zeros_and_long_rows_end_with_their_table():
+    c = make([64, 61, 64], 128, seed=4)
+    t = c["table"].copy()
+    nb = c["pool"].num_blocks
+    t[1, 2], t[1, 3], t[2, 1] = nb, 2 ** 31 - 1, -1
+    err = i32([0])
+    out = run(dict(c, table=t), err=err)
+    assert err.item() == binding.DEVERR_BAD_TABLE
+    # the same call with a block of zeros where the bad ids were
+    more = binding.Kv4Pool(*(torch.cat([p, torch.zeros_like(p[:1])]) for p in
+                             (c["pool"].k, c["pool"].v)), c["pool"].k_scale, c["pool"].v_scale)
+    z = c["table"].copy()
+    z[1, 2] = z[1, 3] = z[2, 1] = nb
+    same = dict(c, pool=more, table=z)
+    err.zero_()
+    assert torch.equal(run(same, err=err), out) and err.item() == 0
+    check(same, out)
+    # lengths behind the table's last entry, and negative ones
+    full = np.maximum(c["table"], 0)
+    width = 16 * full.shape[1]
+    got = run(dict(c, table=full), lens=[10 ** 6, width, -3], err=err)
+    assert err.item() == binding.DEVERR_SEQ_LEN
+    ends = dict(c, table=full, lens=[width, width, 0])
+    assert torch.equal(run(ends), got) and not got[2].any()
+    check(ends, got)
+
+
+def test_expand_leaves_what_bad_ids_name():
+    c = make([48], 128, spare=0)
+    k16 = torch.full((2, 2, 16, 128), 3.0, dtype=torch.bfloat16, device=DEV)
+    v16, err = k16.clone(), i32([0])
+    binding.paged_kv4_expand(c["pool"], k16, v16, i32([3, 0, -1, 1]), i32([0, 2, 1, -5]), err)
+    torch.cuda.synchronize()
+    assert err.item() == binding.DEVERR_BAD_TABLE
+    assert k16.eq(3.0).all() and v16.eq(3.0).all()
