@@ -445,8 +445,10 @@ int paged_kv4_expand(const pka_kv4_pool* kv, const pka_kv_pool* dst, const int32
 /* Decode over a 4-bit cache: paged_decode_attn_ws on the values the pool
  * holds (arithmetic on them in fp32, or in f16 where that is exact; softmax weights
  * rounded to f16; bf16 out).  Arguments, masks and errors as there; any group
- * of 1 to 8 query heads per KV head.  A table id outside the pool reads as
- * zeros and ORs PKA_DEVERR_BAD_TABLE into params->err.
+ * of 1 to 8 query heads per KV head; B * Hkv and B * the most blocks a query
+ * sees (max_blocks, fewer with a window) at most 2^30, else PKA_ERR_SHAPE.  A
+ * table id outside the pool reads as zeros and ORs PKA_DEVERR_BAD_TABLE into
+ * params->err.
  * One launch: short segments (request, KV head) stream whole; longer ones are
  * cut into pieces, at most 30 each, whose fp32 partials the last piece to
  * arrive merges in a fixed order (the same bits every time).  max_seq_len

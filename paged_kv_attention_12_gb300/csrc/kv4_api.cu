@@ -195,12 +195,12 @@ int paged_kv4_decode_attn_ws(const void* q, void* out, const pka_kv4_pool* kv,
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return PKA_ERR_ALIGN;
   const Kv4Layout L = kv4_layout(B, Hq, kv->head_dim, max_seq_len, params->window);
   if (workspace_bytes < L.total()) return PKA_ERR_WORKSPACE;
-  // the work line (visible blocks and a fixed cost of 16 units per segment) in
-  // the kernels' 32-bit arithmetic
+  // what the kernels count in 32 bits: the CTAs (one a segment and some more),
+  // and the plan's sum of the requests' visible blocks
   int64_t per = max_blocks;
   if (params->window > 0) per = std::min<int64_t>(per, (params->window - 1) / 16 + 2);
-  if (static_cast<int64_t>(B) * kv->num_kv_heads * (per + 16) > (int64_t(1) << 30))
-    return PKA_ERR_SHAPE;
+  constexpr int64_t kMost = int64_t(1) << 30;
+  if (static_cast<int64_t>(B) * kv->num_kv_heads > kMost || B * per > kMost) return PKA_ERR_SHAPE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   pka::Kv4DecodeArgs a{};
   a.base.q = static_cast<const uint16_t*>(q);

@@ -165,3 +165,23 @@ def test_expand_leaves_what_bad_ids_name():
     torch.cuda.synchronize()
     assert err.item() == binding.DEVERR_BAD_TABLE
     assert k16.eq(3.0).all() and v16.eq(3.0).all()
+
+
+def test_wide_tables_of_many_heads():
+    """512 segments over table rows of 2 million entries: the requests' blocks are
+    counted, not each KV head's again."""
+    lens = [5000] + [40 + i for i in range(63)]
+    c = make(lens, 128, seed=1)
+    p = c["pool"]
+    pool = binding.Kv4Pool(*(t.repeat(1, 4, 1, 1) for t in (p.k, p.v)), p.k_scale, p.v_scale)
+    q = c["q"].repeat(1, 4, 1)
+    ws = torch.zeros(binding.paged_kv4_decode_attn_ws_bytes(64, 32, 8, 128, 5000),
+                     dtype=torch.uint8, device=DEV)
+    table = torch.full((64, (1 << 21) - 15), -1, dtype=torch.int32, device=DEV)
+    narrow = i32(c["table"])
+    table[:, :narrow.shape[1]] = narrow
+    out = [torch.full_like(q, float("nan")) for _ in range(2)]
+    for t, o in zip((table, narrow), out):
+        binding.paged_kv4_decode_attn_ws(q, o, pool, t, i32(lens), 5000, ws, scale=c["scale"])
+    torch.cuda.synchronize()
+    assert torch.equal(*out) and torch.isfinite(out[0]).all()
