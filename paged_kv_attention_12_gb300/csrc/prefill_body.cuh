@@ -846,6 +846,7 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs& a, const CUtenso
     // capped path does.
     const bool prescale = capped || !(sl2 > 0.f);
     const float cap_in = capped ? a.scale / a.softcap : 0.f;
+    const float cap_mag = fabsf(cap_in);  // (the range of y is the same for scale < 0)
     const float cap_out = a.softcap * kLog2e;
     // The three-term form of cap_out * tanh(cap_in * s) written in s:
     // x(s) = s (k1 + s^2 (k3 + k5 s^2)), k1 = cap_in cap_out,
@@ -907,13 +908,13 @@ __device__ __forceinline__ void prefill_body(const PrefillArgs& a, const CUtenso
         // Taylor form when every |y| of the warp's rows is below 1/8 (three
         // terms) or 0.5 (six terms), else the exp2 form.  With scale > 0 the
         // three-term form stays folded (see k1, k3, k5) and s stays raw.
-        if (fold_ok && __all_sync(0xffffffffu, amax * cap_in < 0.125f)) {
+        if (fold_ok && __all_sync(0xffffffffu, amax * cap_mag < 0.125f)) {
           folded = true;
           have_max = !need_mask;
-        } else if (__all_sync(0xffffffffu, amax * cap_in < 0.125f)) {
+        } else if (__all_sync(0xffffffffu, amax * cap_mag < 0.125f)) {
 #pragma unroll
           for (int c = 0; c < BN; ++c) s[c] = cap_out * tanh_taylor_short(s[c] * cap_in);
-        } else if (__all_sync(0xffffffffu, amax * cap_in < 0.5f)) {
+        } else if (__all_sync(0xffffffffu, amax * cap_mag < 0.5f)) {
 #pragma unroll
           for (int c = 0; c < BN; ++c) s[c] = cap_out * tanh_taylor(s[c] * cap_in);
         } else {
