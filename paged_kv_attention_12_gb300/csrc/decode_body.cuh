@@ -695,7 +695,8 @@ __device__ __forceinline__ void decode_body(const DecodeArgs& a, const CUtensorM
 
   // ============================ consumer warps ============================
   const int g = lane >> 2, t = lane & 3;
-  const float inv_cap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
+  // (finite for caps near 0 too: 0 * inf would make a logit of 0 NaN)
+  const float inv_cap = a.softcap > 0.f ? fminf(1.f / a.softcap, kFltMax) : 0.f;
   const float qscale = a.scale * (a.softcap > 0.f ? 1.f : kLog2e);
   int tile_base = 0;
   int nmerge = 0;  // pieces merged so far (phases of staging_free)

@@ -45,8 +45,6 @@
 // P = 2^(x - m + kShift) lies in (0, 2^15]: f16 (11 bits, the only rounding
 // of P), of use down to 2^-32 of the largest weight.  The weights' sums are
 // taken over the rounded values, in fp32 on the tensor cores.
-#include <float.h>
-
 #include <algorithm>
 
 #include "decode_body.cuh"
@@ -558,7 +556,7 @@ __global__ void __launch_bounds__(S::NW * 32, S::CTAS)
   // (log2-domain logits; a cap near 0 would give an infinite factor, and NaN
   // for a logit of 0)
   const float lscale = a.scale * ka.k_scale * kLog2e;
-  const float cap_in = fminf(kLn2 / a.softcap, FLT_MAX), cap_out = a.softcap * kLog2e;
+  const float cap_in = fminf(kLn2 / a.softcap, kFltMax), cap_out = a.softcap * kLog2e;
 
   // this warp's tiles of the piece: first .. first + mine - 1
   const int first = pc.ntiles * warp / NW, mine = pc.ntiles * (warp + 1) / NW - first;

@@ -20,6 +20,9 @@ int g_sm_count[kMaxDevices] = {0};
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// An infinite cap is no cap, and neither is one that times log2 e leaves fp32.
+float effective_cap(float softcap) { return softcap > 1e38f ? 0.f : softcap; }
+
 bool supported_dim(int d) { return d == 128 || d == 256; }
 bool supported_group(int g) { return g == 1 || g == 2 || g == 4 || g == 8; }
 
@@ -87,7 +90,7 @@ pka::DecodeArgs decode_args(const void* q, const pka_kv_pool* kv, const int32_t*
   a.num_blocks = kv->num_blocks;
   a.max_blocks = max_blocks;
   a.scale = p->scale;
-  a.softcap = std::isinf(p->softcap) ? 0.f : p->softcap;  // an infinite cap is no cap
+  a.softcap = effective_cap(p->softcap);
   a.window = p->window;
   return a;
 }
@@ -370,7 +373,7 @@ pka::PrefillArgs prefill_args(const void* q, void* out, const pka_kv_pool* kv,
   a.max_query_len = max_query_len;
   a.max_seq_len = max_seq_len;
   a.scale = params->scale;
-  a.softcap = std::isinf(params->softcap) ? 0.f : params->softcap;
+  a.softcap = effective_cap(params->softcap);
   a.window = params->window;
   return a;
 }

@@ -579,7 +579,9 @@ __device__ __forceinline__ void prefill2_body(const PrefillArgs& a, const CUtens
     // (uniform over the launch) the logits are scaled before the mask, as the
     // capped path does.
     const bool prescale = capped || !(sl2 > 0.f);
-    const float cap_in = capped ? a.scale / a.softcap : 0.f;
+    // (finite for caps near 0 too: 0 * inf would make a logit of 0 NaN)
+    const float cap_in =
+        capped ? fmaxf(fminf(a.scale / a.softcap, kFltMax), -kFltMax) : 0.f;
     const float cap_mag = fabsf(cap_in);  // (the range of y is the same for scale < 0)
     const float cap_out = a.softcap * kLog2e;
     // The three-term form of cap_out * tanh(cap_in * s) written in s:
@@ -587,11 +589,11 @@ __device__ __forceinline__ void prefill2_body(const PrefillArgs& a, const CUtens
     // k3 = -cap_in^3 cap_out / 3, k5 = 2 cap_in^5 cap_out / 15.  For
     // cap_in > 0 it increases with s, so the row maximum of x is x(max s),
     // and a masked column (s = -inf) gives x = -inf, as long as k5 > 0
-    // (no 0 * inf).
+    // (no 0 * inf); a cap so small that k5 overflows would do the same to s = 0.
     const float k1 = cap_in * cap_out;
     const float k3 = -cap_in * cap_in * k1 * (1.f / 3.f);
     const float k5 = 2.f * cap_in * cap_in * cap_in * cap_in * k1 * (1.f / 15.f);
-    const bool fold_ok = capped && cap_in > 0.f && k5 > 0.f;
+    const bool fold_ok = capped && cap_in > 0.f && k5 > 0.f && k5 <= kFltMax;
     float m_ref = -INFINITY;
     float l = 0.f;
     bool ok = true;

@@ -44,3 +44,14 @@ SHAPES = [([300, 200, 33], [130, 200, 1]), ([900, 40, 1], [1, 1, 1])]
 def test_negative_scale(D, L, n, softcap):
     """Logits on both sides of the cap's bend, of either sign of the scale."""
     check(batch(D, L, n, softcap, scale=-0.25))
+
+
+@pytest.mark.parametrize("softcap", [1e-40, 1e-12, 1e-3, 1.5e38, 3.4e38])
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("L,n", SHAPES)
+def test_ends_of_the_range(D, L, n, softcap):
+    """A cap near 0 makes every key alike, one near the largest float none
+    different, and queries of zeros average their values under both."""
+    b = batch(D, L, n, softcap, seed=1)
+    b.q[:max(1, n[0] // 2)] = 0.0
+    check(b)
