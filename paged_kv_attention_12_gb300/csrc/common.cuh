@@ -38,6 +38,7 @@ __device__ __forceinline__ unsigned long long timeline_now() {
 constexpr int kBlockSize = 16;        // tokens per KV block (the only supported size)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kWideCap = 64.f;      // caps above it take care of small logits (bf16 decode)
 constexpr float kFltMax = 0x1.fffffep127f;
 // A bounded wait gives up after this many SM clock cycles (about a second).
 constexpr long long kWaitBudgetCycles = 2000000000LL;

@@ -55,3 +55,10 @@ def test_ends_of_the_range(D, L, n, softcap):
     b = batch(D, L, n, softcap, seed=1)
     b.q[:max(1, n[0] // 2)] = 0.0
     check(b)
+
+
+@pytest.mark.parametrize("softcap", [64.5, 300.0, 1e4, 1e6, 1e9, 1e20])
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("L,n", SHAPES)
+def test_caps_far_above_the_logits(D, L, n, softcap):
+    check(batch(D, L, n, softcap, seed=2))
