@@ -33,7 +33,7 @@ int check_kv4_pointers(const pka_kv4_pool* kv) {
 // outputs and partial LSEs.  The counters lie in the same place whatever the
 // sizes are, so that calls of all sizes can share a workspace in turn.
 struct Kv4Layout {
-  int32_t S, C;  // partial slots per (request, query head); shortest piece in tiles
+  int32_t S, C;  // partial slots per (request, query head); the plan's shortest piece
   size_t o_bytes, lse_bytes;
   size_t total() const { return pka::kKv4CounterBytes + o_bytes + lse_bytes; }
 };
@@ -46,7 +46,8 @@ int32_t kv4_max_tiles(int32_t max_seq_len, int32_t window) {
 Kv4Layout kv4_layout(int32_t B, int32_t Hq, int32_t D, int32_t max_seq_len, int32_t window) {
   Kv4Layout L;
   const int32_t T = kv4_max_tiles(max_seq_len, window);
-  // at least four tiles a piece, and at most 30 pieces of a segment
+  // at most 30 pieces of a segment, of C tiles or more.  (The plan's own minimum
+  // is 16 tiles, so that shorter requests leave some of their slots unused.)
   L.C = std::max(4, (T + 28) / 29);
   L.S = (T + L.C - 1) / L.C + 1;
   L.o_bytes = static_cast<size_t>(B) * Hq * L.S * D * sizeof(float);
@@ -214,7 +215,7 @@ int paged_kv4_decode_attn_ws(const void* q, void* out, const pka_kv4_pool* kv,
   a.base.num_blocks = kv->num_blocks;
   a.base.max_blocks = max_blocks;
   a.base.scale = params->scale;
-  a.base.softcap = std::isinf(params->softcap) ? 0.f : params->softcap;
+  a.base.softcap = params->softcap > 1e38f ? 0.f : params->softcap;
   a.base.window = params->window;
   a.base.num_splits = L.S;
   a.base.split_blocks = L.C;

@@ -19,9 +19,11 @@ namespace {
 // side, a V unit a group's tokens.  Grid: y the head and 128 channels (and K or
 // V), x the tokens, so that nothing is divided by sizes.  Bound by arithmetic and
 // by the time a warp waits for its rows: 8192 tokens x 4 heads x 128, 21.5 MB,
-// 4.9 us, 3.2 us of it HBM (K and V on warps of their own 5.5 us, unpaired
-// arithmetic 5.6, four CTAs per SM 6.0, a warp index divided by the heads 6.4, a
-// division per value 9.8).  32 tokens: 1.8 us, 2.2 with BOTH.
+// 5.0 us, 3.2 us of it HBM; its 1024 CTAs are 1.35 waves of the 760 that run at
+// once (K and V on warps of their own 5.5 us, unpaired arithmetic 5.6, four CTAs
+// per SM 6.0, a warp index divided by the heads 6.4, a division per value 9.8).
+// 32 tokens: 1.8 us, 2.2 with BOTH.  (Calls in a captured graph, three input sets
+// in turn.)
 template <bool BOTH>
 __global__ void __launch_bounds__(256, 5)
     kv4_append_kernel(const __grid_constant__ Kv4AppendArgs a) {
@@ -76,9 +78,10 @@ __global__ void __launch_bounds__(256, 5)
 // One warp per unit (16 tokens x 128 channels of a block and head, K or V): a
 // lane takes 8 channels of two tokens apart at a time, so that every store of
 // the warp is two whole rows of 256 bytes; the unit's loads are in flight
-// together.  Bound by HBM: 4096 blocks x 4 heads x 128, 172 MB, 27 us, 6.4 TB/s,
-// 94% of a plain copy (31 us without the streaming stores; a thread per 8
-// channels with an index division each took 74 us).
+// together.  Bound by HBM: 4096 blocks x 4 heads x 128, 172 MB, 30.3 us, 5.7 TB/s,
+// 84% of a plain copy, three input sets in turn.  With one set, part of which
+// stays in L2: 25.6 us (31 without the streaming stores; 74 with a thread per 8
+// channels and an index division each).
 __global__ void __launch_bounds__(256) kv4_expand_kernel(const __grid_constant__ Kv4ExpandArgs a) {
   const int lane = threadIdx.x & 31;
   const int units = a.head_dim / kUnitChannels;

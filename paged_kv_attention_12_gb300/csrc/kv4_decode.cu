@@ -11,8 +11,14 @@
 // one piece per CTA; a CTA of NW warps gives each warp a run of the piece's
 // tiles and merges the warps' states in shared memory.  Few segments run on CTAs
 // that fill an SM (16 warps at D = 128, 8 at 256), more of them on CTAs of a
-// half or a quarter of that: uniform batches of 608 segments reach 4.4 TB/s
-// (1680 tokens, D = 128) to 5.4 TB/s (6720 tokens) that way.
+// half or a quarter of that: uniform batches of 608 segments reach 4.5 TB/s
+// (1680 tokens, D = 128) to 5.5 TB/s (6720 tokens) that way.  Batches of more
+// requests than the plan has room for (kMaxBatch) are not cut: 704 requests of 64
+// tokens but for one of 100000 take 41 us (D = 128), 705 take 637; 712 and 713 at
+// D = 256 111 and 1789.
+//
+// Times here and below: calls in a captured graph, three input sets in turn
+// unless another condition stands beside them.
 //
 // Loads.  Every warp streams its own tiles: cp.async, 16 bytes a lane, into
 // its own ring of STAGES tiles in shared memory, so no other warp is waited
@@ -20,11 +26,12 @@
 // against 4.9 TB/s with one bulk copy per unit.  Four tiles a warp in flight; five
 // or six were slower (4 x 32..131 K keys: 43.3, 44.5, 45.1 us).
 //
-// What bounds it: HBM.  With long segments a tile takes an SM 55 ns (D = 128)
-// or 110 ns (D = 256), 6.4 TB/s over the GPU, 94% of a plain copy, at 300 and
-// 490 instructions and 2.8 and 2.3 of 4 a cycle.  Around that lie about 4 us from the launch to
-// the first tiles, 1.5 us for the warps' merge and, where segments are cut, 3 us
-// for the merge through global memory.
+// What bounds it: HBM.  With long segments a tile takes an SM 56 ns (D = 128)
+// or 111 ns (D = 256), 6.2 TB/s over the GPU, 92% of a plain copy, at 298 and
+// 489 instructions and 2.8 and 2.3 of 4 a cycle (the difference of 2048 and 6144
+// tokens, 152 segments).  Around that lie about 4 us from the launch to the first
+// tiles, 1.5 us for the warps' merge and, where segments are cut, 3 us for the
+// merge through global memory.  A logit cap costs the serving layer 0.7 us.
 //
 // Arithmetic per tile and warp: S^T = K q^T and O^T += V^T P^T with m16n8k16
 // f16 MMAs (keys or channels on M, the G <= 8 query heads on N).  Codes go
@@ -56,15 +63,26 @@ namespace pka {
 namespace {
 
 // When no segment can be longer than this many tiles, none is cut: a merge
-// through global memory costs about 3 us.  (B = 8, Hkv = 2, G = 4, us a call in
-// a stream of them, whole / cut: D = 128, 1024 tokens 7.6 / 8.3, 1280 tokens
-// 8.8 / 8.5; D = 256, 640 tokens 8.4 / 9.0, 800 tokens 10.0 / 9.0.)
+// through global memory costs about 3 us.  (16 segments of one length, us whole /
+// cut: D = 128, 1024 tokens 7.6 / 8.2, 1152 8.6 / 8.3, 1600 10.4 / 8.5; D = 256,
+// 640 tokens 8.6 / 8.8, 800 10.3 / 8.9.)
+// The half-SM CTAs take half of it.  (200 segments of 1..n tokens: D = 128, n =
+// 576 7.9 / 9.7, 768 9.1 / 10.2, 1024 10.9 / 11.1, 1536 14.5 / 12.9; D = 256, n =
+// 320 8.2 / 11.3, 512 10.7 / 12.3, 768 14.0 / 14.1: the two cross at 64 and 48
+// tiles only.)
 constexpr int whole_tiles(int head_dim) { return head_dim == 128 ? 72 : 40; }
-// The same for the small CTAs of large batches.
+// The same for the small CTAs of large batches.  (608 segments of 1..n tokens:
+// D = 128, n = 960 18.8 / 19.9, 1440 25.4 / 25.6, 1920 31.4 / 31.2; D = 256, n =
+// 960 32.2 / 37.2, 1920 56.8 / 62.7: past 60 tiles the two are alike at D = 128,
+// at 256 whole segments stay ahead.)
 constexpr int kSmallWhole = 60;
-// Pieces beyond one for each segment, when the segments are more than run at once.
+// Pieces beyond one for each segment, when the segments are more than run at
+// once.  (800 segments, none / 64 / 200 of them: D = 128, 16..2000 tokens 40.4 /
+// 40.9 / 41.2 us; D = 256, 1..1500 tokens 65.0 / 63.2 / 62.6.)
 constexpr int kMoreThan = 64;
-// Else the shortest piece, in tiles.
+// Else the shortest piece, in tiles.  (16 segments, 8 / 16 / 32 tiles: D = 128,
+// 1280 tokens 8.6 / 8.6 / 8.8 us; D = 256, 800 tokens 9.5 / 9.0 / 9.9, 1280 11.2 /
+// 9.7 / 10.7, 2560 12.0 / 12.0 / 11.6.)
 constexpr int kMinPiece = 16;
 
 constexpr float kGrow = 7.f;
@@ -280,7 +298,8 @@ __device__ __forceinline__ void kv4_values(const uint8_t* tile, float (&o)[D / 1
 // term under 2^-26.  The error is at most 2^-18 of the logit whatever the cap.
 // The exp2 form is left out where no logit of the warp wants it: the serving
 // layer with a cap of 50 takes 17.0 us that way, with both forms for every logit
-// 17.4 (one input set, in a graph).  NaN stays NaN.
+// 17.4 (one input set); with logits that all want it 20.5 in place of 19.9 (three).
+// NaN stays NaN.
 template <int NT>
 __device__ __forceinline__ void cap_logits(float (&x)[NT][4], float in, float out) {
   float top = 0.f, y[NT][4];
