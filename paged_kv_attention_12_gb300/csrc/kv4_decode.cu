@@ -42,9 +42,9 @@
 // nibbles of the two keys are interleaved before the conversion.  q is f16
 // after a power-of-two scaling per head that brings its largest element to
 // [1, 2): exact but for elements below 2^-17 of the largest, whose error
-// (2^-25 of the largest) is that of fp32 sums.  Pool scales, the softmax
+// (2^-25 of the largest) is that of fp32 sums.  K's pool scale, the softmax
 // scale and q's power of two are one fp32 factor on the logits; V's pool
-// scale is applied once to the result.
+// scale multiplies the finished result.
 //
 // Softmax in the exp2 domain with a reference m per head that all lanes
 // share; it moves (and O is rescaled) only when a logit exceeds it by more
