@@ -78,6 +78,7 @@ typedef enum {
 #define PKA_DEVERR_QUERY_LOC 8  /* query_start_loc span outside [0, total_q], negative,
                                    or longer than max_query_len (request skipped) */
 #define PKA_DEVERR_REFCOUNT 16  /* a block's reference count fell below zero */
+#define PKA_DEVERR_TREE 32      /* a drafted token's parent is not a token before it */
 
 /* One layer's K/V block pool.  k and v are device pointers, 16-byte aligned,
  * bf16 [num_blocks][num_kv_heads][block_size][head_dim]. */
@@ -518,6 +519,138 @@ int paged_kv_compact(void* const* pools, int32_t num_pools, int32_t num_blocks,
                      const int32_t* block_tables, int32_t* new_tables, int32_t max_blocks,
                      const int32_t* seq_lens, int32_t B, int32_t* remap, int32_t* moves,
                      int32_t* err, void* stream);
+
+/* Draft trees (speculative decoding).  The pages have no counterpart; these
+ * entry points are services of this library beside its prefill, append and page
+ * calls.  In a step each request brings n <= 64 drafted tokens that form a tree:
+ * token 0 is its root (the last token the model chose, whose K/V are not cached
+ * yet), token i > 0 follows token parents[i] < i.  The n tokens take the cache
+ * positions L - n .. L - 1 in order (L = seq_lens[b], the drafted tokens
+ * included), whatever their depth.  A step is: paged_tree_plan, then per layer
+ * paged_kv_append[_rope] with the plan's slots and positions and
+ * paged_tree_attn_ws with its masks, then paged_tree_accept.
+ * Rows are those of paged_prefill_attn: request b owns rows
+ * [query_start_loc[b], query_start_loc[b+1]) of the total_q rows.
+ *
+ * paged_tree_plan: for each token i of a tree
+ *   tree_masks uint64 [total_q]: bit j is set iff token j is i or one of its
+ *              ancestors;
+ *   positions  int32 [total_q]: T - n + (the number of i's ancestors), for the
+ *              rotary embedding; T = total_lens[b] (NULL: L), the length of the
+ *              sequence where keys were evicted from its cache;
+ *   slots      int32 [total_q]: the pool slot of cache position L - n + i.
+ *   Each of the three may be NULL.  parents int32 [total_q]: a token before it in
+ *   its tree, -1: none (more than one token may have none); another value ORs
+ *   PKA_DEVERR_TREE into *err and counts as -1.  Rows from query_start_loc[B] on
+ *   (padding) get mask 0, position 0, slot -1.  A request whose span is not as
+ *   in paged_prefill_attn is left out (PKA_DEVERR_QUERY_LOC, its rows unwritten);
+ *   one with n > L or L past its table row gets mask 0, position 0, slot -1
+ *   (PKA_DEVERR_SEQ_LEN); a table id outside the pool gives slot -1
+ *   (PKA_DEVERR_BAD_TABLE).  max_query_len > 64: PKA_ERR_UNSUPPORTED. */
+int paged_tree_plan(const int32_t* parents, const int32_t* query_start_loc,
+                    const int32_t* seq_lens, const int32_t* total_lens,
+                    const int32_t* block_tables, int32_t max_blocks, int32_t num_blocks, int32_t B,
+                    int32_t total_q, int32_t max_query_len, uint64_t* tree_masks,
+                    int32_t* positions, int32_t* slots, int32_t* err, void* stream);
+
+/* Attention of drafted tokens: as paged_prefill_attn (arguments, head mapping,
+ * scale, cap, table and length errors), but query i of a request sees
+ *   - key t < L - n iff window <= 0 or t > p_i - window, with the position
+ *     p_i = L - n + max(d_i, 1) - 1, d_i the bits of its mask below n;
+ *   - key L - n + j (j < n) iff bit j of tree_masks[row] is set and window <= 0
+ *     or d_i - d_j < window.
+ * The masks need not come from a tree.  No visible key: output 0; visible
+ * logits that are all -infinity: NaN.  Infinities and NaN in K or V reach the
+ * queries that see them and no others.  Rows of no request are not written.
+ * Keys are cache positions: with a window the cache has to hold the sequence
+ * unevicted.
+ * One launch, or two: the segments (request, KV head, tile of 128 / G or 64 / G
+ * query tokens) are streamed in equal chunks of their keys, one per SM, and what
+ * a chunk cuts is merged in key order by the second launch (the same bits every
+ * time).  Where max_seq_len and the number of segments allow no cut there is no
+ * second launch.  max_seq_len is a promise; longer rows are computed all the same.
+ * workspace: 16-byte aligned, at least paged_tree_attn_ws_bytes() bytes (which
+ * depend on no length and no batch), needs no initialisation.  Calls sharing one
+ * workspace must not overlap on the GPU.
+ * tree_masks 8-byte aligned.  max_query_len > 64: PKA_ERR_UNSUPPORTED.
+ * PKA_ERR_SHAPE if the segments times (visible blocks of a table row + 4) exceed
+ * 2^30, or num_blocks * Hkv * 16 exceeds 2^31 - 1. */
+size_t paged_tree_attn_ws_bytes(int32_t Hq, int32_t Hkv, int32_t D, int32_t max_query_len);
+int paged_tree_attn_ws(const void* q, void* out, const pka_kv_pool* kv,
+                       const int32_t* block_tables, int32_t max_blocks,
+                       const int32_t* query_start_loc, const uint64_t* tree_masks,
+                       const int32_t* seq_lens, int32_t B, int32_t Hq, int32_t total_q,
+                       int32_t max_query_len, int32_t max_seq_len, const pka_attn_params* params,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Acceptance of drafted tokens.  Walk of each tree: from token 0, while a token
+ * c (the lowest) has parents[c] = the current one and tokens[c] = targets[the
+ * current one], go to c.  targets int32 [total_q] are the target model's next
+ * tokens after each drafted one: its most probable tokens, or samples of its
+ * distribution (which makes the accepted text a sample of it, too).
+ *   path         int32 [B][max_query_len]: the walk's tokens (indexes within the
+ *                tree, the first is 0), -1 after the last;
+ *   accepted     int32 [B]: their number (n = 0: 0);
+ *   next_tokens  int32 [B]: the target's token after the last one (n = 0: -1),
+ *                root of the next step's tree;
+ *   new_seq_lens int32 [B]: L - n + accepted (may be seq_lens itself).
+ * In each of num_pools bf16 pools (host array; K and V of every layer) the K/V
+ * rows of the walk's tokens move to the tree's first slots, so that the cache
+ * goes on without a gap: the row at slots[path[k]] to slots[k], both of the
+ * request's rows of `slots` (paged_tree_plan); pairs with a negative slot are
+ * left out, a slot past the pool ORs PKA_DEVERR_BAD_TABLE into *err.  The slots
+ * of all trees must be distinct.  num_pools = 0: the walk alone (slots and the
+ * pools' sizes are not looked at).  A bad span leaves a request as if n = 0
+ * (PKA_DEVERR_QUERY_LOC).  num_kv_heads at most 1024. */
+int paged_tree_accept(void* const* pools, int32_t num_pools, int32_t num_blocks,
+                      int32_t num_kv_heads, int32_t block_size, int32_t head_dim,
+                      const int32_t* parents, const int32_t* tokens, const int32_t* targets,
+                      const int32_t* slots, const int32_t* query_start_loc,
+                      const int32_t* seq_lens, int32_t B, int32_t total_q, int32_t max_query_len,
+                      int32_t* path, int32_t* accepted, int32_t* next_tokens,
+                      int32_t* new_seq_lens, int32_t* err, void* stream);
+
+/* H2O eviction ("Eviction policies -- Pluggable per-session: LRU, AttentionSink,
+ * H2O", github README, "What's inside"): holds the cache of each (layer,
+ * request, KV head) to `budget` keys by the mass that paged_decode_key_mass
+ * gathers.
+ *   key_mass, key_pos  fp32 and int32 [num_layers][B][Hkv][max_blocks * 16]: a
+ *            key's mass and its position in the sequence; position -1: a key
+ *            appended since the last eviction (key t of L then has position
+ *            T - L + t, T = total_lens[b], NULL: L; T >= L).  Before its first
+ *            eviction a request's positions are all -1.
+ * Of the L keys n = min(L, budget) stay: first the keys at positions below
+ * `sinks` or from T - `recent` on, lowest index first, then the others by mass
+ * (NaN below everything), ties to the lowest index.  Kept keys with an index of
+ * n or more move, with mass and position, to the indexes below n that do not
+ * stay: the highest of them to the lowest such index, and so on.  (Their order in
+ * the cache does not matter to decode without a window.)  Then
+ *   new_mass, new_pos  (may be key_mass, key_pos) hold the kept keys in [0, n)
+ *            with their positions, 0 and -1 in [n, L), entries from L on as they
+ *            were;
+ *   new_seq_lens int32 [B] (may be seq_lens) = n;
+ *   pools    (host array of 2 * num_layers bf16 pools: K and V of each layer) hold
+ *            the kept rows; rows from n on keep their contents, and their blocks
+ *            can be given back (paged_kv_ref_blocks with the old lengths and -1,
+ *            then with the new ones and +1).
+ * refcounts (NULL: not looked at) int32 [num_blocks]: a request of whose blocks
+ * below n one has a count above 1 is left whole (n = L): it shares them with
+ * another request, which would see its rows move (copy them first,
+ * paged_kv_copy_blocks).  Without refcounts those blocks must be the request's own.
+ * 1 <= budget, sinks + recent <= budget.  A length outside [0, max_blocks * 16]
+ * is clamped, T < L taken as L (PKA_DEVERR_SEQ_LEN); a table id outside the pool
+ * leaves its rows unmoved (PKA_DEVERR_BAD_TABLE).
+ * workspace: 4-byte aligned, at least paged_kv_evict_ws_bytes() bytes, needs no
+ * initialisation; calls sharing one must not overlap on the GPU. */
+size_t paged_kv_evict_ws_bytes(int32_t num_layers, int32_t B, int32_t Hkv, int32_t max_blocks,
+                               int32_t budget);
+int paged_kv_evict(void* const* pools, int32_t num_layers, int32_t num_blocks,
+                   int32_t num_kv_heads, int32_t block_size, int32_t head_dim,
+                   const int32_t* block_tables, int32_t max_blocks, const int32_t* seq_lens,
+                   const int32_t* total_lens, int32_t B, int32_t budget, int32_t sinks,
+                   int32_t recent, const float* key_mass, float* new_mass, const int32_t* key_pos,
+                   int32_t* new_pos, int32_t* new_seq_lens, const int32_t* refcounts,
+                   void* workspace, size_t workspace_bytes, int32_t* err, void* stream);
 
 #ifdef __cplusplus
 }

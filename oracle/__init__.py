@@ -15,3 +15,7 @@ from .key_mass import key_mass  # noqa: F401
 from .rope_norm import rms_norm, rope, kv_append_rope  # noqa: F401
 from .kv4 import kv4_append, kv4_decode, kv4_place, kv4_quantise  # noqa: F401
 from .pages import compact, copy_blocks, ref_blocks  # noqa: F401
+from .draft_tree import (  # noqa: F401
+    ancestors, tree_accept, tree_attention, tree_move, tree_plan, tree_visible,
+)
+from .evict import evict, evict_plan  # noqa: F401

@@ -29,6 +29,7 @@ DEVERR_TIMEOUT = 2
 DEVERR_SEQ_LEN = 4
 DEVERR_QUERY_LOC = 8
 DEVERR_REFCOUNT = 16
+DEVERR_TREE = 32
 
 EXPORTS = [
     "pka_version", "pka_status_string", "paged_decode_attn", "paged_decode_splitk_plan",
@@ -39,7 +40,8 @@ EXPORTS = [
     "paged_kv_append_rope", "paged_prefill_attn_ws_bytes", "paged_prefill_attn_ws",
     "pka_selftest_bounded_wait", "paged_kv4_pool_bytes", "paged_kv4_append", "paged_kv4_expand",
     "paged_kv4_decode_attn_ws_bytes", "paged_kv4_decode_attn_ws", "paged_kv_ref_blocks",
-    "paged_kv_copy_blocks", "paged_kv_compact",
+    "paged_kv_copy_blocks", "paged_kv_compact", "paged_tree_plan", "paged_tree_attn_ws_bytes",
+    "paged_tree_attn_ws", "paged_tree_accept", "paged_kv_evict_ws_bytes", "paged_kv_evict",
 ]
 
 KV4_UNIT_BYTES = 1152  # 16 tokens x 128 channels of a 4-bit pool
@@ -155,6 +157,21 @@ def lib() -> ctypes.CDLL:
     L.paged_kv_copy_blocks.argtypes = [VP, I32, I32, I64, VP, VP, I32, VP, VP]
     L.paged_kv_compact.restype = ctypes.c_int
     L.paged_kv_compact.argtypes = [VP, I32, I32, I64, VP, VP, VP, VP, I32, VP, I32, VP, VP, VP, VP]
+    L.paged_tree_plan.restype = ctypes.c_int
+    L.paged_tree_plan.argtypes = [VP, VP, VP, VP, VP, I32, I32, I32, I32, I32, VP, VP, VP, VP, VP]
+    L.paged_tree_attn_ws_bytes.restype = ctypes.c_size_t
+    L.paged_tree_attn_ws_bytes.argtypes = [I32, I32, I32, I32]
+    L.paged_tree_attn_ws.restype = ctypes.c_int
+    L.paged_tree_attn_ws.argtypes = [VP, VP, P(PkaKvPool), VP, I32, VP, VP, VP, I32, I32, I32, I32,
+                                     I32, P(PkaAttnParams), VP, ctypes.c_size_t, VP]
+    L.paged_tree_accept.restype = ctypes.c_int
+    L.paged_tree_accept.argtypes = [VP, I32, I32, I32, I32, I32, VP, VP, VP, VP, VP, VP, I32, I32,
+                                    I32, VP, VP, VP, VP, VP, VP]
+    L.paged_kv_evict_ws_bytes.restype = ctypes.c_size_t
+    L.paged_kv_evict_ws_bytes.argtypes = [I32, I32, I32, I32, I32]
+    L.paged_kv_evict.restype = ctypes.c_int
+    L.paged_kv_evict.argtypes = [VP, I32, I32, I32, I32, I32, VP, I32, VP, VP, I32, I32, I32, I32,
+                                 VP, VP, VP, VP, VP, VP, VP, ctypes.c_size_t, VP, VP]
     _lib = L
     return L
 
@@ -621,6 +638,181 @@ def paged_kv_compact(pools, refcounts, block_tables, seq_lens, new_refcounts, ne
         _raw_stream(dev, stream))
     if st != PKA_OK:
         raise PagedAttnError("paged_kv_compact", st)
+
+
+# ------------------------------------- draft trees and eviction by mass
+def paged_tree_plan(parents, query_start_loc, seq_lens, block_tables, num_blocks: int,
+                    max_query_len: int, tree_masks, positions, slots, *, total_lens=None, err=None,
+                    stream=None):
+    """Ancestor masks (int64 [total_q]), positions and cache slots (int32) of
+    drafted tokens from their ``parents`` (int32 [total_q], indexes within a
+    tree, -1: none).  An output may be None."""
+    import torch
+    dev = _cuda_device(parents, "parents")
+    i32, B, rows, width = torch.int32, seq_lens.shape[0], parents.shape[0], block_tables.shape[-1]
+    _tensor(parents, "parents", i32, dev, (rows,))
+    _tensor(query_start_loc, "query_start_loc", i32, dev, (B + 1,))
+    _tensor(seq_lens, "seq_lens", i32, dev, (B,))
+    _tensor(block_tables, "block_tables", i32, dev, (B, width))
+    if total_lens is not None:
+        _tensor(total_lens, "total_lens", i32, dev, (B,))
+    if tree_masks is not None:
+        _tensor(tree_masks, "tree_masks", torch.int64, dev, (rows,))
+    if positions is not None:
+        _tensor(positions, "positions", i32, dev, (rows,))
+    if slots is not None:
+        _tensor(slots, "slots", i32, dev, (rows,))
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return paged_tree_plan(parents, query_start_loc, seq_lens, block_tables, num_blocks,
+                                   max_query_len, tree_masks, positions, slots,
+                                   total_lens=total_lens, err=err, stream=stream)
+    st = lib().paged_tree_plan(
+        parents.data_ptr(), query_start_loc.data_ptr(), seq_lens.data_ptr(), _ptr(total_lens),
+        block_tables.data_ptr(), width, int(num_blocks), B, rows, int(max_query_len),
+        _ptr(tree_masks), _ptr(positions), _ptr(slots), None if err is None else _err(err, dev),
+        _raw_stream(dev, stream))
+    if st != PKA_OK:
+        raise PagedAttnError("paged_tree_plan", st)
+
+
+def paged_tree_attn_ws_bytes(Hq, Hkv, D, max_query_len) -> int:
+    return int(lib().paged_tree_attn_ws_bytes(Hq, Hkv, D, int(max_query_len)))
+
+
+def paged_tree_attn_ws(q, out, k_pool, v_pool, block_tables, query_start_loc, tree_masks, seq_lens,
+                       max_query_len, max_seq_len, workspace, *, scale, softcap=0.0, window=0,
+                       err=None, stream=None):
+    """Attention of drafted tokens over their requests' cached prefixes and, by
+    ``tree_masks`` (int64 [total_q], bit j: token j), each other: ``q``, ``out``
+    bf16 [total_q][Hq][D].  ``workspace``: device bytes, at least
+    ``paged_tree_attn_ws_bytes``; not to be shared by calls that can overlap."""
+    import torch
+    dev = _cuda_device(q, "q")
+    bf16, i32, B, width = torch.bfloat16, torch.int32, seq_lens.shape[0], block_tables.shape[-1]
+    rows, _, d = shape = q.shape
+    pool = k_pool.shape
+    _tensor(q, "q", bf16, dev, shape)
+    _tensor(out, "out", bf16, dev, shape)
+    if len(pool) != 4 or pool[2] != 16 or pool[3] != d:
+        _refuse(k_pool, "k_pool", f"bfloat16 [num_blocks][Hkv][16][{d}]")
+    _tensor(k_pool, "k_pool", bf16, dev, pool)
+    _tensor(v_pool, "v_pool", bf16, dev, pool)
+    _tensor(block_tables, "block_tables", i32, dev, (B, width))
+    _tensor(query_start_loc, "query_start_loc", i32, dev, (B + 1,))
+    _tensor(tree_masks, "tree_masks", torch.int64, dev, (rows,))
+    _tensor(seq_lens, "seq_lens", i32, dev, (B,))
+    _tensor(workspace, "workspace", workspace.dtype, dev, workspace.shape)
+    kv = PkaKvPool(k_pool.data_ptr(), v_pool.data_ptr(), *pool)
+    par = PkaAttnParams(scale, softcap, window, None if err is None else _err(err, dev))
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return paged_tree_attn_ws(q, out, k_pool, v_pool, block_tables, query_start_loc,
+                                      tree_masks, seq_lens, max_query_len, max_seq_len, workspace,
+                                      scale=scale, softcap=softcap, window=window, err=err,
+                                      stream=stream)
+    st = lib().paged_tree_attn_ws(
+        q.data_ptr(), out.data_ptr(), ctypes.byref(kv), block_tables.data_ptr(), width,
+        query_start_loc.data_ptr(), tree_masks.data_ptr(), seq_lens.data_ptr(), B, shape[1], rows,
+        int(max_query_len), int(max_seq_len), ctypes.byref(par), workspace.data_ptr(),
+        workspace.nbytes, _raw_stream(dev, stream))
+    if st != PKA_OK:
+        raise PagedAttnError("paged_tree_attn_ws", st)
+
+
+def _kv_pools(pools):
+    """Checks bf16 pools [num_blocks][Hkv][16][D] of one shape: their pointers, shape, device."""
+    import torch
+    first = pools[0]
+    if first.dtype is not torch.bfloat16 or first.dim() != 4:
+        _refuse(first, "pools", "bfloat16 [num_blocks][Hkv][16][D]")
+    ptrs, _, _, dev = _pool_list(pools)
+    return ptrs, first.shape, dev
+
+
+def paged_tree_accept(pools, parents, tokens, targets, slots, query_start_loc, seq_lens, path,
+                      accepted, next_tokens, new_seq_lens, err=None, stream=None):
+    """Walk each tree along the target model's tokens (``targets``, one after
+    each drafted token) and move the accepted tokens' rows in ``pools`` (bf16, K
+    and V of every layer) to the tree's first ``slots``.  Writes ``path`` (int32
+    [B][max_query_len]), ``accepted``, ``next_tokens`` and ``new_seq_lens``
+    (may be ``seq_lens``).  Without pools the walk alone (``slots`` may be None)."""
+    import torch
+    ptrs, shape, dev = _kv_pools(pools) if pools else (None, (0, 0, 0, 0),
+                                                       _cuda_device(parents, "parents"))
+    i32, B, rows = torch.int32, seq_lens.shape[0], parents.shape[0]
+    width = path.shape[-1]
+    _tensor(parents, "parents", i32, dev, (rows,))
+    _tensor(tokens, "tokens", i32, dev, (rows,))
+    _tensor(targets, "targets", i32, dev, (rows,))
+    if pools or slots is not None:
+        _tensor(slots, "slots", i32, dev, (rows,))
+    _tensor(query_start_loc, "query_start_loc", i32, dev, (B + 1,))
+    _tensor(seq_lens, "seq_lens", i32, dev, (B,))
+    _tensor(path, "path", i32, dev, (B, width))
+    _tensor(accepted, "accepted", i32, dev, (B,))
+    _tensor(next_tokens, "next_tokens", i32, dev, (B,))
+    _tensor(new_seq_lens, "new_seq_lens", i32, dev, (B,))
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return paged_tree_accept(pools, parents, tokens, targets, slots, query_start_loc,
+                                     seq_lens, path, accepted, next_tokens, new_seq_lens, err,
+                                     stream)
+    st = lib().paged_tree_accept(
+        ptrs, len(pools), *shape, parents.data_ptr(), tokens.data_ptr(), targets.data_ptr(),
+        _ptr(slots), query_start_loc.data_ptr(), seq_lens.data_ptr(), B, rows, width,
+        path.data_ptr(), accepted.data_ptr(), next_tokens.data_ptr(), new_seq_lens.data_ptr(),
+        None if err is None else _err(err, dev), _raw_stream(dev, stream))
+    if st != PKA_OK:
+        raise PagedAttnError("paged_tree_accept", st)
+
+
+def paged_kv_evict_ws_bytes(num_layers, B, Hkv, max_blocks, budget) -> int:
+    return int(lib().paged_kv_evict_ws_bytes(num_layers, B, Hkv, max_blocks, int(budget)))
+
+
+def paged_kv_evict(pools, key_mass, key_pos, block_tables, seq_lens, total_lens, budget: int,
+                   sinks: int, recent: int, new_mass, new_pos, new_seq_lens, workspace, *,
+                   refcounts=None, err=None, stream=None):
+    """Hold every (layer, request, KV head) of a cache to ``budget`` keys: those
+    at positions below ``sinks``, the ``recent`` last ones and the heaviest by
+    ``key_mass`` (fp32 [layers][B][Hkv][max_blocks * 16]; ``key_pos`` int32, -1:
+    appended since the last eviction).  Rows move in ``pools`` (bf16, K and V of
+    layer 0, 1, ...); the outputs may be the inputs.  ``total_lens`` None: the
+    sequences' lengths are their caches'.  With ``refcounts`` requests that share
+    a block to be written are left whole.  ``workspace``: device bytes, at least
+    ``paged_kv_evict_ws_bytes``; not to be shared by calls that can overlap."""
+    import torch
+    ptrs, pool, dev = _kv_pools(pools)
+    i32, B, width = torch.int32, seq_lens.shape[0], block_tables.shape[-1]
+    shape = (len(pools) // 2, B, pool[1], width * 16)
+    if len(pools) % 2:
+        raise ValueError(f"pools: K and V of each layer are wanted, got {len(pools)} pools")
+    _tensor(key_mass, "key_mass", torch.float32, dev, shape)
+    _tensor(new_mass, "new_mass", torch.float32, dev, shape)
+    _tensor(key_pos, "key_pos", i32, dev, shape)
+    _tensor(new_pos, "new_pos", i32, dev, shape)
+    _tensor(block_tables, "block_tables", i32, dev, (B, width))
+    _tensor(seq_lens, "seq_lens", i32, dev, (B,))
+    _tensor(new_seq_lens, "new_seq_lens", i32, dev, (B,))
+    _tensor(workspace, "workspace", workspace.dtype, dev, workspace.shape)
+    if total_lens is not None:
+        _tensor(total_lens, "total_lens", i32, dev, (B,))
+    if refcounts is not None:
+        _tensor(refcounts, "refcounts", i32, dev, (pool[0],))
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return paged_kv_evict(pools, key_mass, key_pos, block_tables, seq_lens, total_lens,
+                                  budget, sinks, recent, new_mass, new_pos, new_seq_lens, workspace,
+                                  refcounts=refcounts, err=err, stream=stream)
+    st = lib().paged_kv_evict(
+        ptrs, shape[0], *pool, block_tables.data_ptr(), width, seq_lens.data_ptr(),
+        _ptr(total_lens), B, int(budget), int(sinks), int(recent), key_mass.data_ptr(),
+        new_mass.data_ptr(), key_pos.data_ptr(), new_pos.data_ptr(), new_seq_lens.data_ptr(),
+        _ptr(refcounts), workspace.data_ptr(), workspace.nbytes,
+        None if err is None else _err(err, dev), _raw_stream(dev, stream))
+    if st != PKA_OK:
+        raise PagedAttnError("paged_kv_evict", st)
 
 
 # ------------------------------------------------------------ batch runners

@@ -108,6 +108,25 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int32_
   return mbar_wait_budget(bar, parity, err, kWaitBudgetCycles);
 }
 
+// Roles of a warp-specialised CTA: *failed tells every role that a wait ran
+// out, so that all of them stop.
+__device__ __forceinline__ bool stop_requested(const volatile int* flag) { return *flag != 0; }
+
+__device__ __forceinline__ bool cta_wait(uint64_t* bar, uint32_t parity, int32_t* err,
+                                         volatile int* failed) {
+  if (mbar_wait(bar, parity, err)) return true;
+  *failed = 1;
+  return false;
+}
+
+// Every lane waits; the warp agrees on one outcome so that it never diverges.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* err,
+                                          volatile int* failed) {
+  const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, err));
+  if (!ok) *failed = 1;
+  return ok;
+}
+
 // ------------------------------------------------------- bulk copy (TMA)
 // 1-D bulk copy global -> shared, completion counted on an mbarrier.  Both
 // addresses 16-byte aligned, bytes a multiple of 16.

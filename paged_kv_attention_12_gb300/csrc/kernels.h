@@ -101,6 +101,114 @@ cudaError_t launch_mixed(const PrefillArgs& pa, const DecodeArgs& da, int head_d
 // Query tokens per 128-row prefill tile (0: unsupported shape).
 int mixed_query_tile(int head_dim, int group);
 
+// Attention of drafted tokens that form trees.
+constexpr int kTreeMaxCtas = 160;  // CTAs (and chunks of the work line) at most
+struct TreeArgs {
+  const uint16_t* q;               // bf16 [total_q][Hq][D]
+  uint16_t* out;                   // bf16 [total_q][Hq][D]
+  const uint16_t* k;               // bf16 [num_blocks][Hkv][bs][D]
+  const uint16_t* v;
+  const int32_t* tables;
+  const int32_t* query_start_loc;  // [B+1]
+  const unsigned long long* masks; // [total_q]: bit j: drafted token j is seen
+  const int32_t* seq_lens;
+  int32_t* err;
+  float* partial_o;                // fp32 [2 * CTAs][D/4][rows][4]
+  float* partial_lse;              // fp32 [2 * CTAs][rows], log2 domain
+  int4* cuts;                      // [CTAs]: the cut segment that begins in the chunk: first
+                                   // query row, first head, rows, pieces (0: none)
+  int32_t batch, Hq, Hkv, num_blocks, max_blocks, total_q, max_query_len;
+  int32_t min_chunk;               // shortest chunk of the work line, in units
+  int32_t whole_slack;             // segments stay whole when none has more units than a
+                                   // chunk and this many
+  int32_t may_cut;                 // 0: every segment stays whole (there are no more than CTAs)
+  float scale, softcap;
+  int32_t window;
+};
+
+struct TreeMergeArgs {
+  const float* partial_o;
+  const float* partial_lse;
+  const int4* cuts;
+  uint16_t* out;
+  int32_t Hq, log2_g, chunks;
+};
+
+// Rows of a query tile for trees of at most max_query_len tokens.
+int tree_tile_rows(int max_query_len, int group);
+
+cudaError_t launch_tree_attn(const TreeArgs& a, int head_dim, int sm_count, cudaStream_t stream);
+
+// Masks, positions and slots of drafted tokens from their trees.
+struct TreePlanArgs {
+  const int32_t* parents;          // [total_q]
+  const int32_t* query_start_loc;  // [B+1]
+  const int32_t* seq_lens;
+  const int32_t* total_lens;       // or null: seq_lens
+  const int32_t* tables;
+  unsigned long long* masks;       // [total_q], or null
+  int32_t* positions;              // [total_q], or null
+  int32_t* slots;                  // [total_q], or null
+  int32_t* err;
+  int32_t batch, num_blocks, max_blocks, total_q, max_query_len;
+};
+
+cudaError_t launch_tree_plan(const TreePlanArgs& a, cudaStream_t stream);
+
+// Walk of the trees along the target's tokens, and the move of the accepted
+// tokens' K/V rows.
+constexpr int kMaxTreePools = 256;  // pools per launch
+struct TreeAcceptArgs {
+  void* pools[kMaxTreePools];
+  const int32_t* parents;          // [total_q]
+  const int32_t* tokens;           // [total_q]
+  const int32_t* targets;          // [total_q]
+  const int32_t* slots;            // [total_q]
+  const int32_t* query_start_loc;  // [B+1]
+  const int32_t* seq_lens;
+  int32_t* path;                   // [B][max_query_len]
+  int32_t* accepted;               // [B]
+  int32_t* next_tokens;            // [B]
+  int32_t* new_seq_lens;           // [B], may be seq_lens; all four null: rows only
+  int32_t* err;
+  int32_t num_pools, batch, total_q, max_query_len, num_blocks, Hkv, head_dim;
+};
+
+cudaError_t launch_tree_accept(const TreeAcceptArgs& a, cudaStream_t stream);
+
+// Eviction by accumulated attention weight.  Segments are (layer, request, KV
+// head), in that order.
+struct EvictArgs {
+  const float* mass;               // [segments][max_blocks * 16]
+  const int32_t* pos;
+  float* new_mass;                 // may be mass
+  int32_t* new_pos;                // may be pos
+  const int32_t* tables;
+  const int32_t* seq_lens;
+  const int32_t* total_lens;       // or null: seq_lens
+  const int32_t* refcounts;        // or null
+  int32_t* new_seq_lens;           // [B], may be seq_lens
+  int32_t* err;
+  int32_t* counts;                 // workspace: [segments] moves,
+  int32_t* kept;                   // [B] keys that stay,
+  int32_t* move_src;               // [segments][max_moves] and so on
+  int32_t* move_dst;
+  float* move_mass;
+  int32_t* move_pos;
+  int32_t batch, Hkv, num_blocks, max_blocks, budget, sinks, recent, max_moves;
+};
+
+constexpr int kMaxEvictLayers = 128;  // layers per launch of the moves
+struct EvictMoveArgs {
+  EvictArgs a;
+  void* pools[2 * kMaxEvictLayers];   // K and V of layers first_layer, first_layer + 1, ...
+  int32_t first_layer, layers;
+};
+
+cudaError_t launch_evict_select(const EvictArgs& a, int layers, cudaStream_t stream);
+cudaError_t launch_evict_move(const EvictMoveArgs& m, int head_dim, int sm_count,
+                              cudaStream_t stream);
+
 // Append of new tokens' K/V rows into a pool.
 struct AppendArgs {
   const uint16_t* k_new;        // bf16 [T][Hkv][D]

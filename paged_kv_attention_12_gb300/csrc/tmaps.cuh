@@ -30,7 +30,7 @@ inline bool tmap_bf16(CUtensorMap* m, const void* base, int rank, const cuuint64
                       const cuuint64_t* strides_bytes, const cuuint32_t* box) {
   auto fn = tmap_encode_fn();
   if (fn == nullptr) return false;
-  const cuuint32_t estr[3] = {1, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims,
             strides_bytes, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -58,6 +58,20 @@ inline bool tmap_pool_tiles_chunks(CUtensorMap* m, const void* base, int D, long
   const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(kBlockSize),
                              static_cast<cuuint32_t>(nchunks)};
   return tmap_bf16(m, base, 3, dims, str, box);
+}
+
+// A pool viewed as 8-row groups: a 4-D tensor (64 columns, 8 rows, D / 64
+// column chunks, num_blocks * Hkv * 2 groups) read in boxes of one (block,
+// head) tile.  Shared memory gets [group][chunk][8 rows][128 bytes], so that
+// both the 8-row groups of a chunk and the chunks of a group lie a fixed
+// distance apart over any number of blocks: one copy per block serves K (read
+// along the columns) and V (read along the rows) alike.
+inline bool tmap_pool_groups(CUtensorMap* m, const void* base, int D, long long rows) {
+  const cuuint64_t dims[4] = {64, 8, static_cast<cuuint64_t>(D / 64),
+                              static_cast<cuuint64_t>(rows / 8)};
+  const cuuint64_t str[3] = {static_cast<cuuint64_t>(D) * 2, 128, static_cast<cuuint64_t>(D) * 16};
+  const cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(D / 64), 2};
+  return tmap_bf16(m, base, 4, dims, str, box);
 }
 
 // q [total_q][Hq][D] as a 3-D tensor (D, Hq, total_q) read in boxes of

@@ -1,0 +1,969 @@
+// Attention of drafted tokens that form a tree over a block-paged cache
+// (sm_103a): tcgen05 + TMEM + TMA.
+//
+// A step of speculative decoding verifies n <= 64 drafted tokens per request.
+// Each of them sees the whole cached prefix and, of the drafted tokens, those
+// of its mask (itself and its ancestors in the tree).  Every key is read once
+// for all n tokens and all G heads of its KV head: n * G rows per 2 * 2 D
+// bytes, so HBM bounds the operator up to a few hundred rows.
+//
+// A row tile packs QR / G tokens x G heads (row = token * G + head) into the
+// rows of a 128-row MMA; QR = 64 leaves the room of the upper 64 rows of Q to
+// the key stages (the MMA reads them from what follows in shared memory; a
+// row's garbage stays in its row).  Work partition: a segment is one (request,
+// KV head, row tile) with nb visible blocks; on a line of work units it takes
+// kPieceUnits (a piece's fixed cost) and then one unit per block.  The line is
+// cut into equal chunks, one per CTA, one CTA per SM.  A segment inside a
+// chunk writes its output; the pieces of a cut one leave softmax-normalised
+// fp32 rows and their log-sum-exp in the workspace, which the combine launch
+// merges in key order.
+//
+// Warps of a CTA: QR / 32 softmax warps (thread r owns row r, its S and O
+// rows in TMEM lane r), one TMA warp each for K, V and Q, and one that issues
+// the MMAs.  The rings of K and V run on over the pieces of a chunk, so that
+// the loads do not stop for an epilogue.
+#include <cuda.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "overlap.cuh"
+#include "softmax_math.cuh"
+#include "tcgen05.cuh"
+#include "tmaps.cuh"
+
+namespace pka {
+
+namespace {
+
+constexpr int kPieceUnits = 4;  // fixed cost of a piece, in blocks
+
+template <int D_, int QR_>
+struct TreeShape {
+  static constexpr int D = D_, QR = QR_;
+  static constexpr int BN = (D == 256) ? 64 : 128;  // keys per key tile
+  static constexpr int BPT = BN / kBlockSize;
+  static constexpr int DC = D / 64;                 // 128-byte chunks of a row
+  static constexpr int kQChunk = QR * 128;
+  static constexpr int kQBytes = QR * D * 2;
+  static constexpr int kBlockBytes = kBlockSize * D * 2;  // [2 groups][D / 64][8 rows][128 B]
+  static constexpr int kStage = BN * D * 2;
+  static constexpr int kGroup = DC * 1024;          // stride of the 8-row groups
+  static constexpr int KST = 3;
+  static constexpr int VST = (kQBytes <= 32768) ? 3 : 2;
+  static constexpr int oQ = 0;
+  static constexpr int oK = kQBytes;
+  static constexpr int oV = oK + KST * kStage;
+  static constexpr int oEnd = oV + VST * kStage;
+  static constexpr int kSmemBytes = oEnd + 1024;    // slack to align the base to 1 KiB
+  static constexpr int kSoftmaxWarps = QR / 32;
+  static constexpr int kWarpK = kSoftmaxWarps, kWarpV = kWarpK + 1, kWarpMma = kWarpK + 2,
+                       kWarpQ = kWarpK + 3;
+  static constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
+  // TMEM columns: S_j (fp32) in buffer j % 2 at (j % 2) * BN, O at 256, P_j
+  // (bf16 pairs) in buffer j % 2 at kTmemP + (j % 2) * BN / 2.
+  static constexpr uint32_t kTmemO = 256;
+  static constexpr uint32_t kTmemP = (D == 256) ? 2 * BN : 256 + D;
+  static constexpr uint32_t kTmemCols = 512;
+  static_assert(kTmemP >= 2 * BN && (kTmemP + BN <= kTmemO || kTmemP >= kTmemO + D) &&
+                    kTmemP + BN <= kTmemCols && kTmemO + D <= kTmemCols,
+                "P buffers clear of S and O");
+  static_assert(kSmemBytes + 1536 <= 232448, "shared memory, the static part included");
+};
+
+struct TreeLaunch {
+  CUtensorMap tm_q, tm_k, tm_v;
+  TreeArgs a;
+  int32_t q_tokens;   // tokens of a Q box
+  int32_t log2_g;
+};
+
+// A request as the kernels take it: n query rows from q0 on, L keys (clamped
+// to the table); n = 0: nothing to do.
+struct Request {
+  int n, q0, L;
+};
+
+__device__ __forceinline__ Request request_of(const TreeArgs& a, int b, bool tell) {
+  Request r;
+  r.q0 = a.query_start_loc[b];
+  const int hi = a.query_start_loc[b + 1];
+  r.L = a.seq_lens[b];
+  r.n = 0;
+  if (r.q0 < 0 || hi < r.q0 || hi > a.total_q || hi - r.q0 > a.max_query_len) {
+    if (tell) report(a.err, PKA_DEVERR_QUERY_LOC);
+    return r;
+  }
+  if (r.L > a.max_blocks * kBlockSize) {
+    if (tell) report(a.err, PKA_DEVERR_SEQ_LEN);
+    r.L = a.max_blocks * kBlockSize;
+  }
+  if (hi - r.q0 > r.L) {
+    if (tell) report(a.err, PKA_DEVERR_SEQ_LEN);
+    return r;
+  }
+  r.n = hi - r.q0;
+  return r;
+}
+
+// First block that a query of the request sees (a query's position is at
+// least L - n).
+__device__ __forceinline__ int first_block(const TreeArgs& a, const Request& r) {
+  return a.window > 0 ? max(0, r.L - r.n - a.window + 1) / kBlockSize : 0;
+}
+
+template <int QR>
+__device__ __forceinline__ int row_tiles(const TreeLaunch& t, const Request& r) {
+  return ((r.n << t.log2_g) + QR - 1) / QR;
+}
+
+// A request's share of the work line: its units, its segments and the units
+// of one of them.
+struct Load {
+  int units, segs, len;
+};
+
+template <int QR>
+__device__ __forceinline__ Load load_of(const TreeLaunch& t, int b, bool tell) {
+  if (b >= t.a.batch) return Load{0, 0, 0};
+  const Request r = request_of(t.a, b, tell);
+  if (r.n == 0) return Load{0, 0, 0};
+  const int nb = (r.L + kBlockSize - 1) / kBlockSize - first_block(t.a, r);
+  const int segs = t.a.Hkv * row_tiles<QR>(t, r);
+  return Load{segs * (kPieceUnits + nb), segs, kPieceUnits + nb};
+}
+
+// Blocks [j0 + lo, j0 + hi) of a segment.
+struct Piece {
+  int b, kvh, tile;
+  int q0, n, L;      // the request
+  int j0, blocks;    // first block of the piece, and how many
+  int after;         // blocks of the segment after the piece
+  bool first;        // it begins with the segment's first block
+};
+
+// Walk over the pieces of a chunk; every warp of the CTA makes its own.
+struct Walk {
+  int b, off, rem;   // request, unit within it, units of the chunk that are left
+
+  template <int QR>
+  __device__ bool next(const TreeLaunch& t, Piece* p) {
+    while (rem > 0 && b < t.a.batch) {
+      const Request r = request_of(t.a, b, false);
+      const int tiles = row_tiles<QR>(t, r);
+      const int j0 = first_block(t.a, r);
+      const int nb = (r.L + kBlockSize - 1) / kBlockSize - j0;
+      const int seg = kPieceUnits + nb;
+      if (off >= t.a.Hkv * tiles * seg) {  // (tiles = 0 without query rows)
+        ++b;
+        off = 0;
+        continue;
+      }
+      const int item = off / seg;
+      const int at = off - item * seg;
+      const int take = min(seg - at, rem);
+      const int lo = max(at, kPieceUnits) - kPieceUnits;
+      const int hi = at + take - kPieceUnits;
+      off += take;
+      rem -= take;
+      if (hi <= lo) continue;
+      p->b = b;
+      p->kvh = item / tiles;
+      p->tile = item - p->kvh * tiles;
+      p->q0 = r.q0;
+      p->n = r.n;
+      p->L = r.L;
+      p->j0 = j0 + lo;
+      p->blocks = hi - lo;
+      p->after = nb - hi;
+      p->first = lo == 0;
+      return true;
+    }
+    return false;
+  }
+};
+
+// Block-wide exclusive scan; every thread gets the total.
+template <int NT>
+__device__ __forceinline__ int excl_scan(int x, int* warp_sums, int* total) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  int incl = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) warp_sums[warp] = incl;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    const int v = warp_sums[w];
+    if (w < warp) before += v;
+    all += v;
+  }
+  __syncthreads();
+  *total = all;
+  return before + incl - x;
+}
+
+// 64 columns from column c0 of the words m << at (at may be negative).
+__device__ __forceinline__ uint64_t shifted(uint64_t m, int at) {
+  if (at >= 64 || at <= -64) return 0;
+  return at >= 0 ? m << at : m >> -at;
+}
+// Bits [lo, hi) of a 64-bit word.
+__device__ __forceinline__ uint64_t bit_range(int lo, int hi) {
+  lo = max(lo, 0);
+  hi = min(hi, 64);
+  if (hi <= lo) return 0;
+  return (~0ull >> (64 - (hi - lo))) << lo;
+}
+
+// Whether either bf16 of a word is an infinity or a NaN.
+__device__ __forceinline__ bool wild(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ uint32_t tamed(uint32_t w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+  return w;
+}
+
+// What a query row sees: the prefix from key `kmin` up to `base`, and the
+// drafted keys of `mask`.
+struct Sight {
+  int kmin, base;
+  uint64_t mask;
+
+  __device__ __forceinline__ uint64_t columns(int t0) const {  // of keys [t0, t0 + 64)
+    return bit_range(kmin - t0, base - t0) | shifted(mask, base - t0);
+  }
+};
+
+// Adds the infinities and NaN of V's keys [lo, hi) that the row sees to its
+// finished output row (the tiles that not every row sees whole go through the
+// MMA with such values as zeros, which would reach the other rows as 0 * inf).
+template <int D, bool kPartial>
+__device__ __noinline__ void add_wild(const TreeArgs& a, const Piece& p, const Sight& see, int lo,
+                                      int hi, float* prow, int pstride, uint16_t* orow) {
+  const int32_t* trow = a.tables + static_cast<size_t>(p.b) * a.max_blocks;
+  for (int t = lo; t < hi; ++t) {
+    if (!(see.columns(t) & 1)) continue;
+    const int id = trow[t / kBlockSize];
+    if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.num_blocks)) continue;
+    const uint16_t* v = a.v + ((static_cast<size_t>(id) * a.Hkv + p.kvh) * kBlockSize +
+                               t % kBlockSize) * D;
+    for (int d = 0; d < D; ++d) {
+      const uint32_t bits = v[d];
+      if ((bits & 0x7f80u) != 0x7f80u) continue;
+      const float x = __uint_as_float(bits << 16);
+      if (kPartial)
+        prow[(d / 4) * pstride + d % 4] += x;
+      else
+        orow[d] = f32_to_bf16_rn(__uint_as_float(static_cast<uint32_t>(orow[d]) << 16) + x);
+    }
+  }
+}
+
+template <int D, int QR>
+__global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
+    tree_attn_kernel(const __grid_constant__ TreeLaunch t) {
+  using S = TreeShape<D, QR>;
+  constexpr int BN = S::BN, BPT = S::BPT, DC = S::DC, NW = S::kSoftmaxWarps;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t b_q, b_qfree, b_k[S::KST], b_kfree[S::KST], b_v[S::VST], b_vfree[S::VST],
+      b_s[2], b_pv[2], b_p[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int failed_flag, wild_piece[2], warp_sums[S::kThreads / 32], start_b, start_off,
+      start_rem, longest;
+  volatile int* failed = &failed_flag;
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* sQ = smem + S::oQ;
+  uint8_t* sK = smem + S::oK;
+  uint8_t* sV = smem + S::oV;
+  const TreeArgs& a = t.a;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  launch_dependents();
+  if (threadIdx.x == 0) {
+    mbar_init(&b_q, 1);
+    mbar_init(&b_qfree, 1);
+    for (int i = 0; i < S::KST; ++i) {
+      mbar_init(&b_k[i], 1);
+      mbar_init(&b_kfree[i], 1);
+    }
+    for (int i = 0; i < S::VST; ++i) {
+      mbar_init(&b_v[i], 1);
+      mbar_init(&b_vfree[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&b_s[i], 1);
+      mbar_init(&b_pv[i], 1);
+      mbar_init(&b_p[i], NW);
+    }
+    failed_flag = 0;
+    wild_piece[0] = wild_piece[1] = 0;
+    longest = 0;
+    mbar_fence_init();
+    prefetch_tensormap(&t.tm_q);
+    prefetch_tensormap(&t.tm_k);
+    prefetch_tensormap(&t.tm_v);
+  }
+  if (warp == S::kWarpMma) tmem_alloc(&tmem_slot, S::kTmemCols);
+  wait_predecessor();
+
+  // ------------------------------------------------------- the CTA's chunk
+  // Every CTA sums the requests' units and segments and finds the unit (or,
+  // where segments stay whole, the segment) that it begins with.
+  constexpr int NT = S::kThreads;
+  const int tid = threadIdx.x;
+  const int grid = static_cast<int>(gridDim.x);
+  Load mine = load_of<QR>(t, tid, blockIdx.x == 0);
+  int units = 0, segs = 0;
+  Load before{excl_scan<NT>(mine.units, warp_sums, &units),
+              excl_scan<NT>(mine.segs, warp_sums, &segs), 0};
+  int len = mine.len;
+  if (a.batch > NT) {
+    Load rest{0, 0, 0};
+    for (int b = tid + NT; b < a.batch; b += NT) {
+      const Load x = load_of<QR>(t, b, blockIdx.x == 0);
+      rest.units += x.units;
+      rest.segs += x.segs;
+      len = max(len, x.len);
+    }
+    int sum;
+    excl_scan<NT>(rest.units, warp_sums, &sum);
+    units += sum;
+    excl_scan<NT>(rest.segs, warp_sums, &sum);
+    segs += sum;
+  }
+  const int chunk = max(a.min_chunk, (units + grid - 1) / grid);
+  len = __reduce_max_sync(0xffffffffu, len);
+  if (lane == 0) atomicMax(&longest, len);
+  __syncthreads();
+  const bool whole = !a.may_cut || (segs <= grid && longest <= chunk + a.whole_slack);
+  // (where may_cut is false there are no more segments than CTAs)
+  const long long begin = static_cast<long long>(blockIdx.x) * (whole ? 1 : chunk);
+  Walk walk{0, 0, 0};
+  const bool any_work = begin < (whole ? segs : units);
+  if (any_work) {
+    const int want = static_cast<int>(begin);
+    auto look = [&](int b, const Load& x, int at_unit, int at_seg) {
+      const int at = whole ? at_seg : at_unit;
+      if (want >= at && want < at + (whole ? x.segs : x.units)) {
+        start_b = b;
+        start_off = (want - at) * (whole ? x.len : 1);
+        if (whole) start_rem = x.len;
+      }
+    };
+    look(tid, mine, before.units, before.segs);
+    if (a.batch > NT) {
+      int at_unit, at_seg, sum;
+      excl_scan<NT>(mine.units, warp_sums, &at_unit);
+      excl_scan<NT>(mine.segs, warp_sums, &at_seg);
+      for (int base = NT; base < a.batch && (whole ? at_seg : at_unit) <= want; base += NT) {
+        const Load x = load_of<QR>(t, base + tid, false);
+        const int u = at_unit + excl_scan<NT>(x.units, warp_sums, &sum);
+        at_unit += sum;
+        const int s = at_seg + excl_scan<NT>(x.segs, warp_sums, &sum);
+        at_seg += sum;
+        look(base + tid, x, u, s);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  if (any_work) {
+    walk.b = start_b;
+    walk.off = start_off;
+    walk.rem = whole ? start_rem : min(chunk, units - static_cast<int>(begin));
+  }
+  Piece p;
+
+  if (warp == S::kWarpK || warp == S::kWarpV) {
+    // ============================ TMA of K, V ============================
+    const bool is_k = warp == S::kWarpK;
+    const CUtensorMap* map = is_k ? &t.tm_k : &t.tm_v;
+    const int nst = is_k ? S::KST : S::VST;
+    uint8_t* ring = is_k ? sK : sV;
+    uint64_t* full = is_k ? b_k : b_v;
+    uint64_t* freed = is_k ? b_kfree : b_vfree;
+    const int past = a.num_blocks * a.Hkv * 2;  // a group past the pool: zeros
+    int g = 0;                                  // tiles issued
+    bool ok = true;
+    while (ok && walk.next<QR>(t, &p)) {
+      const int32_t* trow = a.tables + static_cast<size_t>(p.b) * a.max_blocks + p.j0;
+      // the piece's blocks, 32 at a time (one per lane), read 32 ahead
+      auto load_groups = [&](int base) -> int {
+        int at = past;
+        if (base + lane < p.blocks) {
+          const int id = trow[base + lane];
+          if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks))
+            at = (id * a.Hkv + p.kvh) * 2;
+          else
+            report(a.err, PKA_DEVERR_BAD_TABLE);
+        }
+        return at;
+      };
+      static_assert(32 % BPT == 0, "a tile's blocks lie in one window of 32");
+      int now = load_groups(0), next = load_groups(32);
+      for (int j = 0; j < p.blocks; j += BPT, ++g) {
+        if (j > 0 && j % 32 == 0) {
+          now = next;
+          next = load_groups(j + 32);
+        }
+        const int at = __shfl_sync(0xffffffffu, now, (j + lane % BPT) & 31);
+        const int st = g % nst;
+        if (g >= nst) ok = warp_wait(&freed[st], (g / nst - 1) & 1, a.err, failed);
+        if (!ok || __any_sync(0xffffffffu, stop_requested(failed))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], S::kStage);
+        __syncwarp();
+        if (lane < BPT)
+          tma_load_4d(ring + st * S::kStage + lane * S::kBlockBytes, map, 0, 0, 0, at, &full[st]);
+      }
+    }
+    // every copy must land before the CTA may end
+    if (lane == 0)
+      for (int j = max(0, g - nst); j < g; ++j) mbar_wait(&full[j % nst], (j / nst) & 1, a.err);
+    __syncwarp();
+  } else if (warp == S::kWarpQ) {
+    // =============================== TMA of Q ===============================
+    int pieces = 0;
+    while (walk.next<QR>(t, &p)) {
+      if (pieces > 0 && !warp_wait(&b_qfree, (pieces - 1) & 1, a.err, failed)) break;
+      if (__any_sync(0xffffffffu, stop_requested(failed))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&b_q, DC * (t.q_tokens << t.log2_g) * 128);
+#pragma unroll
+        for (int c = 0; c < DC; ++c)
+          tma_load_3d(sQ + c * S::kQChunk, &t.tm_q, c * 64, p.kvh << t.log2_g,
+                      p.q0 + p.tile * (QR >> t.log2_g), &b_q);
+      }
+      __syncwarp();
+      ++pieces;
+    }
+    if (lane == 0 && pieces > 0) mbar_wait(&b_q, (pieces - 1) & 1, a.err);
+    __syncwarp();
+  } else if (warp == S::kWarpMma) {
+    // ================================ MMA ================================
+    constexpr uint32_t idesc_qk = idesc_bf16_f32(128, BN, 0, 0);
+    constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 0, 1);
+    const uint32_t aQ = smem_u32(sQ), aK = smem_u32(sK), aV = smem_u32(sV);
+    int g = 0, issued_pv = 0, pieces = 0;
+    bool ok = true;
+    auto issue_qk = [&](int i, bool last) -> bool {
+      const int ks = i % S::KST;
+      if (!warp_wait(&b_k[ks], (i / S::KST) & 1, a.err, failed)) return false;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t kst = aK + ks * S::kStage;
+#pragma unroll
+        for (int c = 0; c < DC; ++c)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16(tmem + (i & 1) * BN, smem_desc_sw128(aQ + c * S::kQChunk + kk * 32, 16, 1024),
+                      smem_desc_sw128(kst + c * 1024 + kk * 32, 16, S::kGroup), idesc_qk,
+                      (c | kk) != 0);
+        umma_commit(&b_s[i & 1]);
+        umma_commit(&b_kfree[ks]);
+        if (last) umma_commit(&b_qfree);
+      }
+      __syncwarp();
+      return true;
+    };
+    while (ok && walk.next<QR>(t, &p)) {
+      const int nt = (p.blocks + BPT - 1) / BPT;
+      ok = warp_wait(&b_q, pieces & 1, a.err, failed);
+      ++pieces;
+      if (ok) ok = issue_qk(g, nt == 1);
+      if (ok && nt > 1) ok = issue_qk(g + 1, nt == 2);
+      for (int j = 0; ok && j < nt; ++j, ++g) {
+        const int st = g & 1, vs = g % S::VST;
+        ok = warp_wait(&b_v[vs], (g / S::VST) & 1, a.err, failed) &&
+             warp_wait(&b_p[st], (g >> 1) & 1, a.err, failed);
+        if (!ok || __any_sync(0xffffffffu, stop_requested(failed))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t vst = aV + vs * S::kStage;
+#pragma unroll
+          for (int k = 0; k < BPT; ++k)
+            umma_bf16_ts(tmem + S::kTmemO, tmem + S::kTmemP + st * (BN / 2) + k * 8,
+                         smem_desc_sw128(vst + k * S::kBlockBytes, 1024, S::kGroup), idesc_pv,
+                         (j > 0 || k > 0) ? 1u : 0u);
+          umma_commit(&b_pv[st]);
+          umma_commit(&b_vfree[vs]);
+        }
+        __syncwarp();
+        issued_pv = g + 1;
+        if (j + 2 < nt) ok = issue_qk(g + 2, j + 3 == nt);
+      }
+    }
+    // the last P V must have finished before TMEM is freed
+    if (issued_pv > 0) mbar_wait(&b_pv[(issued_pv - 1) & 1], ((issued_pv - 1) >> 1) & 1, a.err);
+    __syncwarp();
+  } else {
+    // ============================== softmax ==============================
+    const int r = threadIdx.x;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const bool capped = a.softcap > 0.f;
+    const float sl2 = a.scale * kLog2e;
+    // scale <= 0 and caps: the logits are formed before the mask
+    const bool prescale = capped || !(sl2 > 0.f);
+    const float cap_in = capped ? fmaxf(fminf(a.scale / a.softcap, kFltMax), -kFltMax) : 0.f;
+    const float cap_mag = fabsf(cap_in);
+    const float cap_out = a.softcap * kLog2e;
+    // x(s) = s (k1 + s^2 (k3 + k5 s^2)): the capped logit's short series, which
+    // grows with s for cap_in > 0 (so the maximum may be taken over raw s)
+    const float k1 = cap_in * cap_out;
+    const float k3 = -cap_in * cap_in * k1 * (1.f / 3.f);
+    const float k5 = 2.f * cap_in * cap_in * cap_in * cap_in * k1 * (1.f / 15.f);
+    const bool fold_ok = capped && cap_in > 0.f && k5 > 0.f && k5 <= kFltMax;
+    int g = 0, piece = 0;
+    bool ok = true;
+    int4 cut = make_int4(0, 0, 0, 0);  // this chunk's segment that goes on in the next one
+    while (ok && walk.next<QR>(t, &p)) {
+      ++piece;
+      const int row = p.tile * QR + r;
+      const int tok = row >> t.log2_g;
+      const bool row_valid = tok < p.n;
+      const bool idle = ((p.tile * QR + warp * 32) >> t.log2_g) >= p.n;  // no row of this warp
+      const int nt = (p.blocks + BPT - 1) / BPT;
+      const int t_begin = p.j0 * kBlockSize;
+      const int t_end = min(t_begin + p.blocks * kBlockSize, p.L);
+      Sight see{0x40000000, p.L - p.n, 0};
+      if (row_valid) {
+        const uint64_t own_bits = p.n == 64 ? ~0ull : (1ull << p.n) - 1;
+        const uint64_t* masks = reinterpret_cast<const uint64_t*>(a.masks) + p.q0;
+        see.mask = masks[tok] & own_bits;
+        const int deep = __popcll(see.mask);
+        see.kmin = a.window > 0 ? see.base + max(deep, 1) - a.window : 0;
+        if (a.window > 0 && a.window < 64) {  // ancestors may lie before the window
+          uint64_t left = see.mask;
+          while (left != 0) {
+            const int j = __ffsll(static_cast<long long>(left)) - 1;
+            left &= left - 1;
+            if (deep - __popcll(masks[j] & own_bits) >= a.window) see.mask &= ~(1ull << j);
+          }
+        }
+      }
+      // tiles that not every row sees whole: from the window's edge and from
+      // the drafted keys on
+      const int edge_lo = a.window > 0 ? p.L - a.window : 0;
+      const int edge_hi = see.base;
+      float m_ref = -INFINITY, l = 0.f;
+      bool seen = false;
+      for (int j = 0; j < nt; ++j, ++g) {
+        const int st = g & 1;
+        const uint32_t ph = (g >> 1) & 1;
+        const int t0 = t_begin + j * BN;
+        if (__any_sync(0xffffffffu, stop_requested(failed)) ||
+            !warp_wait(&b_s[st], ph, a.err, failed)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (t0 < edge_lo || t0 + BN > edge_hi) {
+          // V's rows past the sequence (stale) and its infinities and NaN
+          // become zeros; the latter are added to the rows that see them
+          const int vs = g % S::VST;
+          if (!warp_wait(&b_v[vs], (g / S::VST) & 1, a.err, failed)) {
+            ok = false;
+            break;
+          }
+          uint8_t* vst = sV + vs * S::kStage;
+          bool found = false;
+          for (int x = warp * 32 + lane; x < S::kStage / 16; x += NW * 32) {
+            const int off = x * 16;
+            const int key = t0 + off / S::kGroup * 8 + off % 1024 / 128;
+            uint4 w = *reinterpret_cast<const uint4*>(vst + off);
+            if (key >= p.L) {
+              *reinterpret_cast<uint4*>(vst + off) = make_uint4(0u, 0u, 0u, 0u);
+            } else if (wild(w.x) || wild(w.y) || wild(w.z) || wild(w.w)) {
+              found = true;
+              *reinterpret_cast<uint4*>(vst + off) =
+                  make_uint4(tamed(w.x), tamed(w.y), tamed(w.z), tamed(w.w));
+            }
+          }
+          if (found) *const_cast<volatile int*>(&wild_piece[piece & 1]) = piece;
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (!idle) {
+          float s[BN];
+#pragma unroll
+          for (int c = 0; c < BN / 64; ++c) {
+            float x[64];
+            tmem_ld64(lane_base + st * BN + c * 64, x);
+#pragma unroll
+            for (int e = 0; e < 64; ++e) s[c * 64 + e] = x[e];
+          }
+          uint64_t vis[BN / 64];
+          bool whole = true;
+#pragma unroll
+          for (int c = 0; c < BN / 64; ++c) {
+            vis[c] = row_valid ? see.columns(t0 + c * 64) & bit_range(0, t_end - t0 - c * 64) : 0;
+            whole = whole && vis[c] == ~0ull;
+            seen = seen || vis[c] != 0;
+          }
+          const bool need_mask = __any_sync(0xffffffffu, !whole);
+          bool folded = false, have_max = false;
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          if (capped) {
+            float n4[4] = {INFINITY, INFINITY, INFINITY, INFINITY};
+#pragma unroll
+            for (int c = 0; c < BN / 2; ++c) {
+              m4[c & 3] = max3f(m4[c & 3], s[2 * c], s[2 * c + 1]);
+              n4[c & 3] = min3f(n4[c & 3], s[2 * c], s[2 * c + 1]);
+            }
+            const float amax = fmaxf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])),
+                                     -fminf(fminf(n4[0], n4[1]), fminf(n4[2], n4[3])));
+            // the form of cap * tanh(s * scale / cap): a short or a long series
+            // while every argument of the warp is below 1/8 or 1/2, else exp2
+            if (fold_ok && __all_sync(0xffffffffu, amax * cap_mag < 0.125f)) {
+              folded = true;
+              have_max = !need_mask;
+            } else if (__all_sync(0xffffffffu, amax * cap_mag < 0.125f)) {
+#pragma unroll
+              for (int c = 0; c < BN; ++c) s[c] = cap_out * tanh_taylor_short(s[c] * cap_in);
+            } else if (__all_sync(0xffffffffu, amax * cap_mag < 0.5f)) {
+#pragma unroll
+              for (int c = 0; c < BN; ++c) s[c] = cap_out * tanh_taylor(s[c] * cap_in);
+            } else {
+#pragma unroll
+              for (int c = 0; c < BN; ++c) s[c] = cap_out * tanh_via_exp2(s[c] * cap_in);
+            }
+          } else if (prescale) {
+#pragma unroll
+            for (int c = 0; c < BN; c += 2) {
+              const float2 v = mul2(make_float2(s[c], s[c + 1]), make_float2(sl2, sl2));
+              s[c] = v.x;
+              s[c + 1] = v.y;
+            }
+          }
+          if (need_mask) {
+#pragma unroll
+            for (int c = 0; c < BN; ++c)
+              if (!((vis[c / 64] >> (c % 64)) & 1)) s[c] = -INFINITY;
+          }
+          if (!have_max) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m4[e] = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < BN / 2; ++c) m4[c & 3] = max3f(m4[c & 3], s[2 * c], s[2 * c + 1]);
+          }
+          float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          if (folded)
+            mx = mx * fmaf(mx * mx, fmaf(mx * mx, k5, k3), k1);
+          else if (!prescale)
+            mx *= sl2;
+          const float m_new = fmaxf(m_ref, mx);
+          // O moves to a new reference only when the maximum grows by more
+          // than 2^8: every weight stays below 2^8, and O and the sum share
+          // the reference, so the result does not depend on it
+          const bool resc = j > 0 && m_new > m_ref + 8.f;
+          if (__any_sync(0xffffffffu, resc)) {
+            if (!warp_wait(&b_pv[(g - 1) & 1], ((g - 1) >> 1) & 1, a.err, failed)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const float f = resc ? fast_exp2(m_ref - m_new) : 1.f;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              float o[32];
+              tmem_ld32(lane_base + S::kTmemO + c * 32, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= f;
+              tmem_st32(lane_base + S::kTmemO + c * 32, o);
+            }
+          }
+          if (resc) l *= fast_exp2(m_ref - m_new);
+          if (j == 0 || resc) m_ref = m_new;
+          const float ms = m_ref == -INFINITY ? 0.f : m_ref;
+          const float xs = prescale ? 1.f : sl2;
+          // P_j's buffer: its last reader, P_{j-2} V_{j-2}, was issued before
+          // S_j, whose completion this thread has waited for
+          auto make_p = [&](auto logit) {
+            float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int h = 0; h < BN / 64; ++h) {
+              uint32_t pk[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float2 x = logit(make_float2(s[h * 64 + 2 * e], s[h * 64 + 2 * e + 1]));
+                const float2 w = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                if (e & 1)
+                  sum1 = add2(sum1, w);
+                else
+                  sum0 = add2(sum0, w);
+                // weights go to the MMA as bf16 (half a step 2^-9 each, over
+                // keys of both signs; the sum is of the unrounded ones)
+                pk[e] = pack_bf16x2(w.x, w.y);
+              }
+              tmem_st32_u(lane_base + S::kTmemP + st * (BN / 2) + h * 32, pk);
+            }
+            const float2 sum = add2(sum0, sum1);
+            return sum.x + sum.y;
+          };
+          const float2 nms = make_float2(-ms, -ms);
+          l += folded ? make_p([&](float2 x) {
+            const float2 y = mul2(x, x);
+            const float2 u =
+                fma2(y, fma2(y, make_float2(k5, k5), make_float2(k3, k3)), make_float2(k1, k1));
+            return fma2(x, u, nms);
+          })
+                      : make_p([&](float2 x) { return fma2(x, make_float2(xs, xs), nms); });
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_p[st]);
+      }
+      // ---------------------------------------------------------- epilogue
+      if (ok) ok = warp_wait(&b_pv[(g - 1) & 1], ((g - 1) >> 1) & 1, a.err, failed);
+      if (!ok) break;
+      tc_fence_after();
+      const bool direct = p.first && p.after == 0;
+      if (p.first && p.after > 0)
+        cut = make_int4(p.q0 + p.tile * (QR >> t.log2_g), p.kvh << t.log2_g,
+                        min(QR, (p.n << t.log2_g) - p.tile * QR), 1 + (p.after + chunk - 1) / chunk);
+      if (!idle) {
+        // a row whose visible logits are all -infinity: 0 / 0; one that sees
+        // nothing: 0
+        const float inv = l > 0.f ? 1.f / l : (seen ? __int_as_float(0x7fffffff) : 0.f);
+        const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (p.first ? 1 : 0);
+        float* prow = a.partial_o + (slot * (D / 4) * QR + r) * 4;
+        uint16_t* orow =
+            a.out + (static_cast<size_t>(p.q0 + tok) * a.Hq + (p.kvh << t.log2_g) +
+                     (row & ((1 << t.log2_g) - 1))) * D;
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
+          float o[64];
+          tmem_ld64(lane_base + S::kTmemO + c * 64, o);
+          if (direct) {
+            if (row_valid) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                *reinterpret_cast<uint4*>(orow + c * 64 + q * 8) =
+                    make_uint4(pack_bf16x2(o[q * 8 + 0] * inv, o[q * 8 + 1] * inv),
+                               pack_bf16x2(o[q * 8 + 2] * inv, o[q * 8 + 3] * inv),
+                               pack_bf16x2(o[q * 8 + 4] * inv, o[q * 8 + 5] * inv),
+                               pack_bf16x2(o[q * 8 + 6] * inv, o[q * 8 + 7] * inv));
+            }
+          } else {
+            // [D / 4][QR rows] float4: each store of a warp is consecutive
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              *reinterpret_cast<float4*>(prow + static_cast<size_t>(c * 16 + e) * QR * 4) =
+                  make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv,
+                              o[4 * e + 3] * inv);
+          }
+        }
+        if (!direct)
+          a.partial_lse[slot * QR + r] =
+              l == 0.f ? -INFINITY : m_ref + log2f(l);  // (a NaN sum: NaN)
+        if (row_valid && *const_cast<volatile int*>(&wild_piece[piece & 1]) == piece) {
+          auto add = [&](int lo, int hi) {
+            if (direct)
+              add_wild<D, false>(a, p, see, lo, hi, nullptr, 0, orow);
+            else
+              add_wild<D, true>(a, p, see, lo, hi, prow, QR * 4, nullptr);
+          };
+          const int mid = min(t_end, max(t_begin, edge_lo + BN));
+          add(t_begin, mid);
+          add(max(mid, edge_hi - BN), t_end);
+        }
+      }
+    }
+    if (threadIdx.x == 0) {
+      if (!any_work || !ok) cut.w = 0;
+      a.cuts[blockIdx.x] = cut;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == S::kWarpMma) tmem_dealloc(tmem, S::kTmemCols);
+}
+
+// Merge of the cut segments' pieces: M = max LSE, out = sum 2^(LSE - M) O /
+// sum 2^(LSE - M).  A unit is 32 rows x 16 columns of one segment; the warps of
+// a CTA take its pieces in turn (piece k to warp k mod 8) and meet in shared
+// memory, in the same order every time.
+constexpr int kMergeWarps = 8;
+
+template <int D, int QR>
+__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(
+    const __grid_constant__ TreeMergeArgs a) {
+  __shared__ int first_unit[kTreeMaxCtas + 1];
+  __shared__ int4 cuts[kTreeMaxCtas];
+  __shared__ float sm[kMergeWarps][2][32];
+  __shared__ float4 so[kMergeWarps][4][32];
+  __shared__ int warp_sums[kMergeWarps];
+  constexpr int kCols = D / 16;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  launch_dependents();
+  wait_predecessor();
+  static_assert(kTreeMaxCtas <= kMergeWarps * 32, "a thread per chunk");
+  int4 c = make_int4(0, 0, 0, 0);
+  if (tid < a.chunks) c = a.cuts[tid];
+  const int mine = c.w > 0 ? (c.z + 31) / 32 * kCols : 0;
+  int total;
+  const int before = excl_scan<kMergeWarps * 32>(mine, warp_sums, &total);
+  if (tid < kTreeMaxCtas) {
+    first_unit[tid] = before;
+    cuts[tid] = c;
+  }
+  if (tid == 0) first_unit[kTreeMaxCtas] = total;
+  __syncthreads();
+  for (int u = blockIdx.x; u < total; u += gridDim.x) {
+    int lo = 0, hi = kTreeMaxCtas;  // the last chunk whose units begin at or before u
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (first_unit[mid] <= u)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const int4 seg = cuts[lo];
+    const int rel = u - first_unit[lo];
+    const int r = rel / kCols * 32 + lane, col = rel % kCols;
+    // piece 0 lies in the second slot of its chunk, the others in the first
+    // slots of the chunks that follow
+    float M = -INFINITY, den = 0.f;
+    float4 acc[4] = {};
+    bool dead = false;  // a piece that sees keys, but with no weight
+    for (int k0 = warp; k0 < seg.w; k0 += 4 * kMergeWarps) {
+      float lse[4];
+      float4 x[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = k0 + i * kMergeWarps;
+        lse[i] = -INFINITY;
+        if (k < seg.w) {
+          const size_t slot = 2 * static_cast<size_t>(lo + k) + (k == 0 ? 1 : 0);
+          lse[i] = a.partial_lse[slot * QR + r];
+          const float4* o = reinterpret_cast<const float4*>(a.partial_o) +
+                            (slot * (D / 4) + col * 4) * QR + r;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) x[i][q] = o[q * QR];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // (a piece without a weight counts as nothing; its row is NaN if it
+        // sees keys whose logits are all -infinity, else zeros)
+        if (lse[i] == -INFINITY) {
+          dead = dead || (k0 + i * kMergeWarps < seg.w && !(x[i][0].x == 0.f));
+          continue;
+        }
+        const float nm = fmaxf(M, lse[i]);
+        const float keep = M == -INFINITY ? 0.f : fast_exp2(M - nm);
+        const float w = fast_exp2(lse[i] - nm);
+        den = den * keep + w;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          acc[q].x = acc[q].x * keep + w * x[i][q].x;
+          acc[q].y = acc[q].y * keep + w * x[i][q].y;
+          acc[q].z = acc[q].z * keep + w * x[i][q].z;
+          acc[q].w = acc[q].w * keep + w * x[i][q].w;
+        }
+        M = nm;
+      }
+    }
+    if (dead && den == 0.f) den = -1.f;
+    sm[warp][0][lane] = M;
+    sm[warp][1][lane] = den;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) so[warp][q][lane] = acc[q];
+    __syncthreads();
+    if (warp < 4) {  // warp q: columns 4 q .. 4 q + 3 of the unit
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, sm[w][0][lane]);
+      float sum = 0.f, empty = 0.f;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kMergeWarps; ++w) {
+        const float m = sm[w][0][lane], d = sm[w][1][lane];
+        if (d == -1.f) empty = __int_as_float(0x7fffffff);
+        if (d == 0.f || d == -1.f) continue;
+        // (m = -infinity: a NaN sum)
+        const float f = m == -INFINITY ? 1.f : fast_exp2(m - top);
+        const float4 x = so[w][warp][lane];
+        sum += f * d;
+        y.x += f * x.x;
+        y.y += f * x.y;
+        y.z += f * x.z;
+        y.w += f * x.w;
+      }
+      if (sum == 0.f) y = make_float4(empty, empty, empty, empty);
+      const float inv = sum == 0.f ? 1.f : 1.f / sum;
+      if (r < seg.z) {
+        const int tok = r >> a.log2_g, head = seg.y + (r & ((1 << a.log2_g) - 1));
+        uint16_t* out = a.out + (static_cast<size_t>(seg.x + tok) * a.Hq + head) * D + col * 16 +
+                        warp * 4;
+        *reinterpret_cast<uint2*>(out) =
+            make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+      }
+    }
+    __syncthreads();
+  }
+}
+
+int log2_of(int g) { return g == 1 ? 0 : g == 2 ? 1 : g == 4 ? 2 : 3; }
+
+template <int D, int QR>
+cudaError_t launch_tree_t(const TreeArgs& a, int sm_count, cudaStream_t stream) {
+  using S = TreeShape<D, QR>;
+  const int G = a.Hq / a.Hkv;
+  TreeLaunch t{};
+  t.a = a;
+  t.log2_g = log2_of(G);
+  t.q_tokens = a.max_query_len < QR / G ? a.max_query_len : QR / G;
+  const long long rows = static_cast<long long>(a.num_blocks) * a.Hkv * kBlockSize;
+  if (!tmap_query_tiles(&t.tm_q, a.q, D, a.Hq, a.total_q, G, t.q_tokens) ||
+      !tmap_pool_groups(&t.tm_k, a.k, D, rows) || !tmap_pool_groups(&t.tm_v, a.v, D, rows))
+    return cudaErrorInvalidValue;
+  auto kern = tree_attn_kernel<D, QR>;
+  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), S::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  const int grid = sm_count < kTreeMaxCtas ? sm_count : kTreeMaxCtas;
+  e = launch_overlapped(kern, dim3(grid), S::kThreads, S::kSmemBytes, stream, t);
+  if (e != cudaSuccess || !a.may_cut) return e;
+  TreeMergeArgs m{};
+  m.partial_o = a.partial_o;
+  m.partial_lse = a.partial_lse;
+  m.cuts = a.cuts;
+  m.out = a.out;
+  m.Hq = a.Hq;
+  m.log2_g = t.log2_g;
+  m.chunks = grid;
+  return launch_overlapped(tree_merge_kernel<D, QR>, dim3(sm_count * 4), kMergeWarps * 32, 0,
+                           stream, m);
+}
+
+}  // namespace
+
+// A batch whose trees all fit 64 rows of a KV head takes the smaller row tile.
+int tree_tile_rows(int max_query_len, int group) { return max_query_len * group <= 64 ? 64 : 128; }
+
+cudaError_t launch_tree_attn(const TreeArgs& a, int head_dim, int sm_count, cudaStream_t stream) {
+  const bool small = tree_tile_rows(a.max_query_len, a.Hq / a.Hkv) == 64;
+  if (head_dim == 128)
+    return small ? launch_tree_t<128, 64>(a, sm_count, stream)
+                 : launch_tree_t<128, 128>(a, sm_count, stream);
+  return small ? launch_tree_t<256, 64>(a, sm_count, stream)
+               : launch_tree_t<256, 128>(a, sm_count, stream);
+}
+
+}  // namespace pka
