@@ -573,7 +573,7 @@ int paged_tree_plan(const int32_t* parents, const int32_t* query_start_loc,
  * depend on no length and no batch), needs no initialisation.  Calls sharing one
  * workspace must not overlap on the GPU.
  * tree_masks 8-byte aligned.  max_query_len > 64: PKA_ERR_UNSUPPORTED.
- * PKA_ERR_SHAPE if the segments times (visible blocks of a table row + 4) exceed
+ * PKA_ERR_SHAPE if the segments times (visible blocks of a table row + 20) exceed
  * 2^30, or num_blocks * Hkv * 16 exceeds 2^31 - 1. */
 size_t paged_tree_attn_ws_bytes(int32_t Hq, int32_t Hkv, int32_t D, int32_t max_query_len);
 int paged_tree_attn_ws(const void* q, void* out, const pka_kv_pool* kv,

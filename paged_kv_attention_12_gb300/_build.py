@@ -1,8 +1,10 @@
 """Builds the CUDA library ``libpaged_attn.so`` in-tree for sm_103a.
 
 Each ``csrc/*.cu`` file is compiled by nvcc in parallel, then linked into one
-shared library next to this file (``lib/libpaged_attn.so``).  Rebuilds only
-when a source or header is newer than the library.
+shared library next to this file (``lib/libpaged_attn.so``).  Beside it
+``csrc/native_binding.cpp``, the Python side of some of the library's calls,
+becomes the module ``lib/_native.so`` (the host compiler, torch's headers).
+Rebuilds only when a source or header is newer than the libraries.
 """
 from __future__ import annotations
 
@@ -18,6 +20,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "lib")
 LIB_PATH = os.path.join(OUT_DIR, "libpaged_attn.so")
+NATIVE_SRC = os.path.join(CSRC, "native_binding.cpp")
+NATIVE_PATH = os.path.join(OUT_DIR, "_native.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -40,11 +44,41 @@ def _deps():
     return files
 
 
-def up_to_date(lib_path: str = LIB_PATH) -> bool:
-    if not os.path.exists(lib_path):
+def _newer(target: str, files) -> bool:
+    if not os.path.exists(target):
         return False
-    t = os.path.getmtime(lib_path)
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(f) <= t for f in files)
+
+
+def up_to_date(lib_path: str = LIB_PATH) -> bool:
+    return _newer(lib_path, _deps())
+
+
+def native_up_to_date() -> bool:
+    return _newer(NATIVE_PATH, [NATIVE_SRC, os.path.join(INCLUDE, "paged_attn.h"),
+                                os.path.abspath(__file__)])
+
+
+def _compile_native() -> None:
+    import sysconfig
+
+    import torch
+    where = os.path.dirname(torch.__file__)
+    libs = os.path.join(where, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    includes = [INCLUDE, os.path.join(where, "include"),
+                os.path.join(where, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], cuda]
+    tmp = NATIVE_PATH + ".tmp"
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{d}" for d in includes], NATIVE_SRC, "-o", tmp, f"-L{libs}", f"-Wl,-rpath,{libs}",
+           "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the host compiler failed on {os.path.basename(NATIVE_SRC)}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, NATIVE_PATH)
 
 
 def _compile(src: str, obj: str, extra) -> None:
@@ -62,14 +96,21 @@ def build(force: bool = False, verbose: bool = False, extra=(), lib_path: str = 
     build); a build with extra flags goes to its own ``lib_path`` so that it
     never replaces the product library.
     """
-    if not force and up_to_date(lib_path):
+    want_lib = force or not up_to_date(lib_path)
+    want_native = lib_path == LIB_PATH and (force or not native_up_to_date())
+    if not want_lib and not want_native:
         return lib_path
     out_dir = os.path.dirname(lib_path)
     os.makedirs(out_dir, exist_ok=True)
+    if not want_lib:
+        _compile_native()
+        return lib_path
     srcs = _sources()
     objs = [os.path.join(out_dir, os.path.basename(s)[:-3] + ".o") for s in srcs]
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
         futs = [ex.submit(_compile, s, o, list(extra)) for s, o in zip(srcs, objs)]
+        if want_native:
+            futs.append(ex.submit(_compile_native))
         for f in futs:
             f.result()
     tmp = lib_path + ".tmp"

@@ -641,37 +641,42 @@ def paged_kv_compact(pools, refcounts, block_tables, seq_lens, new_refcounts, ne
 
 
 # ------------------------------------- draft trees and eviction by mass
+# These calls check their tensors as the ones above do (ValueError), in the
+# module lib/_native.so: between small kernels the checks would cost more than
+# the launch.
+_native_module = None
+
+
+def _native():
+    global _native_module
+    if _native_module is None:
+        import importlib.machinery
+        import importlib.util
+
+        import torch  # noqa: F401  (its libraries come first)
+        L = lib()
+        path = os.path.join(HERE, "lib", "_native.so")
+        if not os.path.exists(path):
+            raise RuntimeError(
+                f"{path} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
+        loader = importlib.machinery.ExtensionFileLoader("_native", path)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_native", loader))
+        loader.exec_module(m)
+        m.attach(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.paged_tree_plan, L.paged_tree_attn_ws, L.paged_tree_accept, L.paged_kv_evict)))
+        _native_module = m
+    return _native_module
+
+
 def paged_tree_plan(parents, query_start_loc, seq_lens, block_tables, num_blocks: int,
                     max_query_len: int, tree_masks, positions, slots, *, total_lens=None, err=None,
                     stream=None):
     """Ancestor masks (int64 [total_q]), positions and cache slots (int32) of
     drafted tokens from their ``parents`` (int32 [total_q], indexes within a
     tree, -1: none).  An output may be None."""
-    import torch
-    dev = _cuda_device(parents, "parents")
-    i32, B, rows, width = torch.int32, seq_lens.shape[0], parents.shape[0], block_tables.shape[-1]
-    _tensor(parents, "parents", i32, dev, (rows,))
-    _tensor(query_start_loc, "query_start_loc", i32, dev, (B + 1,))
-    _tensor(seq_lens, "seq_lens", i32, dev, (B,))
-    _tensor(block_tables, "block_tables", i32, dev, (B, width))
-    if total_lens is not None:
-        _tensor(total_lens, "total_lens", i32, dev, (B,))
-    if tree_masks is not None:
-        _tensor(tree_masks, "tree_masks", torch.int64, dev, (rows,))
-    if positions is not None:
-        _tensor(positions, "positions", i32, dev, (rows,))
-    if slots is not None:
-        _tensor(slots, "slots", i32, dev, (rows,))
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return paged_tree_plan(parents, query_start_loc, seq_lens, block_tables, num_blocks,
-                                   max_query_len, tree_masks, positions, slots,
-                                   total_lens=total_lens, err=err, stream=stream)
-    st = lib().paged_tree_plan(
-        parents.data_ptr(), query_start_loc.data_ptr(), seq_lens.data_ptr(), _ptr(total_lens),
-        block_tables.data_ptr(), width, int(num_blocks), B, rows, int(max_query_len),
-        _ptr(tree_masks), _ptr(positions), _ptr(slots), None if err is None else _err(err, dev),
-        _raw_stream(dev, stream))
+    st = (_native_module or _native()).tree_plan(
+        parents, query_start_loc, seq_lens, block_tables, num_blocks, max_query_len, tree_masks,
+        positions, slots, total_lens, err, stream)
     if st != PKA_OK:
         raise PagedAttnError("paged_tree_plan", st)
 
@@ -687,47 +692,11 @@ def paged_tree_attn_ws(q, out, k_pool, v_pool, block_tables, query_start_loc, tr
     ``tree_masks`` (int64 [total_q], bit j: token j), each other: ``q``, ``out``
     bf16 [total_q][Hq][D].  ``workspace``: device bytes, at least
     ``paged_tree_attn_ws_bytes``; not to be shared by calls that can overlap."""
-    import torch
-    dev = _cuda_device(q, "q")
-    bf16, i32, B, width = torch.bfloat16, torch.int32, seq_lens.shape[0], block_tables.shape[-1]
-    rows, _, d = shape = q.shape
-    pool = k_pool.shape
-    _tensor(q, "q", bf16, dev, shape)
-    _tensor(out, "out", bf16, dev, shape)
-    if len(pool) != 4 or pool[2] != 16 or pool[3] != d:
-        _refuse(k_pool, "k_pool", f"bfloat16 [num_blocks][Hkv][16][{d}]")
-    _tensor(k_pool, "k_pool", bf16, dev, pool)
-    _tensor(v_pool, "v_pool", bf16, dev, pool)
-    _tensor(block_tables, "block_tables", i32, dev, (B, width))
-    _tensor(query_start_loc, "query_start_loc", i32, dev, (B + 1,))
-    _tensor(tree_masks, "tree_masks", torch.int64, dev, (rows,))
-    _tensor(seq_lens, "seq_lens", i32, dev, (B,))
-    _tensor(workspace, "workspace", workspace.dtype, dev, workspace.shape)
-    kv = PkaKvPool(k_pool.data_ptr(), v_pool.data_ptr(), *pool)
-    par = PkaAttnParams(scale, softcap, window, None if err is None else _err(err, dev))
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return paged_tree_attn_ws(q, out, k_pool, v_pool, block_tables, query_start_loc,
-                                      tree_masks, seq_lens, max_query_len, max_seq_len, workspace,
-                                      scale=scale, softcap=softcap, window=window, err=err,
-                                      stream=stream)
-    st = lib().paged_tree_attn_ws(
-        q.data_ptr(), out.data_ptr(), ctypes.byref(kv), block_tables.data_ptr(), width,
-        query_start_loc.data_ptr(), tree_masks.data_ptr(), seq_lens.data_ptr(), B, shape[1], rows,
-        int(max_query_len), int(max_seq_len), ctypes.byref(par), workspace.data_ptr(),
-        workspace.nbytes, _raw_stream(dev, stream))
+    st = (_native_module or _native()).tree_attn_ws(
+        q, out, k_pool, v_pool, block_tables, query_start_loc, tree_masks, seq_lens, max_query_len,
+        max_seq_len, workspace, scale, softcap, window, err, stream)
     if st != PKA_OK:
         raise PagedAttnError("paged_tree_attn_ws", st)
-
-
-def _kv_pools(pools):
-    """Checks bf16 pools [num_blocks][Hkv][16][D] of one shape: their pointers, shape, device."""
-    import torch
-    first = pools[0]
-    if first.dtype is not torch.bfloat16 or first.dim() != 4:
-        _refuse(first, "pools", "bfloat16 [num_blocks][Hkv][16][D]")
-    ptrs, _, _, dev = _pool_list(pools)
-    return ptrs, first.shape, dev
 
 
 def paged_tree_accept(pools, parents, tokens, targets, slots, query_start_loc, seq_lens, path,
@@ -737,32 +706,9 @@ def paged_tree_accept(pools, parents, tokens, targets, slots, query_start_loc, s
     and V of every layer) to the tree's first ``slots``.  Writes ``path`` (int32
     [B][max_query_len]), ``accepted``, ``next_tokens`` and ``new_seq_lens``
     (may be ``seq_lens``).  Without pools the walk alone (``slots`` may be None)."""
-    import torch
-    ptrs, shape, dev = _kv_pools(pools) if pools else (None, (0, 0, 0, 0),
-                                                       _cuda_device(parents, "parents"))
-    i32, B, rows = torch.int32, seq_lens.shape[0], parents.shape[0]
-    width = path.shape[-1]
-    _tensor(parents, "parents", i32, dev, (rows,))
-    _tensor(tokens, "tokens", i32, dev, (rows,))
-    _tensor(targets, "targets", i32, dev, (rows,))
-    if pools or slots is not None:
-        _tensor(slots, "slots", i32, dev, (rows,))
-    _tensor(query_start_loc, "query_start_loc", i32, dev, (B + 1,))
-    _tensor(seq_lens, "seq_lens", i32, dev, (B,))
-    _tensor(path, "path", i32, dev, (B, width))
-    _tensor(accepted, "accepted", i32, dev, (B,))
-    _tensor(next_tokens, "next_tokens", i32, dev, (B,))
-    _tensor(new_seq_lens, "new_seq_lens", i32, dev, (B,))
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return paged_tree_accept(pools, parents, tokens, targets, slots, query_start_loc,
-                                     seq_lens, path, accepted, next_tokens, new_seq_lens, err,
-                                     stream)
-    st = lib().paged_tree_accept(
-        ptrs, len(pools), *shape, parents.data_ptr(), tokens.data_ptr(), targets.data_ptr(),
-        _ptr(slots), query_start_loc.data_ptr(), seq_lens.data_ptr(), B, rows, width,
-        path.data_ptr(), accepted.data_ptr(), next_tokens.data_ptr(), new_seq_lens.data_ptr(),
-        None if err is None else _err(err, dev), _raw_stream(dev, stream))
+    st = (_native_module or _native()).tree_accept(
+        pools, parents, tokens, targets, slots, query_start_loc, seq_lens, path, accepted,
+        next_tokens, new_seq_lens, err, stream)
     if st != PKA_OK:
         raise PagedAttnError("paged_tree_accept", st)
 
@@ -782,35 +728,9 @@ def paged_kv_evict(pools, key_mass, key_pos, block_tables, seq_lens, total_lens,
     sequences' lengths are their caches'.  With ``refcounts`` requests that share
     a block to be written are left whole.  ``workspace``: device bytes, at least
     ``paged_kv_evict_ws_bytes``; not to be shared by calls that can overlap."""
-    import torch
-    ptrs, pool, dev = _kv_pools(pools)
-    i32, B, width = torch.int32, seq_lens.shape[0], block_tables.shape[-1]
-    shape = (len(pools) // 2, B, pool[1], width * 16)
-    if len(pools) % 2:
-        raise ValueError(f"pools: K and V of each layer are wanted, got {len(pools)} pools")
-    _tensor(key_mass, "key_mass", torch.float32, dev, shape)
-    _tensor(new_mass, "new_mass", torch.float32, dev, shape)
-    _tensor(key_pos, "key_pos", i32, dev, shape)
-    _tensor(new_pos, "new_pos", i32, dev, shape)
-    _tensor(block_tables, "block_tables", i32, dev, (B, width))
-    _tensor(seq_lens, "seq_lens", i32, dev, (B,))
-    _tensor(new_seq_lens, "new_seq_lens", i32, dev, (B,))
-    _tensor(workspace, "workspace", workspace.dtype, dev, workspace.shape)
-    if total_lens is not None:
-        _tensor(total_lens, "total_lens", i32, dev, (B,))
-    if refcounts is not None:
-        _tensor(refcounts, "refcounts", i32, dev, (pool[0],))
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return paged_kv_evict(pools, key_mass, key_pos, block_tables, seq_lens, total_lens,
-                                  budget, sinks, recent, new_mass, new_pos, new_seq_lens, workspace,
-                                  refcounts=refcounts, err=err, stream=stream)
-    st = lib().paged_kv_evict(
-        ptrs, shape[0], *pool, block_tables.data_ptr(), width, seq_lens.data_ptr(),
-        _ptr(total_lens), B, int(budget), int(sinks), int(recent), key_mass.data_ptr(),
-        new_mass.data_ptr(), key_pos.data_ptr(), new_pos.data_ptr(), new_seq_lens.data_ptr(),
-        _ptr(refcounts), workspace.data_ptr(), workspace.nbytes,
-        None if err is None else _err(err, dev), _raw_stream(dev, stream))
+    st = (_native_module or _native()).kv_evict(
+        pools, key_mass, key_pos, block_tables, seq_lens, total_lens, budget, sinks, recent,
+        new_mass, new_pos, new_seq_lens, workspace, refcounts, err, stream)
     if st != PKA_OK:
         raise PagedAttnError("paged_kv_evict", st)
 

@@ -103,6 +103,8 @@ int mixed_query_tile(int head_dim, int group);
 
 // Attention of drafted tokens that form trees.
 constexpr int kTreeMaxCtas = 160;  // CTAs (and chunks of the work line) at most
+// Fixed cost of a segment on the work line, in blocks of 16 keys.
+constexpr int kTreePieceUnits(int head_dim) { return head_dim == 256 ? 10 : 20; }
 struct TreeArgs {
   const uint16_t* q;               // bf16 [total_q][Hq][D]
   uint16_t* out;                   // bf16 [total_q][Hq][D]

@@ -139,12 +139,12 @@ int paged_tree_attn_ws(const void* q, void* out, const pka_kv_pool* kv,
     return PKA_ERR_ALIGN;
   const TreeLayout lay = tree_layout(G, kv->head_dim, max_query_len);
   if (workspace_bytes < lay.total()) return PKA_ERR_WORKSPACE;
-  // the work line (segments times their blocks and 4) is counted in 32 bits
+  // the work line (segments times their blocks and a fixed cost) is counted in 32 bits
   const int64_t tile_rows = pka::tree_tile_rows(max_query_len, G);
   const int64_t segs = static_cast<int64_t>(B) * Hkv * ((max_query_len * G + tile_rows - 1) / tile_rows);
   int64_t per = max_blocks;
   if (params->window > 0) per = std::min<int64_t>(per, (static_cast<int64_t>(params->window) + kMaxTree) / 16 + 2);
-  if (segs * (per + 4) > (int64_t(1) << 30)) return PKA_ERR_SHAPE;
+  if (segs * (per + pka::kTreePieceUnits(128)) > (int64_t(1) << 30)) return PKA_ERR_SHAPE;
   const int sms = pka::device_sm_count();
   if (sms <= 0) return PKA_ERR_CUDA;
   int64_t longest = max_seq_len / 16 + (max_seq_len % 16 != 0);
@@ -171,7 +171,7 @@ int paged_tree_attn_ws(const void* q, void* out, const pka_kv_pool* kv,
   a.max_blocks = max_blocks;
   a.total_q = total_q;
   a.max_query_len = max_query_len;
-  a.min_chunk = 8;
+  a.min_chunk = pka::kTreePieceUnits(kv->head_dim) + 8;
   a.whole_slack = kv->head_dim == 256 ? 16 : 32;
   a.may_cut = segs > std::min(sms, pka::kTreeMaxCtas) || longest > a.whole_slack;
   a.scale = params->scale;

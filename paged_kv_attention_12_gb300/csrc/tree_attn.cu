@@ -35,8 +35,6 @@ namespace pka {
 
 namespace {
 
-constexpr int kPieceUnits = 4;  // fixed cost of a piece, in blocks
-
 template <int D_, int QR_>
 struct TreeShape {
   static constexpr int D = D_, QR = QR_;
@@ -59,6 +57,7 @@ struct TreeShape {
   static constexpr int kWarpK = kSoftmaxWarps, kWarpV = kWarpK + 1, kWarpMma = kWarpK + 2,
                        kWarpQ = kWarpK + 3;
   static constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
+  static constexpr int kPieceUnits = kTreePieceUnits(D);
   // TMEM columns: S_j (fp32) in buffer j % 2 at (j % 2) * BN, O at 256, P_j
   // (bf16 pairs) in buffer j % 2 at kTmemP + (j % 2) * BN / 2.
   static constexpr uint32_t kTmemO = 256;
@@ -122,14 +121,16 @@ struct Load {
   int units, segs, len;
 };
 
-template <int QR>
-__device__ __forceinline__ Load load_of(const TreeLaunch& t, int b, bool tell) {
-  if (b >= t.a.batch) return Load{0, 0, 0};
-  const Request r = request_of(t.a, b, tell);
+template <typename S>
+__device__ __forceinline__ Load load_of(const TreeLaunch& t, const Request& r) {
   if (r.n == 0) return Load{0, 0, 0};
   const int nb = (r.L + kBlockSize - 1) / kBlockSize - first_block(t.a, r);
-  const int segs = t.a.Hkv * row_tiles<QR>(t, r);
-  return Load{segs * (kPieceUnits + nb), segs, kPieceUnits + nb};
+  const int segs = t.a.Hkv * row_tiles<S::QR>(t, r);
+  return Load{segs * (S::kPieceUnits + nb), segs, S::kPieceUnits + nb};
+}
+template <typename S>
+__device__ __forceinline__ Load load_of(const TreeLaunch& t, int b, bool tell) {
+  return b < t.a.batch ? load_of<S>(t, request_of(t.a, b, tell)) : Load{0, 0, 0};
 }
 
 // Blocks [j0 + lo, j0 + hi) of a segment.
@@ -144,37 +145,36 @@ struct Piece {
 // Walk over the pieces of a chunk; every warp of the CTA makes its own.
 struct Walk {
   int b, off, rem;   // request, unit within it, units of the chunk that are left
+  Request r;         // request b
 
-  template <int QR>
+  template <typename S>
   __device__ bool next(const TreeLaunch& t, Piece* p) {
-    while (rem > 0 && b < t.a.batch) {
-      const Request r = request_of(t.a, b, false);
-      const int tiles = row_tiles<QR>(t, r);
-      const int j0 = first_block(t.a, r);
-      const int nb = (r.L + kBlockSize - 1) / kBlockSize - j0;
-      const int seg = kPieceUnits + nb;
-      if (off >= t.a.Hkv * tiles * seg) {  // (tiles = 0 without query rows)
-        ++b;
+    while (rem > 0) {
+      const Load load = load_of<S>(t, r);
+      if (off >= load.units) {
+        if (++b >= t.a.batch) return false;
         off = 0;
+        r = request_of(t.a, b, false);
         continue;
       }
-      const int item = off / seg;
-      const int at = off - item * seg;
-      const int take = min(seg - at, rem);
-      const int lo = max(at, kPieceUnits) - kPieceUnits;
-      const int hi = at + take - kPieceUnits;
+      const int item = off / load.len;
+      const int at = off - item * load.len;
+      const int take = min(load.len - at, rem);
+      const int lo = max(at, S::kPieceUnits) - S::kPieceUnits;
+      const int hi = at + take - S::kPieceUnits;
       off += take;
       rem -= take;
       if (hi <= lo) continue;
+      const int tiles = row_tiles<S::QR>(t, r);
       p->b = b;
       p->kvh = item / tiles;
       p->tile = item - p->kvh * tiles;
       p->q0 = r.q0;
       p->n = r.n;
       p->L = r.L;
-      p->j0 = j0 + lo;
+      p->j0 = first_block(t.a, r) + lo;
       p->blocks = hi - lo;
-      p->after = nb - hi;
+      p->after = load.len - S::kPieceUnits - hi;
       p->first = lo == 0;
       return true;
     }
@@ -219,14 +219,52 @@ __device__ __forceinline__ uint64_t bit_range(int lo, int hi) {
   return (~0ull >> (64 - (hi - lo))) << lo;
 }
 
-// Whether either bf16 of a word is an infinity or a NaN.
-__device__ __forceinline__ bool wild(uint32_t w) {
-  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+// Whether a bf16 of the words is an infinity or a NaN (an exponent of ones
+// carries into the sign's place).
+__device__ __forceinline__ bool wild(const uint4& w) {
+  constexpr uint32_t e = 0x7f807f80u, one = 0x00800080u;
+  return ((((w.x & e) + one) | ((w.y & e) + one) | ((w.z & e) + one) | ((w.w & e) + one)) &
+          0x80008000u) != 0;
 }
 __device__ __forceinline__ uint32_t tamed(uint32_t w) {
   if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
   if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
   return w;
+}
+
+// A V tile's keys [lo, hi) (of the tile, NW warps share them): infinities and
+// NaN become zeros; returns whether this lane met one.  A row is a warp's load
+// (D = 128: two rows), four in flight.
+template <typename S>
+__device__ __forceinline__ bool tame_rows(uint8_t* vst, int lo, int hi, int warp, int lane) {
+  constexpr int kLanes = S::D / 8, kRows = 32 / kLanes, kStep = S::kSoftmaxWarps * kRows;
+  const int part = lane % kLanes;
+  uint8_t* col = vst + part / 8 * 1024 + part % 8 * 16;
+  auto at = [&](int r) { return reinterpret_cast<uint4*>(col + r / 8 * S::kGroup + r % 8 * 128); };
+  bool found = false;
+  for (int r = lo + warp * kRows + lane / kLanes; r < hi; r += 4 * kStep) {
+    uint4 w[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      w[u] = r + u * kStep < hi ? *at(r + u * kStep) : make_uint4(0u, 0u, 0u, 0u);
+    if (wild(w[0]) || wild(w[1]) || wild(w[2]) || wild(w[3])) {
+      found = true;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (wild(w[u]))
+          *at(r + u * kStep) = make_uint4(tamed(w[u].x), tamed(w[u].y), tamed(w[u].z), tamed(w[u].w));
+    }
+  }
+  return found;
+}
+// The same keys' rows as zeros.
+template <typename S>
+__device__ __forceinline__ void clear_rows(uint8_t* vst, int lo, int hi, int warp, int lane) {
+  constexpr int kLanes = S::D / 8, kRows = 32 / kLanes;
+  const int part = lane % kLanes;
+  for (int r = lo + warp * kRows + lane / kLanes; r < hi; r += S::kSoftmaxWarps * kRows)
+    *reinterpret_cast<uint4*>(vst + r / 8 * S::kGroup + r % 8 * 128 + part / 8 * 1024 +
+                              part % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // What a query row sees: the prefix from key `kmin` up to `base`, and the
@@ -274,8 +312,8 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
   __shared__ uint64_t b_q, b_qfree, b_k[S::KST], b_kfree[S::KST], b_v[S::VST], b_vfree[S::VST],
       b_s[2], b_pv[2], b_p[2];
   __shared__ uint32_t tmem_slot;
-  __shared__ int failed_flag, wild_piece[2], warp_sums[S::kThreads / 32], start_b, start_off,
-      start_rem, longest;
+  __shared__ int failed_flag, wild_piece[2], warp_sums[S::kThreads / 32], longest;
+  __shared__ Walk start;  // of the CTA's chunk
   volatile int* failed = &failed_flag;
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sQ = smem + S::oQ;
@@ -318,7 +356,9 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
   constexpr int NT = S::kThreads;
   const int tid = threadIdx.x;
   const int grid = static_cast<int>(gridDim.x);
-  Load mine = load_of<QR>(t, tid, blockIdx.x == 0);
+  Request mine_r{0, 0, 0};
+  if (tid < a.batch) mine_r = request_of(a, tid, blockIdx.x == 0);
+  const Load mine = load_of<S>(t, mine_r);
   int units = 0, segs = 0;
   Load before{excl_scan<NT>(mine.units, warp_sums, &units),
               excl_scan<NT>(mine.segs, warp_sums, &segs), 0};
@@ -326,7 +366,7 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
   if (a.batch > NT) {
     Load rest{0, 0, 0};
     for (int b = tid + NT; b < a.batch; b += NT) {
-      const Load x = load_of<QR>(t, b, blockIdx.x == 0);
+      const Load x = load_of<S>(t, b, blockIdx.x == 0);
       rest.units += x.units;
       rest.segs += x.segs;
       len = max(len, x.len);
@@ -344,30 +384,29 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
   const bool whole = !a.may_cut || (segs <= grid && longest <= chunk + a.whole_slack);
   // (where may_cut is false there are no more segments than CTAs)
   const long long begin = static_cast<long long>(blockIdx.x) * (whole ? 1 : chunk);
-  Walk walk{0, 0, 0};
   const bool any_work = begin < (whole ? segs : units);
   if (any_work) {
     const int want = static_cast<int>(begin);
-    auto look = [&](int b, const Load& x, int at_unit, int at_seg) {
+    auto look = [&](int b, const Request& r, const Load& x, int at_unit, int at_seg) {
       const int at = whole ? at_seg : at_unit;
-      if (want >= at && want < at + (whole ? x.segs : x.units)) {
-        start_b = b;
-        start_off = (want - at) * (whole ? x.len : 1);
-        if (whole) start_rem = x.len;
-      }
+      if (want >= at && want < at + (whole ? x.segs : x.units))
+        start = Walk{b, (want - at) * (whole ? x.len : 1),
+                     whole ? x.len : min(chunk, units - want), r};
     };
-    look(tid, mine, before.units, before.segs);
+    look(tid, mine_r, mine, before.units, before.segs);
     if (a.batch > NT) {
       int at_unit, at_seg, sum;
       excl_scan<NT>(mine.units, warp_sums, &at_unit);
       excl_scan<NT>(mine.segs, warp_sums, &at_seg);
       for (int base = NT; base < a.batch && (whole ? at_seg : at_unit) <= want; base += NT) {
-        const Load x = load_of<QR>(t, base + tid, false);
+        Request r{0, 0, 0};
+        if (base + tid < a.batch) r = request_of(a, base + tid, false);
+        const Load x = load_of<S>(t, r);
         const int u = at_unit + excl_scan<NT>(x.units, warp_sums, &sum);
         at_unit += sum;
         const int s = at_seg + excl_scan<NT>(x.segs, warp_sums, &sum);
         at_seg += sum;
-        look(base + tid, x, u, s);
+        look(base + tid, r, x, u, s);
       }
     }
   }
@@ -375,11 +414,8 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  if (any_work) {
-    walk.b = start_b;
-    walk.off = start_off;
-    walk.rem = whole ? start_rem : min(chunk, units - static_cast<int>(begin));
-  }
+  Walk walk{0, 0, 0, {0, 0, 0}};
+  if (any_work) walk = start;
   Piece p;
 
   if (warp == S::kWarpK || warp == S::kWarpV) {
@@ -391,9 +427,10 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
     uint64_t* full = is_k ? b_k : b_v;
     uint64_t* freed = is_k ? b_kfree : b_vfree;
     const int past = a.num_blocks * a.Hkv * 2;  // a group past the pool: zeros
+    const uint64_t policy = policy_evict_first();
     int g = 0;                                  // tiles issued
     bool ok = true;
-    while (ok && walk.next<QR>(t, &p)) {
+    while (ok && walk.next<S>(t, &p)) {
       const int32_t* trow = a.tables + static_cast<size_t>(p.b) * a.max_blocks + p.j0;
       // the piece's blocks, 32 at a time (one per lane), read 32 ahead
       auto load_groups = [&](int base) -> int {
@@ -424,7 +461,8 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
         if (lane == 0) mbar_arrive_expect_tx(&full[st], S::kStage);
         __syncwarp();
         if (lane < BPT)
-          tma_load_4d(ring + st * S::kStage + lane * S::kBlockBytes, map, 0, 0, 0, at, &full[st]);
+          tma_load_4d(ring + st * S::kStage + lane * S::kBlockBytes, map, 0, 0, 0, at, &full[st],
+                      policy);
       }
     }
     // every copy must land before the CTA may end
@@ -434,7 +472,7 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
   } else if (warp == S::kWarpQ) {
     // =============================== TMA of Q ===============================
     int pieces = 0;
-    while (walk.next<QR>(t, &p)) {
+    while (walk.next<S>(t, &p)) {
       if (pieces > 0 && !warp_wait(&b_qfree, (pieces - 1) & 1, a.err, failed)) break;
       if (__any_sync(0xffffffffu, stop_requested(failed))) break;
       if (lane == 0) {
@@ -476,7 +514,7 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
       __syncwarp();
       return true;
     };
-    while (ok && walk.next<QR>(t, &p)) {
+    while (ok && walk.next<S>(t, &p)) {
       const int nt = (p.blocks + BPT - 1) / BPT;
       ok = warp_wait(&b_q, pieces & 1, a.err, failed);
       ++pieces;
@@ -529,7 +567,7 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
     int g = 0, piece = 0;
     bool ok = true;
     int4 cut = make_int4(0, 0, 0, 0);  // this chunk's segment that goes on in the next one
-    while (ok && walk.next<QR>(t, &p)) {
+    while (ok && walk.next<S>(t, &p)) {
       ++piece;
       const int row = p.tile * QR + r;
       const int tok = row >> t.log2_g;
@@ -570,32 +608,6 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
           break;
         }
         tc_fence_after();
-        if (t0 < edge_lo || t0 + BN > edge_hi) {
-          // V's rows past the sequence (stale) and its infinities and NaN
-          // become zeros; the latter are added to the rows that see them
-          const int vs = g % S::VST;
-          if (!warp_wait(&b_v[vs], (g / S::VST) & 1, a.err, failed)) {
-            ok = false;
-            break;
-          }
-          uint8_t* vst = sV + vs * S::kStage;
-          bool found = false;
-          for (int x = warp * 32 + lane; x < S::kStage / 16; x += NW * 32) {
-            const int off = x * 16;
-            const int key = t0 + off / S::kGroup * 8 + off % 1024 / 128;
-            uint4 w = *reinterpret_cast<const uint4*>(vst + off);
-            if (key >= p.L) {
-              *reinterpret_cast<uint4*>(vst + off) = make_uint4(0u, 0u, 0u, 0u);
-            } else if (wild(w.x) || wild(w.y) || wild(w.z) || wild(w.w)) {
-              found = true;
-              *reinterpret_cast<uint4*>(vst + off) =
-                  make_uint4(tamed(w.x), tamed(w.y), tamed(w.z), tamed(w.w));
-            }
-          }
-          if (found) *const_cast<volatile int*>(&wild_piece[piece & 1]) = piece;
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
         if (!idle) {
           float s[BN];
 #pragma unroll
@@ -723,6 +735,23 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
                       : make_p([&](float2 x) { return fma2(x, make_float2(xs, xs), nms); });
           tmem_wait_st();
         }
+        if (t0 < edge_lo || t0 + BN > edge_hi) {
+          // V's rows past the sequence are stale: zeros.  Infinities and NaN of
+          // the keys that not every row sees become zeros here and are added to
+          // the rows that see them in the end.
+          const int vs = g % S::VST;
+          if (!warp_wait(&b_v[vs], (g / S::VST) & 1, a.err, failed)) {
+            ok = false;
+            break;
+          }
+          uint8_t* vst = sV + vs * S::kStage;
+          const int stale = min(BN, (p.L + kBlockSize - 1) / kBlockSize * kBlockSize - t0);
+          bool found = tame_rows<S>(vst, 0, min(BN, edge_lo - t0), warp, lane);
+          if (tame_rows<S>(vst, max(0, edge_hi - t0), min(BN, p.L - t0), warp, lane)) found = true;
+          clear_rows<S>(vst, max(0, p.L - t0), stale, warp, lane);
+          if (found) *const_cast<volatile int*>(&wild_piece[piece & 1]) = piece;
+          fence_proxy_async_smem();
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b_p[st]);
@@ -777,9 +806,9 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
             else
               add_wild<D, true>(a, p, see, lo, hi, prow, QR * 4, nullptr);
           };
-          const int mid = min(t_end, max(t_begin, edge_lo + BN));
+          const int mid = min(t_end, max(t_begin, edge_lo));
           add(t_begin, mid);
-          add(max(mid, edge_hi - BN), t_end);
+          add(max(mid, edge_hi), t_end);
         }
       }
     }
@@ -796,34 +825,44 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
 }
 
 // Merge of the cut segments' pieces: M = max LSE, out = sum 2^(LSE - M) O /
-// sum 2^(LSE - M).  A unit is 32 rows x 16 columns of one segment; the warps of
-// a CTA take its pieces in turn (piece k to warp k mod 8) and meet in shared
-// memory, in the same order every time.
+// sum 2^(LSE - M).  A warp takes 32 rows x 8 columns, a row a lane; for segments
+// of many pieces 2 to 8 warps share them (piece k to warp k mod their number)
+// and meet in shared memory.  The order of the sums depends on the number of
+// pieces alone.
 constexpr int kMergeWarps = 8;
 
+struct MergeState {
+  float M, den;      // den = -1: pieces that see keys, but no weight
+  float4 acc[2];
+};
+
+// Warps that share the pieces.
+__device__ __forceinline__ int merge_share(int pieces) {
+  return pieces <= 4 ? 1 : pieces <= 8 ? 2 : pieces <= 16 ? 4 : 8;
+}
+
 template <int D, int QR>
-__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(
+__global__ void __launch_bounds__(kMergeWarps * 32, 4) tree_merge_kernel(
     const __grid_constant__ TreeMergeArgs a) {
   __shared__ int first_unit[kTreeMaxCtas + 1];
   __shared__ int4 cuts[kTreeMaxCtas];
   __shared__ float sm[kMergeWarps][2][32];
-  __shared__ float4 so[kMergeWarps][4][32];
+  __shared__ float4 so[kMergeWarps][2][32];
   __shared__ int warp_sums[kMergeWarps];
-  constexpr int kCols = D / 16;
+  constexpr int kCols = D / 8;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   launch_dependents();
   wait_predecessor();
   static_assert(kTreeMaxCtas <= kMergeWarps * 32, "a thread per chunk");
   int4 c = make_int4(0, 0, 0, 0);
   if (tid < a.chunks) c = a.cuts[tid];
-  const int mine = c.w > 0 ? (c.z + 31) / 32 * kCols : 0;
+  const int mine = c.w > 0 ? (c.z + 31) / 32 * (kCols * merge_share(c.w) / kMergeWarps) : 0;
   int total;
   const int before = excl_scan<kMergeWarps * 32>(mine, warp_sums, &total);
   if (tid < kTreeMaxCtas) {
     first_unit[tid] = before;
     cuts[tid] = c;
   }
-  if (tid == 0) first_unit[kTreeMaxCtas] = total;
   __syncthreads();
   for (int u = blockIdx.x; u < total; u += gridDim.x) {
     int lo = 0, hi = kTreeMaxCtas;  // the last chunk whose units begin at or before u
@@ -835,27 +874,30 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(
         hi = mid;
     }
     const int4 seg = cuts[lo];
-    const int rel = u - first_unit[lo];
-    const int r = rel / kCols * 32 + lane, col = rel % kCols;
+    const int share = merge_share(seg.w);
+    const int rel = u - first_unit[lo], per_row = kCols * share / kMergeWarps;
+    const int r = rel / per_row * 32 + lane;
+    const int col = rel % per_row * (kMergeWarps / share) + warp / share;
+    const int part = warp % share;
     // piece 0 lies in the second slot of its chunk, the others in the first
     // slots of the chunks that follow
-    float M = -INFINITY, den = 0.f;
-    float4 acc[4] = {};
+    MergeState x{-INFINITY, 0.f, {}};
     bool dead = false;  // a piece that sees keys, but with no weight
-    for (int k0 = warp; k0 < seg.w; k0 += 4 * kMergeWarps) {
+    for (int k0 = part; k0 < seg.w; k0 += 4 * share) {
       float lse[4];
-      float4 x[4][4];
+      float4 y[4][2];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int k = k0 + i * kMergeWarps;
+        const int k = k0 + i * share;
         lse[i] = -INFINITY;
+        y[i][0] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (k < seg.w) {
           const size_t slot = 2 * static_cast<size_t>(lo + k) + (k == 0 ? 1 : 0);
           lse[i] = a.partial_lse[slot * QR + r];
           const float4* o = reinterpret_cast<const float4*>(a.partial_o) +
-                            (slot * (D / 4) + col * 4) * QR + r;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) x[i][q] = o[q * QR];
+                            (slot * (D / 4) + col * 2) * QR + r;
+          y[i][0] = o[0];
+          y[i][1] = o[QR];
         }
       }
 #pragma unroll
@@ -863,60 +905,68 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(
         // (a piece without a weight counts as nothing; its row is NaN if it
         // sees keys whose logits are all -infinity, else zeros)
         if (lse[i] == -INFINITY) {
-          dead = dead || (k0 + i * kMergeWarps < seg.w && !(x[i][0].x == 0.f));
+          dead = dead || !(y[i][0].x == 0.f);
           continue;
         }
-        const float nm = fmaxf(M, lse[i]);
-        const float keep = M == -INFINITY ? 0.f : fast_exp2(M - nm);
+        const float nm = fmaxf(x.M, lse[i]);
+        const float keep = x.M == -INFINITY ? 0.f : fast_exp2(x.M - nm);
         const float w = fast_exp2(lse[i] - nm);
-        den = den * keep + w;
+        x.den = x.den * keep + w;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          acc[q].x = acc[q].x * keep + w * x[i][q].x;
-          acc[q].y = acc[q].y * keep + w * x[i][q].y;
-          acc[q].z = acc[q].z * keep + w * x[i][q].z;
-          acc[q].w = acc[q].w * keep + w * x[i][q].w;
+        for (int q = 0; q < 2; ++q) {
+          x.acc[q].x = x.acc[q].x * keep + w * y[i][q].x;
+          x.acc[q].y = x.acc[q].y * keep + w * y[i][q].y;
+          x.acc[q].z = x.acc[q].z * keep + w * y[i][q].z;
+          x.acc[q].w = x.acc[q].w * keep + w * y[i][q].w;
         }
-        M = nm;
+        x.M = nm;
       }
     }
-    if (dead && den == 0.f) den = -1.f;
-    sm[warp][0][lane] = M;
-    sm[warp][1][lane] = den;
+    if (dead && x.den == 0.f) x.den = -1.f;
+    if (share > 1) {  // uniform over the CTA
+      sm[warp][0][lane] = x.M;
+      sm[warp][1][lane] = x.den;
+      so[warp][0][lane] = x.acc[0];
+      so[warp][1][lane] = x.acc[1];
+      __syncthreads();
+      if (part == 0) {
+        float top = -INFINITY, sum = 0.f;
+        bool nothing = false;
+        float4 y[2] = {};
+        for (int w = warp; w < warp + share; ++w) top = fmaxf(top, sm[w][0][lane]);
+        for (int w = warp; w < warp + share; ++w) {
+          const float m = sm[w][0][lane], d = sm[w][1][lane];
+          if (d == -1.f) nothing = true;
+          if (d == 0.f || d == -1.f) continue;
+          const float f = m == -INFINITY ? 1.f : fast_exp2(m - top);  // (-infinity: a NaN sum)
+          sum += f * d;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) so[warp][q][lane] = acc[q];
-    __syncthreads();
-    if (warp < 4) {  // warp q: columns 4 q .. 4 q + 3 of the unit
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, sm[w][0][lane]);
-      float sum = 0.f, empty = 0.f;
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kMergeWarps; ++w) {
-        const float m = sm[w][0][lane], d = sm[w][1][lane];
-        if (d == -1.f) empty = __int_as_float(0x7fffffff);
-        if (d == 0.f || d == -1.f) continue;
-        // (m = -infinity: a NaN sum)
-        const float f = m == -INFINITY ? 1.f : fast_exp2(m - top);
-        const float4 x = so[w][warp][lane];
-        sum += f * d;
-        y.x += f * x.x;
-        y.y += f * x.y;
-        y.z += f * x.z;
-        y.w += f * x.w;
+          for (int q = 0; q < 2; ++q) {
+            const float4 v = so[w][q][lane];
+            y[q].x += f * v.x;
+            y[q].y += f * v.y;
+            y[q].z += f * v.z;
+            y[q].w += f * v.w;
+          }
+        }
+        x.den = sum == 0.f && nothing ? -1.f : sum;
+        x.acc[0] = y[0];
+        x.acc[1] = y[1];
       }
-      if (sum == 0.f) y = make_float4(empty, empty, empty, empty);
-      const float inv = sum == 0.f ? 1.f : 1.f / sum;
-      if (r < seg.z) {
-        const int tok = r >> a.log2_g, head = seg.y + (r & ((1 << a.log2_g) - 1));
-        uint16_t* out = a.out + (static_cast<size_t>(seg.x + tok) * a.Hq + head) * D + col * 16 +
-                        warp * 4;
-        *reinterpret_cast<uint2*>(out) =
-            make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
-      }
+      __syncthreads();
     }
-    __syncthreads();
+    if (part == 0 && r < seg.z) {
+      const float inv = x.den == 0.f    ? 0.f
+                        : x.den == -1.f ? __int_as_float(0x7fffffff)
+                                        : 1.f / x.den;
+      const int tok = r >> a.log2_g, head = seg.y + (r & ((1 << a.log2_g) - 1));
+      uint16_t* out = a.out + (static_cast<size_t>(seg.x + tok) * a.Hq + head) * D + col * 8;
+      *reinterpret_cast<uint4*>(out) =
+          make_uint4(pack_bf16x2(x.acc[0].x * inv, x.acc[0].y * inv),
+                     pack_bf16x2(x.acc[0].z * inv, x.acc[0].w * inv),
+                     pack_bf16x2(x.acc[1].x * inv, x.acc[1].y * inv),
+                     pack_bf16x2(x.acc[1].z * inv, x.acc[1].w * inv));
+    }
   }
 }
 
