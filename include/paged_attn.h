@@ -640,6 +640,7 @@ int paged_tree_accept(void* const* pools, int32_t num_pools, int32_t num_blocks,
  * 1 <= budget, sinks + recent <= budget.  A length outside [0, max_blocks * 16]
  * is clamped, T < L taken as L (PKA_DEVERR_SEQ_LEN); a table id outside the pool
  * leaves its rows unmoved (PKA_DEVERR_BAD_TABLE).
+ * key_mass, key_pos, new_mass and new_pos 16-byte aligned.
  * workspace: 4-byte aligned, at least paged_kv_evict_ws_bytes() bytes, needs no
  * initialisation; calls sharing one must not overlap on the GPU. */
 size_t paged_kv_evict_ws_bytes(int32_t num_layers, int32_t B, int32_t Hkv, int32_t max_blocks,

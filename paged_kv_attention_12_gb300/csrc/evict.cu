@@ -24,12 +24,13 @@ namespace {
 
 constexpr int kSelWarps = 32;
 constexpr int kSelThreads = kSelWarps * 32;
-constexpr int kKeep = 16;                 // keys per thread that stay in registers
-constexpr int kBins = 2048;
-// digits of a 32-bit rank, from the top: 11, 11 and 10 bits
-constexpr int kPasses = 3;
-__device__ __forceinline__ int digit_shift(int pass) { return pass == 0 ? 21 : pass == 1 ? 10 : 0; }
-__device__ __forceinline__ int digit_bits(int pass) { return pass == 2 ? 10 : 11; }
+constexpr int kGroup = 4;                 // neighbouring keys that a lane takes at once
+// The n-th largest rank is found digit by digit, 8 bits from the top.  A lane
+// counts in a copy of the histogram of its own (bank = lane): masses share few
+// exponents and held keys one rank, and in a single copy the lanes of a warp
+// wait for one another.
+constexpr int kDigits = 4, kBins = 256;
+constexpr int kCtaKeys = 16384;           // keys of a CTA of a cluster, at most (8 CTAs: more)
 
 constexpr uint32_t kHeld = 0xffffffffu;   // above every mass
 
@@ -40,24 +41,24 @@ __device__ __forceinline__ uint32_t rank_of(float mass) {
   return x & 0x80000000u ? ~x : x | 0x80000000u;
 }
 
+// Ranks of the CTA's keys lie in shared memory (those past a.rank_room are made
+// again from mass and position where they are wanted), and every pass over them
+// is a short loop: with the ranks in registers the unrolled passes were 32 KB of
+// instructions, which a launch fetches anew (one row of 411 keys 13 us).
 template <int CTAS>
-__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const EvictArgs a) {
-  // hist is read, and totals are written, by the other CTAs of the cluster
-  __shared__ int hist[kPasses][kBins];
-  __shared__ int totals[4][CTAS];
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(
+    const __grid_constant__ EvictArgs a) {
+  extern __shared__ int hist[];          // [kBins][32], then the ranks
+  __shared__ int digit[kDigits][kBins];  // read by the other CTAs of the cluster,
+  __shared__ int totals[3][CTAS];        // written by them
+  __shared__ int sums[kBins];
   __shared__ int warp_sum[kSelWarps];
   __shared__ int found[3];
   __shared__ int shared_block;
+  uint32_t* ranks = reinterpret_cast<uint32_t*>(hist + kBins * 32);
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = CTAS > 1 ? static_cast<int>(cluster.block_rank()) : 0;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  auto sync = [&]() {
-    if constexpr (CTAS > 1)
-      cluster.sync();
-    else
-      __syncthreads();
-  };
-  for (int i = threadIdx.x; i < kPasses * kBins; i += kSelThreads) hist[0][i] = 0;
   if (threadIdx.x == 0) shared_block = 0;
   launch_dependents();
   wait_predecessor();
@@ -74,13 +75,13 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     T = max(T, L);
   }
   int n = min(L, a.budget);
-  __syncthreads();
+  const int32_t* table = a.tables + static_cast<size_t>(b) * a.max_blocks;
   if (a.refcounts != nullptr && n < L) {
     // a block that would be written and that another request reads too
-    const int32_t* row = a.tables + static_cast<size_t>(b) * a.max_blocks;
+    __syncthreads();
     bool shared = false;
     for (int j = threadIdx.x; j < (n + kBlockSize - 1) / kBlockSize; j += kSelThreads) {
-      const int id = row[j];
+      const int id = table[j];
       if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks))
         shared = shared || a.refcounts[id] > 1;
     }
@@ -98,92 +99,152 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
   int32_t* new_pos = a.new_pos + first;
   // keys without a position are the latest ones, in order
   auto position = [&](int t, int p) { return p >= 0 ? p : T - (L - t); };
+  auto rank_at = [&](float m, int at) {
+    return at < a.sinks || at >= T - a.recent ? kHeld : rank_of(m);
+  };
 
-  // this warp's keys: a run of its own, 32 at a time
+  // this warp's keys [lo, hi): a run of its own
   const int per_warp = ((L + CTAS * kSelWarps - 1) / (CTAS * kSelWarps) + 31) / 32 * 32;
-  const int lo = min(static_cast<long long>(rank * kSelWarps + warp) * per_warp,
-                     static_cast<long long>(L));
+  const int cta_lo = static_cast<int>(
+      min(static_cast<long long>(rank) * kSelWarps * per_warp, static_cast<long long>(L)));
+  const int lo = static_cast<int>(
+      min(static_cast<long long>(rank * kSelWarps + warp) * per_warp, static_cast<long long>(L)));
   const int hi = min(lo + per_warp, L);
+  // f(t): the lane's keys t .. t + 3 (t < hi; a row is a multiple of 16 keys, so
+  // all four can be read).  Every lane of the warp makes every step.
+  auto each = [&](auto f) {
+#pragma unroll 1
+    for (int g = lo; g < hi; g += 32 * kGroup) f(g + kGroup * lane);
+  };
+  auto load = [&](int t, float* m, int* p) {
+    const float4 x = *reinterpret_cast<const float4*>(mass + t);
+    const int4 y = *reinterpret_cast<const int4*>(pos + t);
+    m[0] = x.x, m[1] = x.y, m[2] = x.z, m[3] = x.w;
+    p[0] = position(t, y.x), p[1] = position(t + 1, y.y);
+    p[2] = position(t + 2, y.z), p[3] = position(t + 3, y.w);
+  };
+  auto store = [&](int t, const float* m, const int* p) {
+    *reinterpret_cast<float4*>(new_mass + t) = make_float4(m[0], m[1], m[2], m[3]);
+    *reinterpret_cast<int4*>(new_pos + t) = make_int4(p[0], p[1], p[2], p[3]);
+  };
   if (n == L) {
-    for (int t = lo + lane; t < hi; t += 32) {
-      new_mass[t] = mass[t];
-      new_pos[t] = position(t, pos[t]);
-    }
+    each([&](int t) {
+      if (t >= hi) return;
+      float m[kGroup];
+      int p[kGroup];
+      load(t, m, p);
+      if (t + kGroup <= hi) {
+        store(t, m, p);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kGroup; ++k)
+          if (t + k < hi) {
+            new_mass[t + k] = m[k];
+            new_pos[t + k] = p[k];
+          }
+      }
+    });
     return;  // the whole cluster
   }
-
-  auto rank_at = [&](int t) -> uint32_t {
-    const float m = mass[t];
-    const int p = position(t, pos[t]);
-    return p < a.sinks || p >= T - a.recent ? kHeld : rank_of(m);
-  };
-  uint32_t keep[kKeep];
+  // the four keys' ranks; keys past the warp's end: 0
+  auto ranks_of = [&](int t, uint32_t* u) {
+    if (t >= hi) {
 #pragma unroll
-  for (int k = 0; k < kKeep; ++k) {
-    const int t = lo + 32 * k + lane;
-    keep[k] = t < hi ? rank_at(t) : 0;
-  }
-  // f(t, rank, whether the lane has a key) for the warp's keys, in order; a
-  // step's lanes hold consecutive keys
-  auto each = [&](auto f) {
-#pragma unroll
-    for (int k = 0; k < kKeep; ++k)
-      if (lo + 32 * k < hi) f(lo + 32 * k + lane, keep[k], lo + 32 * k + lane < hi);
-    for (int base = lo + 32 * kKeep; base < hi; base += 32) {
-      const int t = base + lane;
-      f(t, t < hi ? rank_at(t) : 0u, t < hi);
+      for (int k = 0; k < kGroup; ++k) u[k] = 0;
+      return;
     }
+    if (t - cta_lo < a.rank_room) {
+      const uint4 x = *reinterpret_cast<const uint4*>(ranks + (t - cta_lo));
+      u[0] = x.x, u[1] = x.y, u[2] = x.z, u[3] = x.w;
+      return;
+    }
+    float m[kGroup];
+    int p[kGroup];
+    load(t, m, p);
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k) u[k] = t + k < hi ? rank_at(m[k], p[k]) : 0;
   };
 
   // ---------------------------------------- the rank of the last key that stays
   uint32_t prefix = 0;
   int need = n, equal = 0;  // keys still to find among those with this prefix
 #pragma unroll 1
-  for (int pass = 0; pass < kPasses; ++pass) {
-    const int shift = digit_shift(pass), bits = digit_bits(pass);
-    each([&](int, uint32_t u, bool in) {
-      if (in && (pass == 0 || u >> (shift + bits) == prefix))
-        atomicAdd(&hist[pass][(u >> shift) & ((1u << bits) - 1)], 1);
-    });
-    sync();
-    // bins from the top, two a thread
-    const int bins = 1 << bits;
-    int c[2] = {0, 0};
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int bin = bins - 1 - (2 * static_cast<int>(threadIdx.x) + e);
-      if (bin < 0) continue;
-      if constexpr (CTAS > 1) {
-#pragma unroll
-        for (int r = 0; r < CTAS; ++r) c[e] += *cluster.map_shared_rank(&hist[pass][bin], r);
-      } else {
-        c[e] = hist[pass][bin];
-      }
-    }
-    int incl = c[0] + c[1];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
+  for (int pass = 0; pass < kDigits; ++pass) {
+    const int shift = 24 - 8 * pass;
+    for (int i = threadIdx.x; i < kBins * 8; i += kSelThreads)
+      reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
     __syncthreads();
-    int above = incl - c[0] - c[1];
-    for (int w = 0; w < warp; ++w) above += warp_sum[w];
+    if (pass == 0) {
+      each([&](int t) {
+        if (t >= hi) return;
+        float m[kGroup];
+        int p[kGroup];
+        uint32_t u[kGroup];
+        load(t, m, p);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (above < need && need <= above + c[e]) {  // exactly one bin
-        found[0] = bins - 1 - (2 * static_cast<int>(threadIdx.x) + e);
-        found[1] = need - above;
-        found[2] = c[e];
-      }
-      above += c[e];
+        for (int k = 0; k < kGroup; ++k) {
+          u[k] = t + k < hi ? rank_at(m[k], p[k]) : 0;
+          if (t + k < hi) atomicAdd(&hist[(u[k] >> 24) * 32 + lane], 1);
+        }
+        if (t - cta_lo < a.rank_room)
+          *reinterpret_cast<uint4*>(ranks + (t - cta_lo)) = make_uint4(u[0], u[1], u[2], u[3]);
+      });
+    } else {
+      each([&](int t) {
+        uint32_t u[kGroup];
+        ranks_of(t, u);
+#pragma unroll
+        for (int k = 0; k < kGroup; ++k)
+          if (t + k < hi && u[k] >> (shift + 8) == prefix)
+            atomicAdd(&hist[(u[k] >> shift & 255) * 32 + lane], 1);
+      });
     }
     __syncthreads();
-    prefix = prefix << bits | static_cast<uint32_t>(found[0]);
+    for (int bin = warp; bin < kBins; bin += kSelWarps) {
+      const int c = __reduce_add_sync(0xffffffffu, hist[bin * 32 + lane]);
+      if (lane == 0) digit[pass][bin] = c;
+    }
+    const int* all = digit[pass];
+    if constexpr (CTAS > 1) {
+      cluster.sync();
+      if (threadIdx.x < kBins) {
+        int c = 0;
+#pragma unroll
+        for (int r = 0; r < CTAS; ++r)
+          c += *cluster.map_shared_rank(&digit[pass][threadIdx.x], r);
+        sums[threadIdx.x] = c;
+      }
+      all = sums;
+    }
+    __syncthreads();
+    if (warp == 0) {  // bins from the top, eight a lane
+      int c[8], mine = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        c[e] = all[kBins - 1 - (lane * 8 + e)];
+        mine += c[e];
+      }
+      int incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      int above = incl - mine;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (above < need && need <= above + c[e]) {  // exactly one bin
+          found[0] = kBins - 1 - (lane * 8 + e);
+          found[1] = need - above;
+          found[2] = c[e];
+        }
+        above += c[e];
+      }
+    }
+    __syncthreads();
+    prefix = prefix << 8 | static_cast<uint32_t>(found[0]);
     need = found[1];
     equal = found[2];
-    __syncthreads();
   }
   const uint32_t last = prefix;
 
@@ -192,12 +253,9 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
   auto before_of = [&](int count, int slot, int* total) {
     if (lane == 0) warp_sum[warp] = count;
     __syncthreads();
-    int below = 0, all = 0;
-    for (int w = 0; w < kSelWarps; ++w) {
-      const int v = warp_sum[w];
-      if (w < warp) below += v;
-      all += v;
-    }
+    const int v = lane < kSelWarps ? warp_sum[lane] : 0;
+    int below = __reduce_add_sync(0xffffffffu, lane < warp ? v : 0);
+    int all = __reduce_add_sync(0xffffffffu, v);
     if constexpr (CTAS > 1) {
       if (threadIdx.x < CTAS) *cluster.map_shared_rank(&totals[slot][rank], threadIdx.x) = all;
       cluster.sync();
@@ -213,71 +271,136 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     return below;
   };
 
+  // keys of rank `last`: all of them stay, or the first `need`
+  const bool some = need < equal;
   int total;
-  int ties = 0;  // keys of rank `last` before this warp's
-  if (need < equal) {
+  int tie = 0;  // those before this warp's
+  if (some) {
     int count = 0;
-    each([&](int, uint32_t u, bool in) {
-      count += __popc(__ballot_sync(0xffffffffu, in && u == last));
+    each([&](int t) {
+      uint32_t u[kGroup];
+      ranks_of(t, u);
+#pragma unroll
+      for (int k = 0; k < kGroup; ++k) count += t + k < hi && u[k] == last;
     });
-    ties = before_of(count, 0, &total);
+    tie = before_of(__reduce_add_sync(0xffffffffu, count), 0, &total);
   }
   const unsigned below_me = (1u << lane) - 1u;
-  auto stays = [&](uint32_t u, bool in, int& tie) {
-    const unsigned same = __ballot_sync(0xffffffffu, in && u == last);
-    const bool yes = in && (u > last || (u == last && tie + __popc(same & below_me) < need));
-    tie += __popc(same);
-    return yes;
+  // in: a property of the four keys; of all keys before the lane's in the step,
+  // how many have it (all: in the step)
+  auto before_lane = [&](const bool* in, int* all) {
+    int below = 0;
+    *all = 0;
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k) {
+      const unsigned m = __ballot_sync(0xffffffffu, in[k]);
+      below += __popc(m & below_me);
+      *all += __popc(m);
+    }
+    return below;
+  };
+  auto stays = [&](int t, const uint32_t* u, bool* yes, int& tie) {
+    if (!some) {
+#pragma unroll
+      for (int k = 0; k < kGroup; ++k) yes[k] = t + k < hi && u[k] >= last;
+      return;
+    }
+    bool same[kGroup];
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k) same[k] = t + k < hi && u[k] == last;
+    int all;
+    int at = tie + before_lane(same, &all);
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k) {
+      yes[k] = t + k < hi && (u[k] > last || (same[k] && at < need));
+      at += same[k];
+    }
+    tie += all;
   };
 
   // ------------------------------------------------- holes, movers and lists
-  int holes = 0, movers = 0, tie = ties;
-  each([&](int t, uint32_t u, bool in) {
-    const bool yes = stays(u, in, tie);
-    holes += __popc(__ballot_sync(0xffffffffu, in && t < n && !yes));
-    movers += __popc(__ballot_sync(0xffffffffu, t >= n && yes));
+  int holes = 0, movers = 0, tie_now = tie;
+  each([&](int t) {
+    uint32_t u[kGroup];
+    bool yes[kGroup];
+    ranks_of(t, u);
+    stays(t, u, yes, tie_now);
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k) {
+      holes += t + k < hi && t + k < n && !yes[k];
+      movers += t + k >= n && yes[k];
+    }
   });
   int moves;
-  int hole = before_of(holes, 1, &moves);
-  int mover = before_of(movers, 2, &moves);
+  int hole = before_of(__reduce_add_sync(0xffffffffu, holes), 1, &moves);
+  int mover = before_of(__reduce_add_sync(0xffffffffu, movers), 2, &moves);
   const size_t list = static_cast<size_t>(seg) * a.max_moves;
   if (rank == 0 && threadIdx.x == 0) a.counts[seg] = moves;
-  tie = ties;
-  each([&](int t, uint32_t u, bool in) {
-    const bool yes = stays(u, in, tie);
-    const unsigned hm = __ballot_sync(0xffffffffu, in && t < n && !yes);
-    const unsigned mm = __ballot_sync(0xffffffffu, t >= n && yes);
-    if (in) {
-      if (t < n && !yes) {
-        a.move_dst[list + hole + __popc(hm & below_me)] = t;
-      } else {
-        const float m = mass[t];
-        const int p = position(t, pos[t]);
-        if (t < n) {
-          new_mass[t] = m;
-          new_pos[t] = p;
-        } else {
-          if (yes) {  // the highest goes into the lowest hole
-            const size_t at = list + (moves - 1 - (mover + __popc(mm & below_me)));
-            a.move_src[at] = t;
-            a.move_mass[at] = m;
-            a.move_pos[at] = p;
-          }
-          new_mass[t] = 0.f;
-          new_pos[t] = -1;
-        }
+  each([&](int t) {
+    uint32_t u[kGroup];
+    bool yes[kGroup], is_hole[kGroup], is_mover[kGroup];
+    ranks_of(t, u);
+    stays(t, u, yes, tie);
+    bool any = false, all_stay = true;
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k) {
+      is_hole[k] = t + k < hi && t + k < n && !yes[k];
+      is_mover[k] = t + k >= n && yes[k];
+      any = any || yes[k];
+      all_stay = all_stay && yes[k] && t + k < n;
+    }
+    float m[kGroup] = {0.f, 0.f, 0.f, 0.f};
+    int p[kGroup] = {-1, -1, -1, -1};
+    if (any) load(t, m, p);
+    const int id = t >= n - kGroup && any ? table[t / kBlockSize] : 0;  // (of all four)
+    int all_h, all_m;
+    int h = hole + before_lane(is_hole, &all_h), v = mover + before_lane(is_mover, &all_m);
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k) {
+      if (is_hole[k]) a.move_dst[list + h] = t + k;
+      if (is_mover[k]) {  // the highest goes into the lowest hole
+        const size_t to = list + (moves - 1 - v);
+        // its row in the pools (counted in 32 bits), -1: a bad id
+        int row = -1;
+        if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks))
+          row = (id * a.Hkv + seg % a.Hkv) * kBlockSize + (t + k) % kBlockSize;
+        else
+          report(a.err, PKA_DEVERR_BAD_TABLE);
+        a.move_src[to] = row;
+        a.move_mass[to] = m[k];
+        a.move_pos[to] = p[k];
+      }
+      h += is_hole[k];
+      v += is_mover[k];
+    }
+    hole += all_h;
+    mover += all_m;
+    if (t >= hi) return;
+    if (t >= n) {
+#pragma unroll
+      for (int k = 0; k < kGroup; ++k) {
+        m[k] = 0.f;
+        p[k] = -1;
       }
     }
-    hole += __popc(hm);
-    mover += __popc(mm);
+    if (t + kGroup <= hi && (t >= n || all_stay)) {
+      store(t, m, p);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kGroup; ++k) {
+        if (t + k >= hi || is_hole[k]) continue;
+        new_mass[t + k] = t + k < n ? m[k] : 0.f;
+        new_pos[t + k] = t + k < n ? p[k] : -1;
+      }
+    }
   });
   if constexpr (CTAS > 1) cluster.sync();  // the others may still read this CTA's counts
 }
 
-// One warp per 8 moves of a segment: their K and V rows, all loads in flight
+// One warp per 4 moves of a segment: their K and V rows, all loads in flight
 // before the stores (sources and destinations are disjoint), and their masses
 // and positions.  `layers` segments' pools are in this launch.
-constexpr int kMoveBatch = 8;
+constexpr int kMoveBatch = 4;
 
 template <int D>
 __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__ EvictMoveArgs m) {
@@ -298,25 +421,29 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__
     const int seg = static_cast<int>(u / per_seg);
     const int at = static_cast<int>(u - static_cast<long long>(seg) * per_seg) * kMoveBatch;
     const size_t gseg = static_cast<size_t>(m.first_layer) * a.batch * a.Hkv + seg;
+    const size_t list = gseg * a.max_moves + at;
+    // the first lanes: the sources' rows, then the destinations' (the list may be
+    // read past its end: it lies in the workspace)
+    const int i = lane & (kMoveBatch - 1);
+    const bool listed = lane < 2 * kMoveBatch && at + i < a.max_moves;
+    int t = -1;
+    if (listed) t = lane < kMoveBatch ? a.move_src[list + i] : a.move_dst[list + i];
     const int count = min(kMoveBatch, a.counts[gseg] - at);
     if (count <= 0) continue;
     const int layer = seg / (a.batch * a.Hkv);
     const int b = seg / a.Hkv % a.batch, head = seg % a.Hkv;
-    const size_t list = gseg * a.max_moves + at;
-    // lanes 0..7: sources, 8..15: destinations, as rows of the pools
-    long long row = -1;
-    if (lane < 2 * kMoveBatch && (lane & 7) < count) {
-      const int t = lane < kMoveBatch ? a.move_src[list + lane] : a.move_dst[list + (lane & 7)];
+    int row = i < count ? t : -1;
+    if (lane >= kMoveBatch && listed && i < count) {
       const int id = a.tables[static_cast<size_t>(b) * a.max_blocks + t / kBlockSize];
-      if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks))
-        row = (static_cast<long long>(id) * a.Hkv + head) * kBlockSize + t % kBlockSize;
-      else
+      if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks)) {
+        row = (id * a.Hkv + head) * kBlockSize + t % kBlockSize;
+      } else {
+        row = -1;
         report(a.err, PKA_DEVERR_BAD_TABLE);
-      if (lane >= kMoveBatch) {
-        const size_t key = gseg * (static_cast<size_t>(a.max_blocks) * kBlockSize) + t;
-        a.new_mass[key] = a.move_mass[list + (lane & 7)];
-        a.new_pos[key] = a.move_pos[list + (lane & 7)];
       }
+      const size_t key = gseg * (static_cast<size_t>(a.max_blocks) * kBlockSize) + t;
+      a.new_mass[key] = a.move_mass[list + i];
+      a.new_pos[key] = a.move_pos[list + i];
     }
     uint4 x[kMoveBatch][kSteps];
 #pragma unroll
@@ -347,21 +474,27 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__
 
 }  // namespace
 
-cudaError_t launch_evict_select(const EvictArgs& a, int layers, cudaStream_t stream) {
+// Rows of up to 16384 keys take a CTA, longer ones a cluster of two, four or eight
+// (131072 keys: 8 CTAs 18 us, one 40).
+cudaError_t launch_evict_select(const EvictArgs& args, int layers, cudaStream_t stream) {
+  EvictArgs a = args;
   const long long segs = static_cast<long long>(layers) * a.batch * a.Hkv;
   const long long keys = static_cast<long long>(a.max_blocks) * kBlockSize;
-  constexpr long long kOne = kSelThreads * kKeep;  // keys that one CTA keeps in registers
-  if (keys <= kOne)
-    return launch_overlapped(evict_select_kernel<1>, dim3(static_cast<unsigned>(segs)),
-                             kSelThreads, 0, stream, a);
-  if (keys <= 2 * kOne)
-    return launch_overlapped(evict_select_kernel<2>, dim3(static_cast<unsigned>(2 * segs)),
-                             kSelThreads, 0, stream, a, 2);
-  if (keys <= 4 * kOne)
-    return launch_overlapped(evict_select_kernel<4>, dim3(static_cast<unsigned>(4 * segs)),
-                             kSelThreads, 0, stream, a, 4);
-  return launch_overlapped(evict_select_kernel<8>, dim3(static_cast<unsigned>(8 * segs)),
-                           kSelThreads, 0, stream, a, 8);
+  auto launch = [&](auto kernel, int ctas) {
+    const long long mine = ((keys + ctas * kSelWarps - 1) / (ctas * kSelWarps) + 31) / 32 * 32 *
+                           kSelWarps;
+    a.rank_room = static_cast<int32_t>(mine < kCtaKeys ? mine : kCtaKeys);
+    const int bytes = (kBins * 32 + a.rank_room) * static_cast<int>(sizeof(int));
+    const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kernel),
+                                        (kBins * 32 + kCtaKeys) * static_cast<int>(sizeof(int)));
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(kernel, dim3(static_cast<unsigned>(ctas * segs)), kSelThreads, bytes,
+                             stream, a, ctas);
+  };
+  if (keys <= kCtaKeys) return launch(evict_select_kernel<1>, 1);
+  if (keys <= 2 * kCtaKeys) return launch(evict_select_kernel<2>, 2);
+  if (keys <= 4 * kCtaKeys) return launch(evict_select_kernel<4>, 4);
+  return launch(evict_select_kernel<8>, 8);
 }
 
 cudaError_t launch_evict_move(const EvictMoveArgs& m, int head_dim, int sm_count,

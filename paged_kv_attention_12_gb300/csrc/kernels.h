@@ -193,11 +193,12 @@ struct EvictArgs {
   int32_t* err;
   int32_t* counts;                 // workspace: [segments] moves,
   int32_t* kept;                   // [B] keys that stay,
-  int32_t* move_src;               // [segments][max_moves] and so on
-  int32_t* move_dst;
+  int32_t* move_src;               // [segments][max_moves]: a row of the pools, or -1
+  int32_t* move_dst;               // an index in the cache, and so on
   float* move_mass;
   int32_t* move_pos;
   int32_t batch, Hkv, num_blocks, max_blocks, budget, sinks, recent, max_moves;
+  int32_t rank_room;               // set by the launcher: keys of a CTA whose ranks it holds
 };
 
 constexpr int kMaxEvictLayers = 128;  // layers per launch of the moves

@@ -262,7 +262,9 @@ int paged_kv_evict(void* const* pools, int32_t num_layers, int32_t num_blocks,
   if (num_layers > 0x7fffffff / 2) return PKA_ERR_SHAPE;
   st = check_pools(pools, 2 * num_layers);
   if (st != PKA_OK) return st;
-  if (!aligned(workspace, 4)) return PKA_ERR_ALIGN;
+  if (!aligned(workspace, 4) || !aligned16(key_mass) || !aligned16(new_mass) ||
+      !aligned16(key_pos) || !aligned16(new_pos))
+    return PKA_ERR_ALIGN;
   // a cluster of up to 8 CTAs for each segment
   if (static_cast<int64_t>(num_layers) * B > (1 << 27) / num_kv_heads) return PKA_ERR_SHAPE;
   const EvictLayout lay = evict_layout(num_layers, B, num_kv_heads, max_blocks, budget);

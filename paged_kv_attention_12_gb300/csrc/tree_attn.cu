@@ -429,7 +429,9 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
     const int past = a.num_blocks * a.Hkv * 2;  // a group past the pool: zeros
     const uint64_t policy = policy_evict_first();
     int g = 0;                                  // tiles issued
-    bool ok = true;
+    // V's first loads wait for K's first tile: what the CTAs ask for at once lands
+    // in about 4 us, and S comes first (serving layer 41.0 -> 40.0 us)
+    bool ok = is_k || !any_work || warp_wait(&b_k[0], 0, a.err, failed);
     while (ok && walk.next<S>(t, &p)) {
       const int32_t* trow = a.tables + static_cast<size_t>(p.b) * a.max_blocks + p.j0;
       // the piece's blocks, 32 at a time (one per lane), read 32 ahead
@@ -787,7 +789,7 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
                                pack_bf16x2(o[q * 8 + 4] * inv, o[q * 8 + 5] * inv),
                                pack_bf16x2(o[q * 8 + 6] * inv, o[q * 8 + 7] * inv));
             }
-          } else {
+          } else if (row_valid) {
             // [D / 4][QR rows] float4: each store of a warp is consecutive
 #pragma unroll
             for (int e = 0; e < 16; ++e)
