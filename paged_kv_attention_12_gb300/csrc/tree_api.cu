@@ -172,8 +172,11 @@ int paged_tree_attn_ws(const void* q, void* out, const pka_kv_pool* kv,
   a.total_q = total_q;
   a.max_query_len = max_query_len;
   a.min_chunk = pka::kTreePieceUnits(kv->head_dim) + 8;
-  a.whole_slack = kv->head_dim == 256 ? 16 : 32;
-  a.may_cut = segs > std::min(sms, pka::kTreeMaxCtas) || longest > a.whole_slack;
+  // A merge costs about 6 us, as much as streaming 28 blocks at D = 256 (a
+  // sliding layer of 64 segments of 34 blocks: cut 23.1 us, whole 20.9).
+  a.whole_slack = kv->head_dim == 256 ? 28 : 56;
+  a.may_cut = segs > std::min(sms, pka::kTreeMaxCtas) ||
+              longest + pka::kTreePieceUnits(kv->head_dim) > a.min_chunk + a.whole_slack;
   a.scale = params->scale;
   a.softcap = params->softcap > 1e38f ? 0.f : params->softcap;
   a.window = params->window;

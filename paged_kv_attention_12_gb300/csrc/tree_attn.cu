@@ -430,8 +430,11 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
     const uint64_t policy = policy_evict_first();
     int g = 0;                                  // tiles issued
     // V's first loads wait for K's first tile: what the CTAs ask for at once lands
-    // in about 4 us, and S comes first (serving layer 41.0 -> 40.0 us)
-    bool ok = is_k || !any_work || warp_wait(&b_k[0], 0, a.err, failed);
+    // in about 4 us, and S comes first (D = 256: serving layer 40.4 -> 39.5 us, a
+    // sliding one 21.1 -> 20.7).  D = 128 gains nothing (four long requests 115.0 us
+    // without, 115.2 with it) and a small call loses (8.3 -> 8.9).
+    const bool late = D == 256 && !is_k && walk.rem > S::kPieceUnits + 4 * BPT;
+    bool ok = true;
     while (ok && walk.next<S>(t, &p)) {
       const int32_t* trow = a.tables + static_cast<size_t>(p.b) * a.max_blocks + p.j0;
       // the piece's blocks, 32 at a time (one per lane), read 32 ahead
@@ -455,7 +458,9 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
         }
         const int at = __shfl_sync(0xffffffffu, now, (j + lane % BPT) & 31);
         const int st = g % nst;
-        if (g >= nst) ok = warp_wait(&freed[st], (g / nst - 1) & 1, a.err, failed);
+        const bool again = g >= nst;
+        if (again || (late && g == 0))
+          ok = warp_wait(again ? &freed[st] : &b_k[0], again ? (g / nst - 1) & 1 : 0, a.err, failed);
         if (!ok || __any_sync(0xffffffffu, stop_requested(failed))) {
           ok = false;
           break;
@@ -1000,7 +1005,7 @@ cudaError_t launch_tree_t(const TreeArgs& a, int sm_count, cudaStream_t stream) 
   m.Hq = a.Hq;
   m.log2_g = t.log2_g;
   m.chunks = grid;
-  return launch_overlapped(tree_merge_kernel<D, QR>, dim3(sm_count * 4), kMergeWarps * 32, 0,
+  return launch_overlapped(tree_merge_kernel<D, QR>, dim3(sm_count * 8), kMergeWarps * 32, 0,
                            stream, m);
 }
 
