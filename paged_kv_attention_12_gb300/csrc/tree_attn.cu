@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
         const uint64_t* masks = reinterpret_cast<const uint64_t*>(a.masks) + p.q0;
         see.mask = masks[tok] & own_bits;
         const int deep = __popcll(see.mask);
-        see.kmin = a.window > 0 ? see.base + max(deep, 1) - a.window : 0;
+        see.kmin = a.window > 0 ? max(0, see.base + max(deep, 1) - a.window) : 0;
         if (a.window > 0 && a.window < 64) {  // ancestors may lie before the window
           uint64_t left = see.mask;
           while (left != 0) {
@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
       }
       // tiles that not every row sees whole: from the window's edge and from
       // the drafted keys on
-      const int edge_lo = a.window > 0 ? p.L - a.window : 0;
+      const int edge_lo = a.window > 0 ? max(0, p.L - a.window) : 0;
       const int edge_hi = see.base;
       float m_ref = -INFINITY, l = 0.f;
       bool seen = false;

@@ -141,7 +141,7 @@ def test_lengths_and_tree_sizes(D, lens, ns):
 
 
 @pytest.mark.parametrize("D", [128, 256])
-@pytest.mark.parametrize("window", [1, 2, 5, 16, 17, 63, 64, 100, 1000])
+@pytest.mark.parametrize("window", [1, 2, 5, 16, 17, 63, 64, 100, 1000, 2 ** 31 - 1])
 def test_windows(D, window):
     c = make([40, 300, 70, 513], [33, 20, 64, 1], D=D, window=window, seed=window)
     err = i32([0])
