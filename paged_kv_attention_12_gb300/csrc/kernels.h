@@ -159,7 +159,7 @@ cudaError_t launch_tree_plan(const TreePlanArgs& a, cudaStream_t stream);
 
 // Walk of the trees along the target's tokens, and the move of the accepted
 // tokens' K/V rows.
-constexpr int kMaxTreePools = 256;  // pools per launch
+constexpr int kMaxTreePools = 255;  // pools per launch
 struct TreeAcceptArgs {
   void* pools[kMaxTreePools];
   const int32_t* parents;          // [total_q]

@@ -204,7 +204,7 @@ int paged_tree_accept(void* const* pools, int32_t num_pools, int32_t num_blocks,
     return PKA_ERR_NULL;
   st = check_pools(pools, num_pools);
   if (st != PKA_OK) return st;
-  if (num_kv_heads > 1024) return PKA_ERR_SHAPE;  // (256 pools a launch, 4 warps a CTA: 2^16 CTAs)
+  if (num_kv_heads > 1024) return PKA_ERR_SHAPE;  // (255 pools a launch, 4 warps a CTA)
   pka::TreeAcceptArgs a{};
   a.parents = parents;
   a.tokens = tokens;

@@ -632,10 +632,17 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
             whole = whole && vis[c] == ~0ull;
             seen = seen || vis[c] != 0;
           }
-          const bool need_mask = __any_sync(0xffffffffu, !whole);
+          // Rows of no token hold what the MMA left there: they have no say in the
+          // warp's votes, and need no mask.
+          const bool need_mask = __any_sync(0xffffffffu, row_valid && !whole);
           bool folded = false, have_max = false;
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
           if (capped) {
+            if (need_mask) {  // (what lies in a hidden column has no say either)
+#pragma unroll
+              for (int c = 0; c < BN; ++c)
+                if (!((vis[c / 64] >> (c % 64)) & 1)) s[c] = 0.f;
+            }
             float n4[4] = {INFINITY, INFINITY, INFINITY, INFINITY};
 #pragma unroll
             for (int c = 0; c < BN / 2; ++c) {
@@ -645,19 +652,22 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
             const float amax = fmaxf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])),
                                      -fminf(fminf(n4[0], n4[1]), fminf(n4[2], n4[3])));
             // the form of cap * tanh(s * scale / cap): a short or a long series
-            // while every argument of the warp is below 1/8 or 1/2, else exp2
-            if (fold_ok && __all_sync(0xffffffffu, amax * cap_mag < 0.125f)) {
+            // while every argument of the warp's rows is below 1/8 or 1/2, else
+            // for each of them the long series or exp2 (whose error, 7e-7 of the
+            // cap, a small logit would feel)
+            const float far = row_valid ? amax * cap_mag : 0.f;
+            if (fold_ok && __all_sync(0xffffffffu, far < 0.125f)) {
               folded = true;
               have_max = !need_mask;
-            } else if (__all_sync(0xffffffffu, amax * cap_mag < 0.125f)) {
-#pragma unroll
-              for (int c = 0; c < BN; ++c) s[c] = cap_out * tanh_taylor_short(s[c] * cap_in);
-            } else if (__all_sync(0xffffffffu, amax * cap_mag < 0.5f)) {
+            } else if (__all_sync(0xffffffffu, far < 0.5f)) {
 #pragma unroll
               for (int c = 0; c < BN; ++c) s[c] = cap_out * tanh_taylor(s[c] * cap_in);
             } else {
 #pragma unroll
-              for (int c = 0; c < BN; ++c) s[c] = cap_out * tanh_via_exp2(s[c] * cap_in);
+              for (int c = 0; c < BN; ++c) {
+                const float y = s[c] * cap_in;
+                s[c] = cap_out * (fabsf(y) < 0.5f ? tanh_taylor(y) : tanh_via_exp2(y));
+              }
             }
           } else if (prescale) {
 #pragma unroll
@@ -687,7 +697,7 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
           // O moves to a new reference only when the maximum grows by more
           // than 2^8: every weight stays below 2^8, and O and the sum share
           // the reference, so the result does not depend on it
-          const bool resc = j > 0 && m_new > m_ref + 8.f;
+          const bool resc = j > 0 && row_valid && m_new > m_ref + 8.f;
           if (__any_sync(0xffffffffu, resc)) {
             if (!warp_wait(&b_pv[(g - 1) & 1], ((g - 1) >> 1) & 1, a.err, failed)) {
               ok = false;

@@ -42,14 +42,15 @@ def tree(n, rng, reach=6):
 
 
 def make(lens, ns, *, hq=8, hkv=2, D=128, window=0, softcap=0.0, scale=None, seed=0, pad=3,
-         drop=True, masks=None, spare=3):
-    """A batch of trees.  What no query may read holds NaN: slots behind a sequence,
-    blocks of no table, and (drop) blocks before every window, whose ids are -1."""
+         drop=True, masks=None, spare=3, poison=NAN):
+    """A batch of trees.  What no query may read holds ``poison``: slots behind a
+    sequence, blocks of no table, and (drop) blocks before every window, whose ids
+    are -1."""
     rng = np.random.default_rng(seed)
     g = torch.Generator().manual_seed(seed)
     nbs = [-(-x // 16) for x in lens]
     blocks = sum(nbs) + spare
-    k, v = (torch.full((blocks, hkv, 16, D), NAN) for _ in range(2))
+    k, v = (torch.full((blocks, hkv, 16, D), poison) for _ in range(2))
     perm = rng.permutation(blocks)
     table, at = np.full((len(lens), max(nbs + [1]) + 1), -1), 0
     for b, (L, n, nb) in enumerate(zip(lens, ns, nbs)):
@@ -157,6 +158,35 @@ def test_caps_and_scales(softcap, scale):
     for D in (128, 256):
         c = make([150, 90], [20, 31], D=D, softcap=softcap, scale=scale, seed=D)
         check(c, run(c))
+
+
+@pytest.mark.parametrize("poison", [math.inf, -math.inf, 3e38])
+@pytest.mark.parametrize("softcap", [0.0, 50.0, 1e6])
+def test_what_lies_beside_the_keys_has_no_say(softcap, poison):
+    """Stale slots and rows of no token pick no form of the logits: the bits are
+    those beside NaN, and a cap of 1e6 keeps its small logits."""
+    for D in (128, 256):
+        args = dict(D=D, hq=4, softcap=softcap, seed=3)
+        c = make([150, 90, 21], [20, 9, 3], poison=poison, **args)
+        d = make([150, 90, 21], [20, 9, 3], **args)
+        out = run(c)
+        assert torch.equal(out, run(d))
+        check(d, out)
+
+
+@pytest.mark.parametrize("D", [128, 256])
+def test_one_row_far_out_under_a_large_cap(D):
+    """A row whose logits reach the cap does not cost its neighbours their accuracy."""
+    c = make([300, 40], [16, 8], D=D, softcap=1e5, scale=1.0, seed=7)
+    c["q"][3] *= 4096
+    ref, _ = expected(c)
+    got = f64(run(c))
+    rest = [r for r in range(24) if r != 3]
+    calm = make([300, 40], [16, 8], D=D, softcap=1e5, scale=1.0, seed=7)
+    want, spread = expected(calm)
+    off = np.abs(got[rest] - want[rest]) / bound(dict(calm, softcap=0.0), want[rest], spread[rest])
+    assert off.max() <= 1.0, off.max()
+    assert np.all(np.isfinite(got[:24]))
 
 
 @pytest.mark.parametrize("D", [128, 256])
