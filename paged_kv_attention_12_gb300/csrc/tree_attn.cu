@@ -19,9 +19,9 @@
 // merges in key order.  Segments that are no longer than a chunk and what a merge
 // costs stay whole, one per CTA.
 //
-// Warps of a CTA: QR / 32 softmax warps (thread r owns row r, its S and O
-// rows in TMEM lane r), one TMA warp each for K, V and Q, and one that issues
-// the MMAs.  The rings of K and V run on over the pieces of a chunk, so that
+// Warps of a CTA: four softmax warps (a row of S and O lies in a TMEM lane; a thread
+// owns a row, or with QR = 64 half of its columns), one TMA warp each for K, V and
+// Q, and one that issues the MMAs.  The rings of K and V run on over the pieces of a chunk, so that
 // the loads do not stop for an epilogue.
 //
 // Where the time goes (a serving layer: 32 trees of 8 to 16 tokens over 512 to
@@ -71,10 +71,14 @@ struct TreeShape {
   static constexpr int oV = oK + KST * kStage;
   static constexpr int oEnd = oV + VST * kStage;
   static constexpr int kSmemBytes = oEnd + 1024;    // slack to align the base to 1 KiB
-  static constexpr int kSoftmaxWarps = QR / 32;
-  static constexpr int kWarpK = kSoftmaxWarps, kWarpV = kWarpK + 1, kWarpMma = kWarpK + 2,
-                       kWarpQ = kWarpK + 3;
-  static constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
+  // Four softmax warps.  With 128 rows a thread owns a row.  With 64 two threads
+  // share one, half of a tile's columns each, in the warps that reach the row's TMEM
+  // lanes (warp w: lanes 32 (w % 4) ..): 0 and 4, 1 and 5.
+  static constexpr int kSoftmaxWarps = 4;
+  static constexpr int kSplit = 128 / QR;
+  static constexpr int CN = BN / kSplit;            // columns of a thread
+  static constexpr int kWarpK = kSplit == 2 ? 2 : 4, kWarpV = kWarpK + 1, kWarpMma = 6, kWarpQ = 7;
+  static constexpr int kThreads = 8 * 32;
   static constexpr int kPieceUnits = kTreePieceUnits(D);
   // TMEM columns: S_j (fp32) in buffer j % 2 at (j % 2) * BN, O at 256, P_j
   // (bf16 pairs) in buffer j % 2 at kTmemP + (j % 2) * BN / 2.
@@ -299,9 +303,11 @@ struct Sight {
 // Adds the infinities and NaN of V's keys [lo, hi) that the row sees to its
 // finished output row (the tiles that not every row sees whole go through the
 // MMA with such values as zeros, which would reach the other rows as 0 * inf).
-template <int D, bool kPartial>
+// Columns [first, first + N) of them.
+template <int N, bool kPartial>
 __device__ __noinline__ void add_wild(const TreeArgs& a, const Piece& p, const Sight& see, int lo,
-                                      int hi, float* prow, int pstride, uint16_t* orow) {
+                                      int hi, int first, int D, float* prow, int pstride,
+                                      uint16_t* orow) {
   const int32_t* trow = a.tables + static_cast<size_t>(p.b) * a.max_blocks;
   for (int t = lo; t < hi; ++t) {
     if (!(see.columns(t) & 1)) continue;
@@ -309,7 +315,7 @@ __device__ __noinline__ void add_wild(const TreeArgs& a, const Piece& p, const S
     if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.num_blocks)) continue;
     const uint16_t* v = a.v + ((static_cast<size_t>(id) * a.Hkv + p.kvh) * kBlockSize +
                                t % kBlockSize) * D;
-    for (int d = 0; d < D; ++d) {
+    for (int d = first; d < first + N; ++d) {
       const uint32_t bits = v[d];
       if ((bits & 0x7f80u) != 0x7f80u) continue;
       const float x = __uint_as_float(bits << 16);
@@ -328,7 +334,8 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
   constexpr int BN = S::BN, BPT = S::BPT, DC = S::DC, NW = S::kSoftmaxWarps;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t b_q, b_qfree, b_k[S::KST], b_kfree[S::KST], b_v[S::VST], b_vfree[S::VST],
-      b_s[2], b_pv[2], b_p[2];
+      b_s[2], b_pv[2], b_p[2], b_pair[2];
+  __shared__ float pair_value[2][2][64];  // [exchange % 2][half][row]
   __shared__ uint32_t tmem_slot;
   __shared__ int failed_flag, wild_piece[2], warp_sums[S::kThreads / 32], longest;
   __shared__ Walk start;  // of the CTA's chunk
@@ -356,6 +363,7 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
       mbar_init(&b_s[i], 1);
       mbar_init(&b_pv[i], 1);
       mbar_init(&b_p[i], NW);
+      mbar_init(&b_pair[i], 2);
     }
     failed_flag = 0;
     wild_piece[0] = wild_piece[1] = 0;
@@ -574,8 +582,25 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
     __syncwarp();
   } else {
     // ============================== softmax ==============================
-    const int r = threadIdx.x;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    constexpr int SPLIT = S::kSplit, CN = S::CN;
+    const int group = SPLIT == 2 ? warp & 1 : warp;  // 32 rows
+    const int half = SPLIT == 2 ? warp >> 2 : 0;     // which columns of them
+    const int sw = SPLIT == 2 ? group + 2 * half : warp;
+    const int r = group * 32 + lane;
+    const int c0 = half * CN;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(group * 32) << 16);
+    // Two threads of a row give each other a value (an mbarrier per 32 rows: a
+    // partner that has stopped is waited for no longer than anything else).
+    int exchanges = 0;
+    auto exchange = [&](float mine, float* other) -> bool {
+      pair_value[exchanges & 1][half][r] = mine;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b_pair[group]);
+      if (!warp_wait(&b_pair[group], exchanges & 1, a.err, failed)) return false;
+      *other = pair_value[exchanges & 1][half ^ 1][r];
+      ++exchanges;
+      return true;
+    };
     const bool capped = a.softcap > 0.f;
     const float sl2 = a.scale * kLog2e;
     // scale <= 0 and caps: the logits are formed before the mask
@@ -597,7 +622,7 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
       const int row = p.tile * QR + r;
       const int tok = row >> t.log2_g;
       const bool row_valid = tok < p.n;
-      const bool idle = ((p.tile * QR + warp * 32) >> t.log2_g) >= p.n;  // no row of this warp
+      const bool idle = ((p.tile * QR + group * 32) >> t.log2_g) >= p.n;  // no row of this warp
       const int nt = (p.blocks + BPT - 1) / BPT;
       const int t_begin = p.j0 * kBlockSize;
       const int t_end = min(t_begin + p.blocks * kBlockSize, p.L);
@@ -634,20 +659,27 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
         }
         tc_fence_after();
         if (!idle) {
-          float s[BN];
+          float s[CN];
+          if constexpr (CN == 32) {
+            tmem_ld32(lane_base + st * BN + c0, s);
+          } else {
 #pragma unroll
-          for (int c = 0; c < BN / 64; ++c) {
-            float x[64];
-            tmem_ld64(lane_base + st * BN + c * 64, x);
+            for (int c = 0; c < CN / 64; ++c) {
+              float x[64];
+              tmem_ld64(lane_base + st * BN + c0 + c * 64, x);
 #pragma unroll
-            for (int e = 0; e < 64; ++e) s[c * 64 + e] = x[e];
+              for (int e = 0; e < 64; ++e) s[c * 64 + e] = x[e];
+            }
           }
-          uint64_t vis[BN / 64];
+          constexpr int kWords = (CN + 63) / 64;
+          uint64_t vis[kWords];
           bool whole = true;
 #pragma unroll
-          for (int c = 0; c < BN / 64; ++c) {
-            vis[c] = row_valid ? see.columns(t0 + c * 64) & bit_range(0, t_end - t0 - c * 64) : 0;
-            whole = whole && vis[c] == ~0ull;
+          for (int c = 0; c < kWords; ++c) {
+            constexpr uint64_t kAll = CN < 64 ? (1ull << (CN % 64)) - 1 : ~0ull;
+            const int at = c0 + c * 64;
+            vis[c] = row_valid ? see.columns(t0 + at) & bit_range(0, t_end - t0 - at) & kAll : 0;
+            whole = whole && vis[c] == kAll;
             seen = seen || vis[c] != 0;
           }
           // Rows of no token hold what the MMA left there: they have no say in the
@@ -658,12 +690,12 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
           if (capped) {
             if (need_mask) {  // (what lies in a hidden column has no say either)
 #pragma unroll
-              for (int c = 0; c < BN; ++c)
+              for (int c = 0; c < CN; ++c)
                 if (!((vis[c / 64] >> (c % 64)) & 1)) s[c] = 0.f;
             }
             float n4[4] = {INFINITY, INFINITY, INFINITY, INFINITY};
 #pragma unroll
-            for (int c = 0; c < BN / 2; ++c) {
+            for (int c = 0; c < CN / 2; ++c) {
               m4[c & 3] = max3f(m4[c & 3], s[2 * c], s[2 * c + 1]);
               n4[c & 3] = min3f(n4[c & 3], s[2 * c], s[2 * c + 1]);
             }
@@ -679,17 +711,17 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
               have_max = !need_mask;
             } else if (__all_sync(0xffffffffu, far < 0.5f)) {
 #pragma unroll
-              for (int c = 0; c < BN; ++c) s[c] = cap_out * tanh_taylor(s[c] * cap_in);
+              for (int c = 0; c < CN; ++c) s[c] = cap_out * tanh_taylor(s[c] * cap_in);
             } else {
 #pragma unroll
-              for (int c = 0; c < BN; ++c) {
+              for (int c = 0; c < CN; ++c) {
                 const float y = s[c] * cap_in;
                 s[c] = cap_out * (fabsf(y) < 0.5f ? tanh_taylor(y) : tanh_via_exp2(y));
               }
             }
           } else if (prescale) {
 #pragma unroll
-            for (int c = 0; c < BN; c += 2) {
+            for (int c = 0; c < CN; c += 2) {
               const float2 v = mul2(make_float2(s[c], s[c + 1]), make_float2(sl2, sl2));
               s[c] = v.x;
               s[c + 1] = v.y;
@@ -697,20 +729,28 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
           }
           if (need_mask) {
 #pragma unroll
-            for (int c = 0; c < BN; ++c)
+            for (int c = 0; c < CN; ++c)
               if (!((vis[c / 64] >> (c % 64)) & 1)) s[c] = -INFINITY;
           }
           if (!have_max) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) m4[e] = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < BN / 2; ++c) m4[c & 3] = max3f(m4[c & 3], s[2 * c], s[2 * c + 1]);
+            for (int c = 0; c < CN / 2; ++c) m4[c & 3] = max3f(m4[c & 3], s[2 * c], s[2 * c + 1]);
           }
           float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           if (folded)
             mx = mx * fmaf(mx * mx, fmaf(mx * mx, k5, k3), k1);
           else if (!prescale)
             mx *= sl2;
+          if constexpr (SPLIT == 2) {  // the row's maximum, of both halves
+            float other;
+            if (!exchange(mx, &other)) {
+              ok = false;
+              break;
+            }
+            mx = fmaxf(mx, other);
+          }
           const float m_new = fmaxf(m_ref, mx);
           // O moves to a new reference only when the maximum grows by more
           // than 2^8: every weight stays below 2^8, and O and the sum share
@@ -724,7 +764,7 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
             tc_fence_after();
             const float f = resc ? fast_exp2(m_ref - m_new) : 1.f;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
+            for (int c = half * (D / 32 / SPLIT); c < (half + 1) * (D / 32 / SPLIT); ++c) {
               float o[32];
               tmem_ld32(lane_base + S::kTmemO + c * 32, o);
 #pragma unroll
@@ -741,21 +781,26 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
           auto make_p = [&](auto logit) {
             float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int h = 0; h < BN / 64; ++h) {
-              uint32_t pk[32];
+            for (int h = 0; h < kWords; ++h) {
+              constexpr int kPairs = CN < 64 ? CN / 2 : 32;
+              uint32_t pk[kPairs];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
+              for (int e = 0; e < kPairs; ++e) {
                 const float2 x = logit(make_float2(s[h * 64 + 2 * e], s[h * 64 + 2 * e + 1]));
                 const float2 w = make_float2(fast_exp2(x.x), fast_exp2(x.y));
                 if (e & 1)
                   sum1 = add2(sum1, w);
                 else
                   sum0 = add2(sum0, w);
-                // weights go to the MMA as bf16 (half a step 2^-9 each, over
-                // keys of both signs; the sum is of the unrounded ones)
+                // weights go to the MMA as bf16 (off by 2^-8 of a weight at
+                // most; the sum is of the unrounded ones)
                 pk[e] = pack_bf16x2(w.x, w.y);
               }
-              tmem_st32_u(lane_base + S::kTmemP + st * (BN / 2) + h * 32, pk);
+              const uint32_t to = lane_base + S::kTmemP + st * (BN / 2) + c0 / 2 + h * 32;
+              if constexpr (kPairs == 16)
+                tmem_st16_u(to, pk);
+              else
+                tmem_st32_u(to, pk);
             }
             const float2 sum = add2(sum0, sum1);
             return sum.x + sum.y;
@@ -781,9 +826,9 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
           }
           uint8_t* vst = sV + vs * S::kStage;
           const int stale = min(BN, (p.L + kBlockSize - 1) / kBlockSize * kBlockSize - t0);
-          bool found = tame_rows<S>(vst, 0, min(BN, edge_lo - t0), warp, lane);
-          if (tame_rows<S>(vst, max(0, edge_hi - t0), min(BN, p.L - t0), warp, lane)) found = true;
-          clear_rows<S>(vst, max(0, p.L - t0), stale, warp, lane);
+          bool found = tame_rows<S>(vst, 0, min(BN, edge_lo - t0), sw, lane);
+          if (tame_rows<S>(vst, max(0, edge_hi - t0), min(BN, p.L - t0), sw, lane)) found = true;
+          clear_rows<S>(vst, max(0, p.L - t0), stale, sw, lane);
           if (found) *const_cast<volatile int*>(&wild_piece[piece & 1]) = piece;
           fence_proxy_async_smem();
         }
@@ -800,6 +845,15 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
         cut = make_int4(p.q0 + p.tile * (QR >> t.log2_g), p.kvh << t.log2_g,
                         min(QR, (p.n << t.log2_g) - p.tile * QR), 1 + (p.after + chunk - 1) / chunk);
       if (!idle) {
+        if constexpr (SPLIT == 2) {  // the row's sum, of both halves
+          float other;  // (-1: it sees keys, but they have no weight)
+          if (!exchange(l == 0.f && seen ? -1.f : l, &other)) {
+            ok = false;
+            break;
+          }
+          seen = seen || other != 0.f;
+          if (other != -1.f) l += other;
+        }
         // a row whose visible logits are all -infinity: 0 / 0; one that sees
         // nothing: 0
         const float inv = l > 0.f ? 1.f / l : (seen ? __int_as_float(0x7fffffff) : 0.f);
@@ -809,7 +863,7 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
             a.out + (static_cast<size_t>(p.q0 + tok) * a.Hq + (p.kvh << t.log2_g) +
                      (row & ((1 << t.log2_g) - 1))) * D;
 #pragma unroll 1
-        for (int c = 0; c < D / 64; ++c) {
+        for (int c = half * (D / 64 / SPLIT); c < (half + 1) * (D / 64 / SPLIT); ++c) {
           float o[64];
           tmem_ld64(lane_base + S::kTmemO + c * 64, o);
           if (direct) {
@@ -831,15 +885,16 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
                               o[4 * e + 3] * inv);
           }
         }
-        if (!direct)
+        if (!direct && half == 0)
           a.partial_lse[slot * QR + r] =
               l == 0.f ? -INFINITY : m_ref + log2f(l);  // (a NaN sum: NaN)
         if (row_valid && *const_cast<volatile int*>(&wild_piece[piece & 1]) == piece) {
           auto add = [&](int lo, int hi) {
             if (direct)
-              add_wild<D, false>(a, p, see, lo, hi, nullptr, 0, orow);
+              add_wild<D / SPLIT, false>(a, p, see, lo, hi, half * (D / SPLIT), D, nullptr, 0, orow);
             else
-              add_wild<D, true>(a, p, see, lo, hi, prow, QR * 4, nullptr);
+              add_wild<D / SPLIT, true>(a, p, see, lo, hi, half * (D / SPLIT), D, prow, QR * 4,
+                                        nullptr);
           };
           const int mid = min(t_end, max(t_begin, edge_lo));
           add(t_begin, mid);
