@@ -356,29 +356,39 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(
     float m[kGroup] = {0.f, 0.f, 0.f, 0.f};
     int p[kGroup] = {-1, -1, -1, -1};
     if (any) load(t, m, p);
-    const int id = t >= n - kGroup && any ? table[t / kBlockSize] : 0;  // (of all four)
-    int all_h, all_m;
-    int h = hole + before_lane(is_hole, &all_h), v = mover + before_lane(is_mover, &all_m);
+    const int step = t - kGroup * lane;  // the warp's first key: holes lie below n, movers above
+    if (step < n) {
+      int all;
+      int h = hole + before_lane(is_hole, &all);
 #pragma unroll
-    for (int k = 0; k < kGroup; ++k) {
-      if (is_hole[k]) a.move_dst[list + h] = t + k;
-      if (is_mover[k]) {  // the highest goes into the lowest hole
-        const size_t to = list + (moves - 1 - v);
-        // its row in the pools (counted in 32 bits), -1: a bad id
-        int row = -1;
-        if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks))
-          row = (id * a.Hkv + seg % a.Hkv) * kBlockSize + (t + k) % kBlockSize;
-        else
-          report(a.err, PKA_DEVERR_BAD_TABLE);
-        a.move_src[to] = row;
-        a.move_mass[to] = m[k];
-        a.move_pos[to] = p[k];
+      for (int k = 0; k < kGroup; ++k) {
+        if (is_hole[k]) a.move_dst[list + h] = t + k;
+        h += is_hole[k];
       }
-      h += is_hole[k];
-      v += is_mover[k];
+      hole += all;
     }
-    hole += all_h;
-    mover += all_m;
+    if (step + 32 * kGroup > n) {
+      const int id = any ? table[t / kBlockSize] : 0;  // (of all four)
+      int all;
+      int v = mover + before_lane(is_mover, &all);
+#pragma unroll
+      for (int k = 0; k < kGroup; ++k) {
+        if (is_mover[k]) {  // the highest goes into the lowest hole
+          const size_t to = list + (moves - 1 - v);
+          // its row in the pools (counted in 32 bits), -1: a bad id
+          int row = -1;
+          if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks))
+            row = (id * a.Hkv + seg % a.Hkv) * kBlockSize + (t + k) % kBlockSize;
+          else
+            report(a.err, PKA_DEVERR_BAD_TABLE);
+          a.move_src[to] = row;
+          a.move_mass[to] = m[k];
+          a.move_pos[to] = p[k];
+        }
+        v += is_mover[k];
+      }
+      mover += all;
+    }
     if (t >= hi) return;
     if (t >= n) {
 #pragma unroll
