@@ -328,3 +328,88 @@ def test_all_four_calls_in_one_graph():
         torch.cuda.synchronize()
         for x, w in zip((*state.values(), *outs.values()), results[shift]):
             assert torch.equal(x, w)
+
+
+def _good():
+    bf = dict(dtype=BF, device=DEV)
+    k, v = torch.zeros((8, 2, 16, 128), **bf), torch.zeros((8, 2, 16, 128), **bf)
+    table, first = i32(np.arange(4).reshape(1, 4)), i32([0, 3])
+    return dict(k=k, v=v, table=table, first=first, lens=i32([20]), parents=i32([-1, 0, 0]),
+                masks=torch.ones(3, dtype=torch.int64, device=DEV), pos=i32([0] * 3),
+                slots=i32([0] * 3), q=torch.zeros((3, 8, 128), **bf), out=torch.zeros((3, 8, 128), **bf),
+                ws=torch.zeros(binding.paged_tree_attn_ws_bytes(8, 2, 128, 3), dtype=torch.uint8,
+                               device=DEV), path=i32([[0] * 3]), one=i32([0]),
+                mass=torch.zeros((1, 1, 2, 64), device=DEV), kpos=i32(np.full((1, 1, 2, 64), -1)),
+                err=i32([0]))
+
+
+CALLS = dict(
+    plan=lambda c: binding.paged_tree_plan(c["parents"], c["first"], c["lens"], c["table"], 8, 3,
+                                           c["masks"], c["pos"], c["slots"], err=c["err"]),
+    attn=lambda c: binding.paged_tree_attn_ws(c["q"], c["out"], c["k"], c["v"], c["table"], c["first"],
+                                              c["masks"], c["lens"], 3, 64, c["ws"], scale=0.1,
+                                              err=c["err"]),
+    accept=lambda c: binding.paged_tree_accept([c["k"], c["v"]], c["parents"], c["pos"], c["pos"],
+                                               c["slots"], c["first"], c["lens"], c["path"], c["one"],
+                                               c["one"], c["one"], c["err"]),
+    evict=lambda c: binding.paged_kv_evict([c["k"], c["v"]], c["mass"], c["kpos"], c["table"], c["lens"],
+                                           None, 10, 1, 2, c["mass"], c["kpos"], c["one"], c["ws"],
+                                           err=c["err"]))
+
+
+@pytest.mark.parametrize("call,name", [
+    ("plan", "parents"), ("plan", "first"), ("plan", "lens"), ("plan", "table"), ("plan", "masks"),
+    ("plan", "pos"), ("plan", "slots"), ("plan", "err"), ("attn", "q"), ("attn", "out"), ("attn", "k"),
+    ("attn", "v"), ("attn", "table"), ("attn", "first"), ("attn", "masks"), ("attn", "lens"),
+    ("attn", "err"), ("accept", "k"), ("accept", "v"), ("accept", "parents"), ("accept", "pos"),
+    ("accept", "slots"), ("accept", "first"), ("accept", "lens"), ("accept", "path"), ("accept", "one"),
+    ("evict", "k"), ("evict", "v"), ("evict", "mass"), ("evict", "kpos"), ("evict", "table"),
+    ("evict", "lens"), ("evict", "one"), ("evict", "err")])
+def test_tensors_that_do_not_fit_are_refused(call, name):
+    """Another type, a strided view, another shape, a host tensor, no tensor: each is
+    refused before anything runs, and the right one is taken."""
+    CALLS[call](_good())
+    x = _good()[name]
+    wider = torch.zeros((*x.shape[:-1], 2 * x.shape[-1]), dtype=x.dtype, device=DEV)[..., ::2]
+    bad = [x.double(), x.cpu(), "no tensor"]
+    if x.numel() > 1:
+        bad.append(wider)
+    if name not in ("err",):
+        bad.append(torch.zeros((*x.shape[:-1], x.shape[-1] + 1), dtype=x.dtype, device=DEV))
+        bad.append(x[None])
+    for y in bad:
+        # (a table or a path may be wider, and then a mass no longer fits it)
+        if call != "evict" and name in ("table", "path") and y is not x and \
+                getattr(y, "is_cuda", False) and y.dtype is x.dtype and y.is_contiguous() and y.dim() == 2:
+            continue
+        with pytest.raises(ValueError):
+            CALLS[call](dict(_good(), **{name: y}))
+    torch.cuda.synchronize()
+
+
+def test_refusals_of_the_library_reach_python():
+    c = _good()
+    with pytest.raises(binding.PagedAttnError, match="PKA_ERR_WORKSPACE"):
+        CALLS["attn"](dict(c, ws=c["ws"][:1000]))
+    with pytest.raises(binding.PagedAttnError, match="PKA_ERR_ALIGN"):
+        CALLS["attn"](dict(c, ws=c["ws"][8:]))
+    with pytest.raises(binding.PagedAttnError, match="PKA_ERR_UNSUPPORTED"):
+        binding.paged_tree_plan(c["parents"], c["first"], c["lens"], c["table"], 8, 65, None, None,
+                                c["slots"])
+    with pytest.raises(binding.PagedAttnError, match="PKA_ERR_SHAPE"):
+        binding.paged_kv_evict([c["k"], c["v"]], c["mass"], c["kpos"], c["table"], c["lens"], None, 5,
+                               4, 4, c["mass"], c["kpos"], c["one"], c["ws"])
+    with pytest.raises(ValueError, match="pools"):
+        binding.paged_kv_evict([c["k"]], c["mass"], c["kpos"], c["table"], c["lens"], None, 5, 1, 1,
+                               c["mass"], c["kpos"], c["one"], c["ws"])
+    with pytest.raises((ValueError, TypeError)):
+        binding.paged_kv_evict([c["k"], c["v"]], c["mass"], c["kpos"], c["table"], c["lens"], None,
+                               2 ** 40, 1, 1, c["mass"], c["kpos"], c["one"], c["ws"])
+    # nothing to do: no rows, no requests
+    none = i32([]).view(0, 4)
+    binding.paged_tree_plan(i32([]), i32([0]), i32([]), none, 8, 3, None, None, i32([]))
+    binding.paged_tree_attn_ws(c["q"][:0], c["out"][:0], c["k"], c["v"], none, i32([0]), c["masks"][:0],
+                               i32([]), 3, 64, c["ws"], scale=0.1)
+    binding.paged_tree_accept([], i32([]), i32([]), i32([]), None, i32([0]), i32([]), i32([]).view(0, 3),
+                              i32([]), i32([]), i32([]))
+    torch.cuda.synchronize()
