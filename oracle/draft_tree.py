@@ -73,7 +73,7 @@ def tree_attention(q, k_pool, v_pool, tables, query_start_loc, masks, seq_lens, 
                     out[lo + i, h] = 0.0
                     continue
                 s = scale * (K[mine, h // G] @ q[lo + i, h])
-                if softcap > 0:
+                if 0 < softcap < np.inf:  # (an infinite cap is none)
                     s = softcap * np.tanh(s / softcap)
                 with np.errstate(invalid="ignore"):
                     p = np.exp(s - np.max(s))

@@ -100,12 +100,14 @@ def expected(c):
 def bound(c, ref, spread):
     """|out - ref| at most: the output's rounding, 2^-8 |ref|; the weights', 2^-8 sum
     p |v|; and what logits off by e do to the weights, 2 e sum p |v|: D products and
-    sums of fp32 (2^-23 of the sum of their sizes each, truncation allowed) and the
-    cap's tanh (7e-7 of the cap)."""
+    sums of fp32 (2^-23 of the sum of their sizes each, truncation allowed), and a
+    cap's forms, each off by less than 7e-7 of the cap and 2e-6 of the logit: the
+    short series below an argument of 1/8 (17/315 y^6 of it and a few roundings), the
+    long one below 1/2 (4.5e-7 / 0.46), exp2 above (7e-7 / 0.46)."""
     D = c["q"].shape[2]
     q, k = f64(c["q"]), f64(c["k"])
     size = abs(c["scale"]) * np.abs(q).sum(-1).max() * np.nanmax(np.abs(k))
-    e = D * 2.0 ** -23 * size + 7e-7 * c["softcap"]
+    e = D * 2.0 ** -23 * size + max(0.0, min(2e-6 * size, 7e-7 * c["softcap"]))
     return 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2 * e + 2.0 ** -14) * spread + 1e-30
 
 
@@ -153,7 +155,9 @@ def test_windows(D, window):
 
 
 @pytest.mark.parametrize("softcap,scale", [(50.0, None), (2.0, None), (0.5, 1.0), (50.0, -0.1),
-                                           (0.0, -0.1), (0.0, 0.0), (1000.0, 0.5)])
+                                           (0.0, -0.1), (0.0, 0.0), (1000.0, 0.5),
+                                           (1e-38, None), (1e-3, -2.0), (1e20, None), (1e37, 0.3),
+                                           (3e38, None), (math.inf, -0.2), (-1.0, 0.1)])
 def test_caps_and_scales(softcap, scale):
     for D in (128, 256):
         c = make([150, 90], [20, 31], D=D, softcap=softcap, scale=scale, seed=D)
