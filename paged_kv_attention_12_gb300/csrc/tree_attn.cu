@@ -25,13 +25,15 @@
 // the loads do not stop for an epilogue.
 //
 // Where the time goes (a serving layer: 32 trees of 8 to 16 tokens over 512 to
-// 4096 keys, 2 KV heads, D = 256; 154 MB, 40 us; global-timer stamps): 0.6 us to
+// 4096 keys, 2 KV heads, D = 256; 154 MB, 38.8 us; global-timer stamps): 0.6 us to
 // the chunk, 2 to the first copy, 2.5 to the first S, then 1.4 us for each tile of
-// 64 keys, 7.0 TB/s over the SMs (its softmax 0.7, the MMAs 0.5, both hidden
-// behind the loads), 2 after the last copy has landed, 1.3 for the pieces' rows,
-// and 6 for the merge and its launch.  DRAM reads are the keys' bytes.  Four long
-// requests (D = 128, 33 to 131 K keys, 672 MB): 115 us, 5.8 TB/s.  64 tokens x 4
-// heads are two row tiles, which read their keys twice, the second time from L2.
+// 64 keys, 7.0 TB/s over the SMs (softmax and MMAs, 0.5 us each, are hidden behind
+// the loads), 2 after the last copy has landed, 1.3 for the pieces' rows, and 6 for
+// the merge and its launch.  DRAM reads are the keys' bytes.  A sliding layer of
+// them (512 keys each, whole segments on 64 SMs): 19.3 us (21.0 with a thread
+// per row), latency.  Four long requests (D = 128, 33 to 131 K keys, 672 MB): 116
+// us, 5.8 TB/s.  64 tokens x 4 heads are two row tiles, which read their keys twice,
+// the second time from L2: 43.7 us, 1.37 a tile, 7.4 TB/s out of L2.
 //
 // Measured and dropped: one pass over S with a reference that moves only when the
 // weights' sum shows that it must (few instructions, which are cold in every launch:
