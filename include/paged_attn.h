@@ -574,7 +574,7 @@ int paged_tree_plan(const int32_t* parents, const int32_t* query_start_loc,
  * workspace must not overlap on the GPU.
  * tree_masks 8-byte aligned.  max_query_len > 64: PKA_ERR_UNSUPPORTED.
  * PKA_ERR_SHAPE if the segments times (visible blocks of a table row + 20) exceed
- * 2^30, or num_blocks * Hkv * 16 exceeds 2^31 - 1. */
+ * 2^30, max_blocks exceeds 2^26, or num_blocks * Hkv * 16 exceeds 2^31 - 1. */
 size_t paged_tree_attn_ws_bytes(int32_t Hq, int32_t Hkv, int32_t D, int32_t max_query_len);
 int paged_tree_attn_ws(const void* q, void* out, const pka_kv_pool* kv,
                        const int32_t* block_tables, int32_t max_blocks,
@@ -631,14 +631,15 @@ int paged_tree_accept(void* const* pools, int32_t num_pools, int32_t num_blocks,
  *            were;
  *   new_seq_lens int32 [B] (may be seq_lens) = n;
  *   pools    (host array of 2 * num_layers distinct bf16 pools: K and V of each
- *            layer; layers that share one evict once) hold the kept rows; rows from n on keep their contents, and their blocks
- *            can be given back (paged_kv_ref_blocks with the old lengths and -1,
- *            then with the new ones and +1).
+ *            layer; layers that share one evict once) hold the kept rows; rows from
+ *            n on keep their contents, and their blocks can be given back
+ *            (paged_kv_ref_blocks with the old lengths and -1, then with the new
+ *            ones and +1).
  * refcounts (NULL: not looked at) int32 [num_blocks]: a request of whose blocks
  * below n one has a count above 1 is left whole (n = L): it shares them with
  * another request, which would see its rows move (copy them first,
  * paged_kv_copy_blocks).  Without refcounts those blocks must be the request's own.
- * 1 <= budget, sinks + recent <= budget.  A length outside [0, max_blocks * 16]
+ * 1 <= budget, sinks + recent <= budget, max_blocks <= 2^26.  A length outside [0, max_blocks * 16]
  * is clamped, T < L taken as L (PKA_DEVERR_SEQ_LEN); a table id outside the pool
  * leaves its rows unmoved (PKA_DEVERR_BAD_TABLE).
  * key_mass, key_pos, new_mass and new_pos 16-byte aligned.

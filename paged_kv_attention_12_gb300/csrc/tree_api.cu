@@ -12,6 +12,9 @@
 namespace {
 
 constexpr int32_t kMaxTree = 64;  // drafted tokens of a request (bits of a mask)
+// Blocks of a table row, where keys are counted in tiles: 2^30 keys, so that no
+// tile's end passes 32 bits.
+constexpr int32_t kMaxRowBlocks = 1 << 26;
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 bool aligned16(const void* p) { return aligned(p, 16); }
@@ -125,7 +128,7 @@ int paged_tree_attn_ws(const void* q, void* out, const pka_kv_pool* kv,
   if (G != 1 && G != 2 && G != 4 && G != 8) return PKA_ERR_UNSUPPORTED;
   st = check_tree(B, total_q, max_query_len);
   if (st != PKA_OK) return st;
-  if (max_blocks <= 0 || max_blocks > 0x7fffffff / 16 || max_seq_len < 0 ||
+  if (max_blocks <= 0 || max_blocks > kMaxRowBlocks || max_seq_len < 0 ||
       max_seq_len > static_cast<int64_t>(max_blocks) * 16)
     return PKA_ERR_SHAPE;
   if (!std::isfinite(params->scale) || std::isnan(params->softcap)) return PKA_ERR_SHAPE;
@@ -144,7 +147,7 @@ int paged_tree_attn_ws(const void* q, void* out, const pka_kv_pool* kv,
   const int64_t segs = static_cast<int64_t>(B) * Hkv * ((max_query_len * G + tile_rows - 1) / tile_rows);
   int64_t per = max_blocks;
   if (params->window > 0) per = std::min<int64_t>(per, (static_cast<int64_t>(params->window) + kMaxTree) / 16 + 2);
-  if (segs * (per + pka::kTreePieceUnits(128)) > (int64_t(1) << 30)) return PKA_ERR_SHAPE;
+  if (segs > (int64_t(1) << 30) / (per + pka::kTreePieceUnits(128))) return PKA_ERR_SHAPE;
   const int sms = pka::device_sm_count();
   if (sms <= 0) return PKA_ERR_CUDA;
   int64_t longest = max_seq_len / 16 + (max_seq_len % 16 != 0);
@@ -252,7 +255,7 @@ int paged_kv_evict(void* const* pools, int32_t num_layers, int32_t num_blocks,
                    void* workspace, size_t workspace_bytes, int32_t* err, void* stream) {
   int st = check_sizes(num_blocks, num_kv_heads, block_size, head_dim);
   if (st != PKA_OK) return st;
-  if (num_layers <= 0 || B < 0 || max_blocks <= 0 || max_blocks > 0x7fffffff / 16)
+  if (num_layers <= 0 || B < 0 || max_blocks <= 0 || max_blocks > kMaxRowBlocks)
     return PKA_ERR_SHAPE;
   if (budget <= 0 || sinks < 0 || recent < 0 ||
       static_cast<int64_t>(sinks) + recent > budget)

@@ -66,7 +66,12 @@ def attn(L, pool=None, scale=0.1, softcap=0.0, window=0, **kw):
     (dict(first=None), "PKA_ERR_NULL"), (dict(lens=None), "PKA_ERR_NULL"),
     (dict(tables=None), "PKA_ERR_NULL"), (dict(ws=None), "PKA_ERR_NULL"), (dict(ws=72), "PKA_ERR_ALIGN"),
     (dict(ws_bytes=1000), "PKA_ERR_WORKSPACE"), (dict(kv=None), "PKA_ERR_NULL"),
-    (dict(par=None), "PKA_ERR_NULL"), (dict(B=2 ** 20, max_blocks=2 ** 12), "PKA_ERR_SHAPE")])
+    (dict(par=None), "PKA_ERR_NULL"), (dict(B=2 ** 20, max_blocks=2 ** 12), "PKA_ERR_SHAPE"),
+    # 2^30 requests x 2^26 heads x 4 tiles x (44 + 20): 2^64
+    (dict(pool=dict(num_blocks=1, hkv=2 ** 26), hq=2 ** 29, B=2 ** 30, most=64, max_blocks=44),
+     "PKA_ERR_SHAPE"),
+    (dict(B=1, pool=dict(hkv=1), hq=1, max_blocks=2 ** 26 + 1), "PKA_ERR_SHAPE"),
+    (dict(B=1, window=5, max_blocks=2 ** 26 + 1), "PKA_ERR_SHAPE")])
 def test_attention_refusals(L, kw, want):
     assert attn(L, **kw) == want
 
@@ -114,8 +119,8 @@ def evict(L, num_layers=1, pool=64, **kw):
     (dict(recent=-1), "PKA_ERR_SHAPE"), (dict(sinks=5, recent=6), "PKA_ERR_SHAPE"),
     (dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1), "PKA_ERR_SHAPE"), (dict(layers=0), "PKA_ERR_SHAPE"),
     (dict(B=-1), "PKA_ERR_SHAPE"), (dict(B=2 ** 27), "PKA_ERR_SHAPE"), (dict(max_blocks=0), "PKA_ERR_SHAPE"),
-    (dict(max_blocks=2 ** 27), "PKA_ERR_SHAPE"), (dict(bs=8), "PKA_ERR_UNSUPPORTED"),
-    (dict(d=512), "PKA_ERR_UNSUPPORTED"), (dict(num_blocks=0), "PKA_ERR_SHAPE"),
+    (dict(max_blocks=2 ** 27), "PKA_ERR_SHAPE"), (dict(max_blocks=2 ** 26 + 1), "PKA_ERR_SHAPE"),
+    (dict(bs=8), "PKA_ERR_UNSUPPORTED"), (dict(d=512), "PKA_ERR_UNSUPPORTED"), (dict(num_blocks=0), "PKA_ERR_SHAPE"),
     (dict(pools=None), "PKA_ERR_NULL"), (dict(pool=None), "PKA_ERR_NULL"), (dict(pool=72), "PKA_ERR_ALIGN"),
     (dict(ws=66), "PKA_ERR_ALIGN"), (dict(ws_bytes=100), "PKA_ERR_WORKSPACE")] + [
     ({key: None}, "PKA_ERR_NULL") for key in ("tables", "lens", "mass", "new_mass", "pos", "new_pos",
