@@ -171,9 +171,10 @@ struct TreeAcceptArgs {
   int32_t* path;                   // [B][max_query_len]
   int32_t* accepted;               // [B]
   int32_t* next_tokens;            // [B]
-  int32_t* new_seq_lens;           // [B], may be seq_lens; all four null: rows only
+  int32_t* new_seq_lens;           // [B], may be seq_lens
   int32_t* err;
   int32_t num_pools, batch, total_q, max_query_len, num_blocks, Hkv, head_dim;
+  int32_t write_walk;              // 0: move rows only
 };
 
 cudaError_t launch_tree_accept(const TreeAcceptArgs& a, cudaStream_t stream);

@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(128) tree_accept_kernel(const __grid_constant_
   const int item = blockIdx.y * (blockDim.x / 32) + threadIdx.x / 32;  // pool * Hkv + head
   const int items = max(1, a.num_pools * a.Hkv);
   if (item >= items) return;
-  const bool writer = item == 0 && a.path != nullptr;
+  const bool writer = item == 0 && a.write_walk != 0;
   int q0;
   const int n = tree_span(a.query_start_loc, b, a.total_q, a.max_query_len, &q0);
   if (n < 0 && item == 0 && lane == 0) report(a.err, PKA_DEVERR_QUERY_LOC);

@@ -83,8 +83,9 @@ int paged_tree_plan(const int32_t* parents, const int32_t* query_start_loc,
       num_blocks > 0x7fffffff / 16)
     return PKA_ERR_SHAPE;
   if (total_q == 0) return PKA_OK;
-  if (parents == nullptr || query_start_loc == nullptr || seq_lens == nullptr ||
-      block_tables == nullptr)
+  // (without requests every row is padding)
+  if (parents == nullptr || query_start_loc == nullptr ||
+      (B > 0 && (seq_lens == nullptr || block_tables == nullptr)))
     return PKA_ERR_NULL;
   if (!aligned(tree_masks, 8)) return PKA_ERR_ALIGN;
   pka::TreePlanArgs a{};
@@ -201,9 +202,12 @@ int paged_tree_accept(void* const* pools, int32_t num_pools, int32_t num_blocks,
   if (st == PKA_OK) st = check_tree(B, total_q, max_query_len);
   if (st != PKA_OK) return st;
   if (B == 0) return PKA_OK;
-  if (parents == nullptr || tokens == nullptr || targets == nullptr ||
-      (slots == nullptr && num_pools > 0) || query_start_loc == nullptr || seq_lens == nullptr ||
-      path == nullptr || accepted == nullptr || next_tokens == nullptr || new_seq_lens == nullptr)
+  // (without rows every tree is empty)
+  if (total_q > 0 && (parents == nullptr || tokens == nullptr || targets == nullptr ||
+                      (slots == nullptr && num_pools > 0)))
+    return PKA_ERR_NULL;
+  if (query_start_loc == nullptr || seq_lens == nullptr || (path == nullptr && max_query_len > 0) ||
+      accepted == nullptr || next_tokens == nullptr || new_seq_lens == nullptr)
     return PKA_ERR_NULL;
   st = check_pools(pools, num_pools);
   if (st != PKA_OK) return st;
@@ -216,6 +220,7 @@ int paged_tree_accept(void* const* pools, int32_t num_pools, int32_t num_blocks,
   a.query_start_loc = query_start_loc;
   a.seq_lens = seq_lens;
   a.path = path;
+  a.write_walk = 1;
   a.accepted = accepted;
   a.next_tokens = next_tokens;
   a.new_seq_lens = new_seq_lens;
@@ -233,7 +238,7 @@ int paged_tree_accept(void* const* pools, int32_t num_pools, int32_t num_blocks,
     for (int32_t i = 0; i < a.num_pools; ++i) a.pools[i] = pools[done + i];
     if (pka::launch_tree_accept(a, static_cast<cudaStream_t>(stream)) != cudaSuccess)
       return PKA_ERR_CUDA;
-    a.path = nullptr;
+    a.write_walk = 0;
     done += a.num_pools;
   } while (done < num_pools);
   return PKA_OK;

@@ -514,3 +514,22 @@ def test_accept_reports():
     assert count.tolist()[:2] == [2, 0] and nxt.tolist()[:2] == [7, -1]
     assert lens.tolist()[:2] == [28, 20]
     assert torch.equal(pool, was)
+
+
+def test_batches_without_rows_and_rows_without_requests():
+    """A step in which no request brings a token; a batch that is all padding."""
+    none, first, lens, table = i32([]), i32([0, 0, 0]), i32([20, 0]), i32([[0, 1], [-1, -1]])
+    pool = [torch.randn((4, 2, 16, 128), device=DEV).to(torch.bfloat16) for _ in range(2)]
+    kept = [p.clone() for p in pool]
+    binding.paged_tree_plan(none, first, lens, table, 4, 8, none.long(), none, none)
+    for pools, slots, width in ((pool, none, 3), ([], None, 0), (pool, none, 0)):
+        path, got, err = i32(np.full((2, width), 7)), [i32([9, 9]) for _ in range(3)], i32([0])
+        binding.paged_tree_accept(pools, none, none, none, slots, first, lens, path, *got, err)
+        torch.cuda.synchronize()
+        assert [x.tolist() for x in got] == [[0, 0], [-1, -1], [20, 0]] and err.item() == 0
+        assert path.tolist() == [[-1] * width] * 2
+    assert all(torch.equal(p, k) for p, k in zip(pool, kept))
+    masks, pos, slots = torch.ones(5, dtype=torch.int64, device=DEV), i32([3] * 5), i32([3] * 5)
+    binding.paged_tree_plan(i32([-1] * 5), i32([0]), none, none.view(0, 4), 4, 8, masks, pos, slots)
+    torch.cuda.synchronize()
+    assert (masks.tolist(), pos.tolist(), slots.tolist()) == ([0] * 5, [0] * 5, [-1] * 5)
