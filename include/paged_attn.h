@@ -600,7 +600,7 @@ int paged_tree_attn_ws(const void* q, void* out, const pka_kv_pool* kv,
  * request's rows of `slots` (paged_tree_plan); pairs with a negative slot are
  * left out, a slot past the pool ORs PKA_DEVERR_BAD_TABLE into *err.  The slots
  * of all trees must be distinct, and so must the pools (layers that share one
- * name it once).  num_pools = 0: the walk alone (slots and the
+ * name it once; PKA_ERR_SHAPE if two share memory).  num_pools = 0: the walk alone (slots and the
  * pools' sizes are not looked at).  A bad span leaves a request as if n = 0
  * (PKA_DEVERR_QUERY_LOC).  num_kv_heads at most 1024. */
 int paged_tree_accept(void* const* pools, int32_t num_pools, int32_t num_blocks,
@@ -631,10 +631,10 @@ int paged_tree_accept(void* const* pools, int32_t num_pools, int32_t num_blocks,
  *            were;
  *   new_seq_lens int32 [B] (may be seq_lens) = n;
  *   pools    (host array of 2 * num_layers distinct bf16 pools: K and V of each
- *            layer; layers that share one evict once) hold the kept rows; rows from
- *            n on keep their contents, and their blocks can be given back
- *            (paged_kv_ref_blocks with the old lengths and -1, then with the new
- *            ones and +1).
+ *            layer; layers that share one evict once; PKA_ERR_SHAPE if two pools
+ *            share memory) hold the kept rows; rows from n on keep their contents,
+ *            and their blocks can be given back (paged_kv_ref_blocks with the old
+ *            lengths and -1, then with the new ones and +1).
  * refcounts (NULL: not looked at) int32 [num_blocks]: a request of whose blocks
  * below n one has a count above 1 is left whole (n = L): it shares them with
  * another request, which would see its rows move (copy them first,

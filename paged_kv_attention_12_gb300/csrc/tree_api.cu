@@ -28,6 +28,10 @@ int check_sizes(int32_t num_blocks, int32_t num_kv_heads, int32_t block_size, in
   return PKA_OK;
 }
 
+uint64_t pool_bytes(int32_t num_blocks, int32_t num_kv_heads, int32_t head_dim) {
+  return static_cast<uint64_t>(num_blocks) * num_kv_heads * 16 * head_dim * 2;
+}
+
 int check_tree(int32_t B, int32_t total_q, int32_t max_query_len) {
   if (B < 0 || B == 0x7fffffff || total_q < 0 || max_query_len < 0) return PKA_ERR_SHAPE;
   return max_query_len > kMaxTree ? PKA_ERR_UNSUPPORTED : PKA_OK;
@@ -40,6 +44,26 @@ int check_pools(void* const* pools, int32_t n) {
     if (!aligned16(pools[i])) return PKA_ERR_ALIGN;
   }
   return PKA_OK;
+}
+
+// Whether two of n pools of so many bytes share memory: rows would move twice.
+// Up to 256 pools are sorted by address first (each with each are 8128 comparisons
+// for 64 layers).
+bool pools_overlap(void* const* pools, int32_t n, uint64_t bytes) {
+  auto at = [&](int32_t i) { return reinterpret_cast<uintptr_t>(pools[i]); };
+  constexpr int32_t kSorted = 256;
+  if (n > kSorted) {
+    for (int32_t i = 1; i < n; ++i)
+      for (int32_t j = 0; j < i; ++j)
+        if ((at(i) > at(j) ? at(i) - at(j) : at(j) - at(i)) < bytes) return true;
+    return false;
+  }
+  uintptr_t sorted[kSorted];
+  for (int32_t i = 0; i < n; ++i) sorted[i] = at(i);
+  std::sort(sorted, sorted + n);
+  for (int32_t i = 1; i < n; ++i)
+    if (sorted[i] - sorted[i - 1] < bytes) return true;
+  return false;
 }
 
 // Workspace of the tree attention: two partial tiles for each chunk of the
@@ -212,6 +236,8 @@ int paged_tree_accept(void* const* pools, int32_t num_pools, int32_t num_blocks,
   st = check_pools(pools, num_pools);
   if (st != PKA_OK) return st;
   if (num_kv_heads > 1024) return PKA_ERR_SHAPE;  // (255 pools a launch, 4 warps a CTA)
+  if (pools_overlap(pools, num_pools, pool_bytes(num_blocks, num_kv_heads, head_dim)))
+    return PKA_ERR_SHAPE;
   pka::TreeAcceptArgs a{};
   a.parents = parents;
   a.tokens = tokens;
@@ -281,6 +307,8 @@ int paged_kv_evict(void* const* pools, int32_t num_layers, int32_t num_blocks,
   const EvictLayout lay = evict_layout(num_layers, B, num_kv_heads, max_blocks, budget);
   if (workspace_bytes < static_cast<size_t>(lay.words() + B) * sizeof(int32_t))
     return PKA_ERR_WORKSPACE;
+  if (pools_overlap(pools, 2 * num_layers, pool_bytes(num_blocks, num_kv_heads, head_dim)))
+    return PKA_ERR_SHAPE;
   const int sms = pka::device_sm_count();
   if (sms <= 0) return PKA_ERR_CUDA;
   pka::EvictMoveArgs m{};

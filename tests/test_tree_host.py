@@ -104,6 +104,23 @@ def test_accept_refusals(L, kw, want):
     assert accept(L, **kw) == want
 
 
+@pytest.mark.parametrize("n", [2, 40, 256, 257, 600])
+def test_pools_that_share_memory_are_refused(L, n):
+    """Rows of a pool named twice would move twice; the last of 8 x 2 x 16 x 256
+    bytes may touch the next pool's first byte only."""
+    size = 8 * 2 * 16 * 256
+    order = [(7 * i) % n if math.gcd(7, n) == 1 else i for i in range(n)]
+    for at, by in ((0, size), (n // 2, 16), (n - 1, size)):
+        ptrs = [64 + i * size for i in order]
+        ptrs[at] = ptrs[at - 1] + (size - by)        # the same pool, or its last row
+        again = (ctypes.c_void_p * n)(*ptrs)
+        assert accept(L, n, pools=again) == "PKA_ERR_SHAPE"
+        if n % 2 == 0:
+            assert evict(L, n // 2, pools=again) == "PKA_ERR_SHAPE"
+    apart = (ctypes.c_void_p * n)(*[64 + i * size for i in order])
+    assert accept(L, n, pools=apart, B=0) == "PKA_OK"
+
+
 def evict(L, num_layers=1, pool=64, **kw):
     ptrs = (ctypes.c_void_p * 2)(pool, pool)
     a = dict(pools=ptrs, layers=num_layers, num_blocks=8, hkv=2, bs=16, d=128, tables=64,
