@@ -566,9 +566,10 @@ int paged_tree_plan(const int32_t* parents, const int32_t* query_start_loc,
  * unevicted.
  * One launch, or two: the segments (request, KV head, tile of 128 / G or 64 / G
  * query tokens) are streamed in equal chunks of their keys, one per SM, and what
- * a chunk cuts is merged in key order by the second launch (the same bits every
- * time).  Where max_seq_len and the number of segments allow no cut there is no
- * second launch.  max_seq_len is a promise; longer rows are computed all the same.
+ * a chunk cuts is merged in key order by the second launch.  Where max_seq_len
+ * and the number of segments let none be cut there is no second launch; few of
+ * them are shared by two CTAs each.  The same call gives the same bits every
+ * time.  max_seq_len is a promise; longer rows are computed all the same.
  * workspace: 16-byte aligned, at least paged_tree_attn_ws_bytes() bytes (which
  * depend on no length and no batch), needs no initialisation.  Calls sharing one
  * workspace must not overlap on the GPU.

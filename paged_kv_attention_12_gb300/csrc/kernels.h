@@ -124,6 +124,8 @@ struct TreeArgs {
   int32_t whole_slack;             // segments stay whole when none has more units than a
                                    // chunk and this many
   int32_t may_cut;                 // 0: every segment stays whole (there are no more than CTAs)
+  int32_t pair;                    // > 0: (may_cut 0) two CTAs of a cluster share a segment's
+                                   // keys, this many clusters
   float scale, softcap;
   int32_t window;
 };

@@ -200,11 +200,23 @@ int paged_tree_attn_ws(const void* q, void* out, const pka_kv_pool* kv,
   a.total_q = total_q;
   a.max_query_len = max_query_len;
   a.min_chunk = pka::kTreePieceUnits(kv->head_dim) + 8;
-  // A merge costs about 6 us, as much as streaming 28 blocks at D = 256 (a
-  // sliding layer of 64 segments of 34 blocks: cut 23.1 us, whole 20.9).
+  // A merge costs about 6 us, as much as streaming 28 blocks at D = 256.
   a.whole_slack = kv->head_dim == 256 ? 28 : 56;
-  a.may_cut = segs > std::min(sms, pka::kTreeMaxCtas) ||
-              longest + pka::kTreePieceUnits(kv->head_dim) > a.min_chunk + a.whole_slack;
+  const int64_t ctas = std::min(sms, pka::kTreeMaxCtas);
+  // Where there are two CTAs for each segment, pairs of them share a segment of
+  // more than two tiles and need no merge, up to the length where cutting would
+  // gain a merge's worth, the mean length taken as half of the longest.  64
+  // segments of 200, 560, 1500 keys, D = 256: pairs 13.1, 16.4, 26.2 us; whole
+  // 13.8, 18.8; cut 21.0, 23.9, 31.7.  4 segments of 200, 560, 1000, 1500: pairs
+  // 10.8, 13.5, 17.7, 22.9; whole 11.4, 17.3; cut 17.5, 17.4, 18.5, 18.1.  Two tiles
+  // (100 keys): pairs 9.3, whole 8.9.  D = 128, 64 segments of 300, 1000, 1500: pairs
+  // 10.9, 14.9, 17.4; whole 10.9, 16.7; cut 18.0, 22.6, 24.5.
+  const bool pairs = 2 * segs <= ctas && longest > (kv->head_dim == 256 ? 8 : 16) &&
+                     longest * (ctas - segs) <= 2 * ctas * a.whole_slack;
+  a.pair = pairs ? static_cast<int32_t>(segs) : 0;
+  // (100 segments of 34 blocks, D = 256: cut 23.1 us, whole 20.9)
+  a.may_cut = !pairs && (segs > ctas || longest + pka::kTreePieceUnits(kv->head_dim) >
+                                            a.min_chunk + a.whole_slack);
   a.scale = params->scale;
   a.softcap = params->softcap > 1e38f ? 0.f : params->softcap;
   a.window = params->window;

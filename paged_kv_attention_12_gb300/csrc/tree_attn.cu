@@ -17,12 +17,15 @@
 // chunk writes its output; the pieces of a cut one leave softmax-normalised
 // fp32 rows and their log-sum-exp in the workspace, which the second launch
 // merges in key order.  Segments that are no longer than a chunk and what a merge
-// costs stay whole, one per CTA.
+// costs stay whole, one per CTA, or, where there are two CTAs for each segment,
+// half of the tiles for each CTA of a cluster of two: each sends the other half of
+// its rows' columns into the other's shared memory and finishes the rest, which
+// takes 1.2 us instead of the merge's 8.
 //
 // Warps of a CTA: four softmax warps (a row of S and O lies in a TMEM lane; a thread
 // owns a row, or with QR = 64 half of its columns), one TMA warp each for K, V and
-// Q, and one that issues the MMAs.  The rings of K and V run on over the pieces of a chunk, so that
-// the loads do not stop for an epilogue.
+// Q, and one that issues the MMAs.  The rings of K and V run on over the pieces of a
+// chunk, so that the loads do not stop for an epilogue.
 //
 // Where the time goes (a serving layer: 32 trees of 8 to 16 tokens over 512 to
 // 4096 keys, 2 KV heads, D = 256; 154 MB, 38.8 us; global-timer stamps): 0.6 us to
@@ -30,8 +33,8 @@
 // 64 keys, 7.0 TB/s over the SMs (softmax and MMAs, 0.5 us each, are hidden behind
 // the loads), 2 after the last copy has landed, 1.3 for the pieces' rows, and 6 for
 // the merge and its launch.  DRAM reads are the keys' bytes.  A sliding layer of
-// them (512 keys each, whole segments on 64 SMs): 19.3 us (21.0 with a thread
-// per row), latency.  Four long requests (D = 128, 33 to 131 K keys, 672 MB): 116
+// them (512 keys each, 64 segments on 64 pairs): 17.7 us (19.3 with a CTA each),
+// latency.  Four long requests (D = 128, 33 to 131 K keys, 672 MB): 116
 // us, 5.8 TB/s.  64 tokens x 4 heads are two row tiles, which read their keys twice,
 // the second time from L2: 43.7 us, 1.37 a tile, 7.4 TB/s out of L2.
 //
@@ -329,6 +332,28 @@ __device__ __noinline__ void add_wild(const TreeArgs& a, const Piece& p, const S
   }
 }
 
+// Pairs of CTAs (a cluster of two).
+__device__ __forceinline__ void pair_sync() {
+  __syncwarp();
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+          : "memory");
+}
+// The address of this CTA's shared variable in the CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t shared_of(const void* p, int rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void store_far(uint32_t to, float x) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(x) : "memory");
+}
+__device__ __forceinline__ void store_far(uint32_t to, float4 x) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(x.x), "f"(x.y),
+               "f"(x.z), "f"(x.w)
+               : "memory");
+}
+
 template <int D, int QR>
 __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
     tree_attn_kernel(const __grid_constant__ TreeLaunch t) {
@@ -411,15 +436,24 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
   __syncthreads();
   const bool whole = !a.may_cut || (segs <= grid && longest <= chunk + a.whole_slack);
   // (where may_cut is false there are no more segments than CTAs)
-  const long long begin = static_cast<long long>(blockIdx.x) * (whole ? 1 : chunk);
+  const int rank = a.pair ? blockIdx.x & 1 : 0;  // of the CTAs that share a segment
+  const long long begin =
+      static_cast<long long>(a.pair ? blockIdx.x / 2 : blockIdx.x) * (whole ? 1 : chunk);
   const bool any_work = begin < (whole ? segs : units);
   if (any_work) {
     const int want = static_cast<int>(begin);
     auto look = [&](int b, const Request& r, const Load& x, int at_unit, int at_seg) {
       const int at = whole ? at_seg : at_unit;
-      if (want >= at && want < at + (whole ? x.segs : x.units))
+      if (want >= at && want < at + (whole ? x.segs : x.units)) {
         start = Walk{b, (want - at) * (whole ? x.len : 1),
                      whole ? x.len : min(chunk, units - want), r};
+        if (a.pair) {  // half of the tiles each, the odd one to the first
+          const int blocks = x.len - S::kPieceUnits;
+          const int half = min(((blocks + BPT - 1) / BPT + 1) / 2 * BPT, blocks);
+          if (rank == 1) start.off += S::kPieceUnits + half;
+          start.rem = rank == 1 ? blocks - half : S::kPieceUnits + half;
+        }
+      }
     };
     look(tid, mine_r, mine, before.units, before.segs);
     if (a.batch > NT) {
@@ -459,9 +493,10 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
     int g = 0;                                  // tiles issued
     // V's first loads wait for K's first tile: what the CTAs ask for at once lands
     // in about 4 us, and S comes first (D = 256: serving layer 40.4 -> 39.5 us, a
-    // sliding one 21.1 -> 20.7).  D = 128 gains nothing (four long requests 115.0 us
-    // without, 115.2 with it) and a small call loses (8.3 -> 8.9).
-    const bool late = D == 256 && !is_k && walk.rem > S::kPieceUnits + 4 * BPT;
+    // sliding one 21.1 -> 20.7, 64 pairs over 300 keys 14.0 -> 13.5).  D = 128 gains
+    // nothing (four long requests 115.0 us without, 115.2 with it) and a small call
+    // loses (8.3 -> 8.9).
+    const bool late = D == 256 && !is_k && (a.pair || walk.rem > S::kPieceUnits + 4 * BPT);
     bool ok = true;
     while (ok && walk.next<S>(t, &p)) {
       const int32_t* trow = a.tables + static_cast<size_t>(p.b) * a.max_blocks + p.j0;
@@ -616,7 +651,7 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
     const float k3 = -cap_in * cap_in * k1 * (1.f / 3.f);
     const float k5 = 2.f * cap_in * cap_in * cap_in * cap_in * k1 * (1.f / 15.f);
     const bool fold_ok = capped && cap_in > 0.f && k5 > 0.f && k5 <= kFltMax;
-    int g = 0, piece = 0;
+    int g = 0, piece = 0, met = 0;
     bool ok = true;
     int4 cut = make_int4(0, 0, 0, 0);  // this chunk's segment that goes on in the next one
     while (ok && walk.next<S>(t, &p)) {
@@ -864,6 +899,84 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
         uint16_t* orow =
             a.out + (static_cast<size_t>(p.q0 + tok) * a.Hq + (p.kvh << t.log2_g) +
                      (row & ((1 << t.log2_g) - 1))) * D;
+        if (a.pair && !direct) {
+          // The other CTA holds the segment's other keys: each gives the other half
+          // of a thread's columns, into the place of its queries, and finishes the rest.
+          constexpr int kKeep = D / SPLIT / 64;  // groups of 32 columns
+          const int give = (half * 2 + (rank ^ 1)) * kKeep, keep = (half * 2 + rank) * kKeep;
+          const uint32_t rows_there = shared_of(sQ, rank ^ 1) + (half * kKeep * 8 * QR + r) * 16;
+          const float4* rows_here =
+              reinterpret_cast<const float4*>(sQ) + half * kKeep * 8 * QR + r;
+          float* lse_here = &pair_value[0][0][0] + r;
+          const float lse = l == 0.f ? -INFINITY : m_ref + log2f(l);
+          pair_sync();  // the other CTA has done with its queries
+          ++met;
+#pragma unroll 1
+          for (int c = 0; c < kKeep; ++c) {
+            float o[32];
+            tmem_ld32(lane_base + S::kTmemO + (give + c) * 32, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              store_far(rows_there + (c * 8 + e) * QR * 16,
+                        make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv,
+                                    o[4 * e + 3] * inv));
+          }
+          if (half == 0) store_far(shared_of(lse_here, rank ^ 1), lse);
+          const volatile int* wild_here = wild_piece;
+          if (wild_here[piece & 1] == piece)
+            store_far(shared_of(&wild_piece[(piece & 1) ^ 1], rank ^ 1), __int_as_float(piece));
+          pair_sync();
+          ++met;
+          const float far_lse = *lse_here;
+          const float top = fmaxf(lse, far_lse);
+          const float w = lse == -INFINITY ? 0.f : fast_exp2(lse - top);
+          const float far_w = far_lse == -INFINITY ? 0.f : fast_exp2(far_lse - top);
+          // (no weight at all: NaN if one of them sees keys, else 0)
+          const float den = w + far_w;
+          const bool none = den == 0.f;
+          const bool dead = none && (!(inv == 0.f) || !(rows_here[0].x == 0.f));
+          const float f = none              ? (dead ? __int_as_float(0x7fffffff) : 0.f)
+                          : lse == -INFINITY ? 0.f
+                                             : w * inv / den;
+          const float far_f = none ? 0.f : far_w / den;
+#pragma unroll 1
+          for (int c = 0; c < kKeep; ++c) {
+            float o[32];
+            tmem_ld32(lane_base + S::kTmemO + (keep + c) * 32, o);
+            if (lse == -INFINITY) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float4 y = rows_here[(c * 8 + e) * QR];
+              if (far_lse == -INFINITY) y = make_float4(0.f, 0.f, 0.f, 0.f);
+              o[4 * e] = fmaf(f, o[4 * e], far_f * y.x);
+              o[4 * e + 1] = fmaf(f, o[4 * e + 1], far_f * y.y);
+              o[4 * e + 2] = fmaf(f, o[4 * e + 2], far_f * y.z);
+              o[4 * e + 3] = fmaf(f, o[4 * e + 3], far_f * y.w);
+            }
+            if (row_valid) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<uint4*>(orow + (keep + c) * 32 + q * 8) =
+                    make_uint4(pack_bf16x2(o[q * 8 + 0], o[q * 8 + 1]),
+                               pack_bf16x2(o[q * 8 + 2], o[q * 8 + 3]),
+                               pack_bf16x2(o[q * 8 + 4], o[q * 8 + 5]),
+                               pack_bf16x2(o[q * 8 + 6], o[q * 8 + 7]));
+            }
+          }
+          if (row_valid && (wild_here[0] == piece || wild_here[1] == piece)) {
+            auto add = [&](int lo, int hi) {
+              add_wild<kKeep * 32, false>(a, p, see, lo, hi, keep * 32, D, nullptr, 0, orow);
+            };
+            const int lo = first_block(a, Request{p.n, p.q0, p.L}) * kBlockSize;
+            const int mid = max(lo, edge_lo);
+            add(lo, mid);
+            add(max(mid, edge_hi), p.L);
+          }
+          break;  // (a pair's CTAs take one piece)
+        }
 #pragma unroll 1
         for (int c = half * (D / 64 / SPLIT); c < (half + 1) * (D / 64 / SPLIT); ++c) {
           float o[64];
@@ -904,10 +1017,18 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
         }
       }
     }
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && a.may_cut) {
       if (!any_work || !ok) cut.w = 0;
       a.cuts[blockIdx.x] = cut;
     }
+    if (a.pair)
+      for (; met < 2; ++met) pair_sync();
+  }
+  // Every warp meets the other CTA twice: after the second time neither writes
+  // into the other's memory.
+  if (a.pair && (warp == S::kWarpK || warp == S::kWarpV || warp == S::kWarpMma || warp == S::kWarpQ)) {
+    pair_sync();
+    pair_sync();
   }
 
   tc_fence_before();
@@ -1080,6 +1201,8 @@ cudaError_t launch_tree_t(const TreeArgs& a, int sm_count, cudaStream_t stream) 
   cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), S::kSmemBytes);
   if (e != cudaSuccess) return e;
   const int grid = sm_count < kTreeMaxCtas ? sm_count : kTreeMaxCtas;
+  if (a.pair)
+    return launch_overlapped(kern, dim3(2 * a.pair), S::kThreads, S::kSmemBytes, stream, t, 2);
   e = launch_overlapped(kern, dim3(grid), S::kThreads, S::kSmemBytes, stream, t);
   if (e != cudaSuccess || !a.may_cut) return e;
   TreeMergeArgs m{};

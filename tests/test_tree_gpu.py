@@ -237,6 +237,50 @@ def test_many_requests(B):
     check(c, run(c))
 
 
+@pytest.mark.parametrize("D,hq,hkv,most", [(128, 8, 2, 16), (256, 8, 2, 16), (128, 8, 2, 40),
+                                           (256, 8, 1, 64), (128, 2, 2, 64), (256, 4, 4, 5)])
+@pytest.mark.parametrize("window", [0, 200])
+def test_segments_shared_by_two(D, hq, hkv, most, window):
+    """Few segments of a few hundred keys: two CTAs take half of the tiles each.
+    Rows of one tile (which the first takes alone), of two, odd and even numbers of
+    tiles, short last ones, and none."""
+    lens = [1, 64, 65, 128, 129, 200, 256, 300, 385, 511, 576, 0]
+    ns = [min(L, 1 + (7 * i) % most) for i, L in enumerate(lens)]
+    c = make(lens, ns, D=D, hq=hq, hkv=hkv, window=window, softcap=30.0 if hkv == 2 else 0.0,
+             seed=D + most)
+    out = run(c)
+    check(c, out)
+    assert torch.equal(run(c), out)
+
+
+@pytest.mark.parametrize("D", [128, 256])
+def test_halves_without_weight_and_with_infinities(D):
+    """Keys whose logits are -infinity fill one half of a segment, or both, for one
+    head; V's infinities and NaN lie in either half."""
+    c = make([512, 512, 512, 300], [9, 9, 16, 9], D=D, seed=1)
+    c["q"][:] = c["q"].abs() + 0.1
+    for b, (lo, hi) in enumerate(((0, 256), (256, 512), (0, 512))):
+        for t in range(lo, hi):
+            c["k"][c["table"][b, t // 16], 1, t % 16, 0] = -math.inf
+    n0 = 512 - 9
+    for b, t, x in ((0, n0 + 3, math.inf), (1, n0 + 8, NAN), (3, 300 - 4, -math.inf)):
+        c["v"][c["table"][b, t // 16], 0, t % 16, 5] = x
+    rows = c["first"][-1]
+    out = f64(run(c))[:rows]
+    with np.errstate(invalid="ignore"):
+        ref = expected(c)[0][:rows]
+    args = dict(c, v=torch.where(torch.isfinite(c["v"]), c["v"], torch.zeros_like(c["v"])))
+    with np.errstate(invalid="ignore"):
+        fine, spread = (x[:rows] for x in expected(args))
+    assert np.array_equal(np.isnan(out), np.isnan(ref))
+    assert np.array_equal(np.isinf(out), np.isinf(ref))
+    assert np.array_equal(np.sign(out[np.isinf(ref)]), np.sign(ref[np.isinf(ref)]))
+    keep = np.isfinite(ref)
+    # (the -infinities of K add nothing to the logits that have weight)
+    args["k"] = torch.where(torch.isfinite(c["k"]), c["k"], torch.zeros_like(c["k"]))
+    assert np.all(np.abs(out - fine)[keep] <= bound(args, fine, spread)[keep])
+
+
 def test_lengths_past_the_promise():
     c = make([700, 90, 333], [6, 9, 12])
     for max_len in (0, 16, 100, 700):
