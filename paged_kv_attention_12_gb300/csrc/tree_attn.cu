@@ -354,7 +354,7 @@ __device__ __forceinline__ void store_far(uint32_t to, float4 x) {
                : "memory");
 }
 
-template <int D, int QR>
+template <int D, int QR, bool PAIR>
 __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
     tree_attn_kernel(const __grid_constant__ TreeLaunch t) {
   using S = TreeShape<D, QR>;
@@ -434,11 +434,11 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
   len = __reduce_max_sync(0xffffffffu, len);
   if (lane == 0) atomicMax(&longest, len);
   __syncthreads();
-  const bool whole = !a.may_cut || (segs <= grid && longest <= chunk + a.whole_slack);
+  const bool whole = PAIR || !a.may_cut || (segs <= grid && longest <= chunk + a.whole_slack);
   // (where may_cut is false there are no more segments than CTAs)
-  const int rank = a.pair ? blockIdx.x & 1 : 0;  // of the CTAs that share a segment
+  const int rank = PAIR ? blockIdx.x & 1 : 0;  // of the CTAs that share a segment
   const long long begin =
-      static_cast<long long>(a.pair ? blockIdx.x / 2 : blockIdx.x) * (whole ? 1 : chunk);
+      static_cast<long long>(PAIR ? blockIdx.x / 2 : blockIdx.x) * (whole ? 1 : chunk);
   const bool any_work = begin < (whole ? segs : units);
   if (any_work) {
     const int want = static_cast<int>(begin);
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
       if (want >= at && want < at + (whole ? x.segs : x.units)) {
         start = Walk{b, (want - at) * (whole ? x.len : 1),
                      whole ? x.len : min(chunk, units - want), r};
-        if (a.pair) {  // half of the tiles each, the odd one to the first
+        if (PAIR) {  // half of the tiles each, the odd one to the first
           const int blocks = x.len - S::kPieceUnits;
           const int half = min(((blocks + BPT - 1) / BPT + 1) / 2 * BPT, blocks);
           if (rank == 1) start.off += S::kPieceUnits + half;
@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
     // sliding one 21.1 -> 20.7, 64 pairs over 300 keys 14.0 -> 13.5).  D = 128 gains
     // nothing (four long requests 115.0 us without, 115.2 with it) and a small call
     // loses (8.3 -> 8.9).
-    const bool late = D == 256 && !is_k && (a.pair || walk.rem > S::kPieceUnits + 4 * BPT);
+    const bool late = D == 256 && !is_k && (PAIR || walk.rem > S::kPieceUnits + 4 * BPT);
     bool ok = true;
     while (ok && walk.next<S>(t, &p)) {
       const int32_t* trow = a.tables + static_cast<size_t>(p.b) * a.max_blocks + p.j0;
@@ -899,7 +899,7 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
         uint16_t* orow =
             a.out + (static_cast<size_t>(p.q0 + tok) * a.Hq + (p.kvh << t.log2_g) +
                      (row & ((1 << t.log2_g) - 1))) * D;
-        if (a.pair && !direct) {
+        if (PAIR && !direct) {
           // The other CTA holds the segment's other keys: each gives the other half
           // of a thread's columns, into the place of its queries, and finishes the rest.
           constexpr int kKeep = D / SPLIT / 64;  // groups of 32 columns
@@ -1021,12 +1021,12 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
       if (!any_work || !ok) cut.w = 0;
       a.cuts[blockIdx.x] = cut;
     }
-    if (a.pair)
+    if (PAIR)
       for (; met < 2; ++met) pair_sync();
   }
   // Every warp meets the other CTA twice: after the second time neither writes
   // into the other's memory.
-  if (a.pair && (warp == S::kWarpK || warp == S::kWarpV || warp == S::kWarpMma || warp == S::kWarpQ)) {
+  if (PAIR && (warp == S::kWarpK || warp == S::kWarpV || warp == S::kWarpMma || warp == S::kWarpQ)) {
     pair_sync();
     pair_sync();
   }
@@ -1197,7 +1197,7 @@ cudaError_t launch_tree_t(const TreeArgs& a, int sm_count, cudaStream_t stream) 
   if (!tmap_query_tiles(&t.tm_q, a.q, D, a.Hq, a.total_q, G, t.q_tokens) ||
       !tmap_pool_groups(&t.tm_k, a.k, D, rows) || !tmap_pool_groups(&t.tm_v, a.v, D, rows))
     return cudaErrorInvalidValue;
-  auto kern = tree_attn_kernel<D, QR>;
+  auto kern = a.pair > 0 ? tree_attn_kernel<D, QR, true> : tree_attn_kernel<D, QR, false>;
   cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), S::kSmemBytes);
   if (e != cudaSuccess) return e;
   const int grid = sm_count < kTreeMaxCtas ? sm_count : kTreeMaxCtas;
