@@ -411,6 +411,44 @@ def test_streams_graphs_and_unaligned_neighbours():
     assert torch.equal(got[:n], ref[:n])
 
 
+@pytest.mark.parametrize("D", [128, 256])
+def test_shared_segments_in_a_graph_behind_one_another(D):
+    """Launches of pairs that follow one another at once, of full and of sliding
+    layers in turn, replayed with other lengths; some of a row's segments then fit one
+    CTA, and one is longer than was promised."""
+    c = make([520, 300, 150], [12, 9, 5], D=D, seed=3)
+    table, first, masks, lens = i32(c["table"]), i32(c["first"]), i64(c["masks"]), i32(c["lens"])
+    ws, outs = workspace(c), [torch.zeros_like(c["q"]) for _ in range(6)]
+
+    def step():
+        for i, o in enumerate(outs):
+            binding.paged_tree_attn_ws(c["q"], o, c["k"], c["v"], table, first, masks, lens, 12, 500,
+                                       ws, scale=c["scale"], window=(0, 300)[i % 2])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    rows = c["first"][-1]
+    for shift in (0, 100, 140):
+        lens.copy_(i32([x - shift for x in c["lens"]]))
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, window in enumerate((0, 300)):
+            d = dict(c, lens=[x - shift for x in c["lens"]], window=window)
+            ref, spread = expected(d)
+            got = f64(outs[i])
+            assert np.all(np.abs(got - ref)[:rows] <= bound(d, ref, spread)[:rows])
+            assert not outs[i][rows:].any()
+            assert all(torch.equal(outs[j], outs[i]) for j in range(i, 6, 2))
+
+
 # ----------------------------------------------------------------- the plan
 @pytest.mark.parametrize("B,most", [(1, 1), (1, 64), (3, 7), (4, 33), (130, 64)])
 @pytest.mark.parametrize("evicted", [False, True])
