@@ -20,7 +20,7 @@
 // costs stay whole, one per CTA, or, where there are two CTAs for each segment,
 // half of the tiles for each CTA of a cluster of two: each sends the other half of
 // its rows' columns into the other's shared memory and finishes the rest, which
-// takes 1.2 us instead of the merge's 8.
+// takes about 2 us instead of the 7 of pieces and merge.
 //
 // Warps of a CTA: four softmax warps (a row of S and O lies in a TMEM lane; a thread
 // owns a row, or with QR = 64 half of its columns), one TMA warp each for K, V and
@@ -33,7 +33,7 @@
 // 64 keys, 7.0 TB/s over the SMs (softmax and MMAs, 0.5 us each, are hidden behind
 // the loads), 2 after the last copy has landed, 1.3 for the pieces' rows, and 6 for
 // the merge and its launch.  DRAM reads are the keys' bytes.  A sliding layer of
-// them (512 keys each, 64 segments on 64 pairs): 17.7 us (19.3 with a CTA each),
+// them (512 keys each, 64 segments on 64 pairs): 17.4 us (19.3 with a CTA each),
 // latency.  Four long requests (D = 128, 33 to 131 K keys, 672 MB): 116
 // us, 5.8 TB/s.  64 tokens x 4 heads are two row tiles, which read their keys twice,
 // the second time from L2: 43.7 us, 1.37 a tile, 7.4 TB/s out of L2.
@@ -44,7 +44,8 @@
 // wide trees 45.9), the walk over the pieces out of line (42.0), L2's normal policy for
 // K and V (42.4 against 38.9: partial rows leave L2 for HBM and their stores
 // wait), a piece's fixed cost of 6 blocks instead of 10 (40.4, and sliding layers 24.5
-// instead of 23.1).
+// instead of 23.1), the pairs' code in the same kernel as the rest (39.1, wide trees
+// 45.0).
 #include <cuda.h>
 
 #include "common.cuh"
