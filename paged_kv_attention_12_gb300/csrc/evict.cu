@@ -10,6 +10,7 @@
 //
 // Two launches: the selection (a CTA or cluster per segment: reads 8 bytes a
 // key, writes the list of moves), then the moves over all segments (bound by HBM).
+// Few moves are made by the selection itself.
 // 128 segments of 700 to 4096 keys (two layers, D = 256) cut to 1000: selection
 // 11 us, moves 28 us, 5.1 TB/s in rows of 512 bytes.
 #include <cooperative_groups.h>
@@ -32,7 +33,7 @@ constexpr int kGroup = 4;                 // neighbouring keys that a lane takes
 // exponents and held keys one rank, and in a single copy the lanes of a warp
 // wait for one another.
 constexpr int kDigits = 4, kBins = 256;
-constexpr int kCtaKeys = 16384;           // keys of a CTA of a cluster, at most (8 CTAs: more)
+constexpr int kCtaKeys = kEvictCtaKeys;   // keys of a CTA of a cluster, at most (8 CTAs: more)
 
 constexpr uint32_t kHeld = 0xffffffffu;   // above every mass
 
@@ -43,6 +44,68 @@ __device__ __forceinline__ uint32_t rank_of(float mass) {
   return x & 0x80000000u ? ~x : x | 0x80000000u;
 }
 
+// One warp per 4 moves of a segment: their K and V rows, all loads in flight
+// before the stores (sources and destinations are disjoint), and their masses
+// and positions (8 moves a warp: 55 us for the call of above instead of 40, at 100
+// registers; 2 moves: 43; streaming hints on the loads or the stores: 42).
+constexpr int kMoveBatch = 4;
+
+template <int D>
+__device__ __forceinline__ void move_batch(const EvictMoveArgs& m, int seg, int at, int lane) {
+  const EvictArgs& a = m.a;
+  constexpr int kRow = D * 2;                 // bytes of a row
+  constexpr int kSteps = 2 * kRow / 512;      // warp-wide copies per move: K's row, then V's
+  const size_t gseg = static_cast<size_t>(m.first_layer) * a.batch * a.Hkv + seg;
+  const size_t list = gseg * a.max_moves + at;
+  // the first lanes: the sources' rows, then the destinations' (the list may be
+  // read past its end: it lies in the workspace)
+  const int i = lane & (kMoveBatch - 1);
+  const bool listed = lane < 2 * kMoveBatch && at + i < a.max_moves;
+  int t = -1;
+  if (listed) t = lane < kMoveBatch ? a.move_src[list + i] : a.move_dst[list + i];
+  const int count = min(kMoveBatch, a.counts[gseg] - at);
+  if (count <= 0) return;
+  const int layer = seg / (a.batch * a.Hkv);
+  const int b = seg / a.Hkv % a.batch, head = seg % a.Hkv;
+  int row = i < count ? t : -1;
+  if (lane >= kMoveBatch && listed && i < count) {
+    const int id = a.tables[static_cast<size_t>(b) * a.max_blocks + t / kBlockSize];
+    if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks)) {
+      row = (id * a.Hkv + head) * kBlockSize + t % kBlockSize;
+    } else {
+      row = -1;
+      report(a.err, PKA_DEVERR_BAD_TABLE);
+    }
+    const size_t key = gseg * (static_cast<size_t>(a.max_blocks) * kBlockSize) + t;
+    a.new_mass[key] = a.move_mass[list + i];
+    a.new_pos[key] = a.move_pos[list + i];
+  }
+  uint4 x[kMoveBatch][kSteps];
+#pragma unroll
+  for (int i = 0; i < kMoveBatch; ++i) {
+    const long long src = __shfl_sync(0xffffffffu, row, i);
+    if (src < 0) continue;  // uniform
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int off = s * 512 + lane * 16;  // over K's row and V's
+      const uint8_t* pool = static_cast<const uint8_t*>(m.pools[2 * layer + off / kRow]);
+      x[i][s] = *reinterpret_cast<const uint4*>(pool + src * kRow + off % kRow);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kMoveBatch; ++i) {
+    const long long src = __shfl_sync(0xffffffffu, row, i);
+    const long long dst = __shfl_sync(0xffffffffu, row, kMoveBatch + i);
+    if (src < 0 || dst < 0) continue;  // uniform
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int off = s * 512 + lane * 16;
+      uint8_t* pool = static_cast<uint8_t*>(m.pools[2 * layer + off / kRow]);
+      *reinterpret_cast<uint4*>(pool + dst * kRow + off % kRow) = x[i][s];
+    }
+  }
+}
+
 // Ranks of the CTA's keys lie in shared memory (those past a.rank_room are made
 // again from mass and position where they are wanted), and every pass over them
 // is a short loop: with the ranks in registers the passes were unrolled, and a
@@ -51,7 +114,8 @@ __device__ __forceinline__ uint32_t rank_of(float mass) {
 // cluster's exchange, and the passes before and after them), issue for long ones.
 template <int CTAS>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(
-    const __grid_constant__ EvictArgs a) {
+    const __grid_constant__ EvictMoveArgs job) {
+  const EvictArgs& a = job.a;
   extern __shared__ int hist[];          // [kBins][32], then the ranks
   __shared__ int digit[kDigits][kBins];  // read by the other CTAs of the cluster,
   __shared__ int totals[3][CTAS];        // written by them
@@ -93,7 +157,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(
     __syncthreads();
     if (shared_block != 0) n = L;  // (the same in every CTA: all of them look at the whole row)
   }
-  if (teller) a.kept[b] = n;
+  if (teller) {
+    a.kept[b] = n;
+    if (job.here) a.new_seq_lens[b] = n;
+  }
   if (rank == 0 && threadIdx.x == 0 && n == L) a.counts[seg] = 0;
 
   const size_t first = static_cast<size_t>(seg) * max_keys;
@@ -408,14 +475,19 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(
       }
     }
   });
-  if constexpr (CTAS > 1) cluster.sync();  // the others may still read this CTA's counts
+  if constexpr (CTAS > 1) {
+    cluster.sync();  // the others may still read this CTA's counts
+  } else if (job.here) {
+    __syncthreads();
+#pragma unroll 1
+    for (int at = warp * kMoveBatch; at < moves; at += kSelWarps * kMoveBatch) {
+      if (job.here == 256)
+        move_batch<256>(job, seg, at, lane);
+      else
+        move_batch<128>(job, seg, at, lane);
+    }
+  }
 }
-
-// One warp per 4 moves of a segment: their K and V rows, all loads in flight
-// before the stores (sources and destinations are disjoint), and their masses
-// and positions (8 moves a warp: 55 us for the call of above instead of 40, at 100
-// registers; 2 moves: 43; streaming hints on the loads or the stores: 42).
-constexpr int kMoveBatch = 4;
 
 template <int D>
 __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__ EvictMoveArgs m) {
@@ -430,60 +502,10 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__
   const int per_seg = (a.max_moves + kMoveBatch - 1) / kMoveBatch;
   const long long units = static_cast<long long>(m.layers) * a.batch * a.Hkv * per_seg;
   const long long stride = static_cast<long long>(gridDim.x) * (blockDim.x / 32);
-  constexpr int kRow = D * 2;                 // bytes of a row
-  constexpr int kSteps = 2 * kRow / 512;      // warp-wide copies per move: K's row, then V's
   for (long long u = gthread / 32; u < units; u += stride) {
     const int seg = static_cast<int>(u / per_seg);
-    const int at = static_cast<int>(u - static_cast<long long>(seg) * per_seg) * kMoveBatch;
-    const size_t gseg = static_cast<size_t>(m.first_layer) * a.batch * a.Hkv + seg;
-    const size_t list = gseg * a.max_moves + at;
-    // the first lanes: the sources' rows, then the destinations' (the list may be
-    // read past its end: it lies in the workspace)
-    const int i = lane & (kMoveBatch - 1);
-    const bool listed = lane < 2 * kMoveBatch && at + i < a.max_moves;
-    int t = -1;
-    if (listed) t = lane < kMoveBatch ? a.move_src[list + i] : a.move_dst[list + i];
-    const int count = min(kMoveBatch, a.counts[gseg] - at);
-    if (count <= 0) continue;
-    const int layer = seg / (a.batch * a.Hkv);
-    const int b = seg / a.Hkv % a.batch, head = seg % a.Hkv;
-    int row = i < count ? t : -1;
-    if (lane >= kMoveBatch && listed && i < count) {
-      const int id = a.tables[static_cast<size_t>(b) * a.max_blocks + t / kBlockSize];
-      if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks)) {
-        row = (id * a.Hkv + head) * kBlockSize + t % kBlockSize;
-      } else {
-        row = -1;
-        report(a.err, PKA_DEVERR_BAD_TABLE);
-      }
-      const size_t key = gseg * (static_cast<size_t>(a.max_blocks) * kBlockSize) + t;
-      a.new_mass[key] = a.move_mass[list + i];
-      a.new_pos[key] = a.move_pos[list + i];
-    }
-    uint4 x[kMoveBatch][kSteps];
-#pragma unroll
-    for (int i = 0; i < kMoveBatch; ++i) {
-      const long long src = __shfl_sync(0xffffffffu, row, i);
-      if (src < 0) continue;  // uniform
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const int off = s * 512 + lane * 16;  // over K's row and V's
-        const uint8_t* pool = static_cast<const uint8_t*>(m.pools[2 * layer + off / kRow]);
-        x[i][s] = *reinterpret_cast<const uint4*>(pool + src * kRow + off % kRow);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kMoveBatch; ++i) {
-      const long long src = __shfl_sync(0xffffffffu, row, i);
-      const long long dst = __shfl_sync(0xffffffffu, row, kMoveBatch + i);
-      if (src < 0 || dst < 0) continue;  // uniform
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const int off = s * 512 + lane * 16;
-        uint8_t* pool = static_cast<uint8_t*>(m.pools[2 * layer + off / kRow]);
-        *reinterpret_cast<uint4*>(pool + dst * kRow + off % kRow) = x[i][s];
-      }
-    }
+    move_batch<D>(m, seg, static_cast<int>(u - static_cast<long long>(seg) * per_seg) * kMoveBatch,
+                  lane);
   }
 }
 
@@ -492,8 +514,9 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__
 // Rows of up to 16384 keys take a CTA, longer ones a cluster of two, four or eight
 // (16 rows of up to 131072 keys, selection alone: of eight 41 us, although one of
 // the clusters has to wait for the others, of four 47).
-cudaError_t launch_evict_select(const EvictArgs& args, int layers, cudaStream_t stream) {
-  EvictArgs a = args;
+cudaError_t launch_evict_select(const EvictMoveArgs& args, int layers, cudaStream_t stream) {
+  EvictMoveArgs m = args;
+  EvictArgs& a = m.a;
   const long long segs = static_cast<long long>(layers) * a.batch * a.Hkv;
   const long long keys = static_cast<long long>(a.max_blocks) * kBlockSize;
   auto launch = [&](auto kernel, int ctas) {
@@ -505,7 +528,7 @@ cudaError_t launch_evict_select(const EvictArgs& args, int layers, cudaStream_t 
                                         (kBins * 32 + kCtaKeys) * static_cast<int>(sizeof(int)));
     if (e != cudaSuccess) return e;
     return launch_overlapped(kernel, dim3(static_cast<unsigned>(ctas * segs)), kSelThreads, bytes,
-                             stream, a, ctas);
+                             stream, m, ctas);
   };
   if (keys <= kCtaKeys) return launch(evict_select_kernel<1>, 1);
   if (keys <= 2 * kCtaKeys) return launch(evict_select_kernel<2>, 2);

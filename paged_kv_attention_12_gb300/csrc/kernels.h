@@ -204,14 +204,16 @@ struct EvictArgs {
   int32_t rank_room;               // set by the launcher: keys of a CTA whose ranks it holds
 };
 
+constexpr int kEvictCtaKeys = 16384;  // longest rows whose segments take one CTA of the selection
 constexpr int kMaxEvictLayers = 128;  // layers per launch of the moves
 struct EvictMoveArgs {
   EvictArgs a;
   void* pools[2 * kMaxEvictLayers];   // K and V of layers first_layer, first_layer + 1, ...
   int32_t first_layer, layers;
+  int32_t here;                       // the head dim: the selection moves its rows itself; or 0
 };
 
-cudaError_t launch_evict_select(const EvictArgs& a, int layers, cudaStream_t stream);
+cudaError_t launch_evict_select(const EvictMoveArgs& a, int layers, cudaStream_t stream);
 cudaError_t launch_evict_move(const EvictMoveArgs& m, int head_dim, int sm_count,
                               cudaStream_t stream);
 

@@ -15,6 +15,12 @@ constexpr int32_t kMaxTree = 64;  // drafted tokens of a request (bits of a mask
 // Blocks of a table row, where keys are counted in tiles: 2^30 keys, so that no
 // tile's end passes 32 bits.
 constexpr int32_t kMaxRowBlocks = 1 << 26;
+// Bytes of K (and of V) that a segment's moves take at most where the selection
+// makes them itself, its CTA beside a second launch over the whole GPU: 2 segments of
+// 411 keys cut to 256, D = 128: 11.1 us (12.0 with the second launch), 64 of them 11.9
+// (14.1); D = 256: 12.4 (12.4) and 13.2 (15.0).  1000 keys cut to 500: D = 128 15.8
+// (14.1) and 17.0 (16.6), D = 256 18.9 (14.5) and 23.9 (20.2).
+constexpr int64_t kMovedHere = 64 << 10;
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 bool aligned16(const void* p) { return aligned(p, 16); }
@@ -351,7 +357,21 @@ int paged_kv_evict(void* const* pools, int32_t num_layers, int32_t num_blocks,
   a.recent = recent;
   a.max_moves = static_cast<int32_t>(lay.moves);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (pka::launch_evict_select(a, num_layers, s) != cudaSuccess) return PKA_ERR_CUDA;
+  // One launch for few moves of a CTA's segments.  (CTAs of a request read its length
+  // at any time: the launch that reads lengths may not write them.)
+  auto apart = [&](const int32_t* p) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(new_seq_lens);
+    const uintptr_t y = reinterpret_cast<uintptr_t>(p);
+    return p == nullptr || (x > y ? x - y : y - x) >= static_cast<uintptr_t>(B) * sizeof(int32_t);
+  };
+  if (apart(seq_lens) && apart(total_lens) && num_layers <= pka::kMaxEvictLayers &&
+      max_blocks <= pka::kEvictCtaKeys / 16 && lay.moves * head_dim * 2 <= kMovedHere) {
+    m.here = head_dim;
+    m.layers = num_layers;
+    for (int32_t i = 0; i < 2 * num_layers; ++i) m.pools[i] = pools[i];
+    return pka::launch_evict_select(m, num_layers, s) == cudaSuccess ? PKA_OK : PKA_ERR_CUDA;
+  }
+  if (pka::launch_evict_select(m, num_layers, s) != cudaSuccess) return PKA_ERR_CUDA;
   for (int32_t done = 0; done < num_layers; done += m.layers) {
     m.first_layer = done;
     m.layers = std::min(num_layers - done, pka::kMaxEvictLayers);

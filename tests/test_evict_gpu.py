@@ -119,6 +119,29 @@ def test_long_rows(L, width, mass):
         check(c, budget, min(4, budget - 1), (budget - 1) // 3, in_place=budget == 257)
 
 
+@pytest.mark.parametrize("D,budget", [(128, 255), (128, 256), (128, 257), (256, 127), (256, 128),
+                                      (256, 129)])
+@pytest.mark.parametrize("heaviest", ["first", "last"])
+def test_moves_with_the_selection_and_behind_it(D, budget, heaviest):
+    """On both sides of the bytes that a selection moves itself: as many moves as there
+    can be, and none; lengths in place and beside, masses in place and lengths not."""
+    c = make([600, 300, 40, 0, 600], hkv=3, layers=2, D=D, seed=budget, mass="random")
+    order = np.arange(c["mass"].shape[-1], dtype=np.float32)
+    c["mass"][:] = order if heaviest == "last" else -order
+    for in_place in (False, True):
+        check(c, budget, 0, 0, in_place=in_place)
+    mass, pos, lens = torch.tensor(c["mass"], device=DEV), i32(c["pos"]), i32(c["lens"])
+    new_lens, ws = i32([7] * 5), torch.full((binding.paged_kv_evict_ws_bytes(
+        2, 5, 3, c["mass"].shape[-1] // 16, budget),), 0xff, dtype=torch.uint8, device=DEV)
+    pools = [p.clone() for p in c["pools"]]
+    binding.paged_kv_evict(pools, mass, pos, i32(c["table"]), lens, None, budget, 0, 0, mass, pos,
+                           new_lens, ws)
+    torch.cuda.synchronize()
+    want, outs = run(c, budget, 0, 0, in_place=True, total=False)
+    assert all(torch.equal(x, y) for x, y in zip((*pools, mass, pos, new_lens), (*want, *outs)))
+    assert lens.tolist() == c["lens"]
+
+
 def test_without_total_lengths():
     check(make([100, 300], seed=3), 64, 4, 16, total=False)
 
