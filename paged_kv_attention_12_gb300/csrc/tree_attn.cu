@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
   constexpr int BN = S::BN, BPT = S::BPT, DC = S::DC, NW = S::kSoftmaxWarps;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t b_q, b_qfree, b_k[S::KST], b_kfree[S::KST], b_v[S::VST], b_vfree[S::VST],
-      b_s[2], b_pv[2], b_p[2], b_pair[2];
+      b_s[2], b_pv[2], b_p[2], b_pair[2], b_first;
   __shared__ float pair_value[2][2][64];  // [exchange % 2][half][row]
   __shared__ uint32_t tmem_slot;
   __shared__ int failed_flag, wild_piece[2], warp_sums[S::kThreads / 32], longest;
@@ -379,6 +379,7 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(&b_q, 1);
     mbar_init(&b_qfree, 1);
+    mbar_init(&b_first, 1);
     for (int i = 0; i < S::KST; ++i) {
       mbar_init(&b_k[i], 1);
       mbar_init(&b_kfree[i], 1);
@@ -496,7 +497,10 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
     // in about 4 us, and S comes first (D = 256: serving layer 40.4 -> 39.5 us, a
     // sliding one 21.1 -> 20.7, 64 pairs over 300 keys 14.0 -> 13.5).  D = 128 gains
     // nothing (four long requests 115.0 us without, 115.2 with it) and a small call
-    // loses (8.3 -> 8.9).
+    // loses (8.3 -> 8.9).  They wait for b_first, which the MMA warp arrives at once in
+    // a launch, when it has seen K's first tile.  b_k[0] itself will not do: K's
+    // stages are refilled without V's help, so its second phase may end before this
+    // warp has looked at the first, whose parity it then never sees.
     const bool late = D == 256 && !is_k && (PAIR || walk.rem > S::kPieceUnits + 4 * BPT);
     bool ok = true;
     while (ok && walk.next<S>(t, &p)) {
@@ -524,7 +528,7 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
         const int st = g % nst;
         const bool again = g >= nst;
         if (again || (late && g == 0))
-          ok = warp_wait(again ? &freed[st] : &b_k[0], again ? (g / nst - 1) & 1 : 0, a.err, failed);
+          ok = warp_wait(again ? &freed[st] : &b_first, again ? (g / nst - 1) & 1 : 0, a.err, failed);
         if (!ok || __any_sync(0xffffffffu, stop_requested(failed))) {
           ok = false;
           break;
@@ -570,6 +574,7 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
       if (!warp_wait(&b_k[ks], (i / S::KST) & 1, a.err, failed)) return false;
       tc_fence_after();
       if (lane == 0) {
+        if (i == 0) mbar_arrive(&b_first);
         const uint32_t kst = aK + ks * S::kStage;
 #pragma unroll
         for (int c = 0; c < DC; ++c)
