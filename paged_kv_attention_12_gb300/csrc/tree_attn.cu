@@ -676,7 +676,9 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
         see.mask = masks[tok] & own_bits;
         const int deep = __popcll(see.mask);
         see.kmin = a.window > 0 ? max(0, see.base + max(deep, 1) - a.window) : 0;
-        if (a.window > 0 && a.window < 64) {  // ancestors may lie before the window
+        // Drafted keys may lie before the window: those of a tree up to 63 before the row,
+        // of other masks 64 (all bits against none).
+        if (a.window > 0 && a.window <= 64) {
           uint64_t left = see.mask;
           while (left != 0) {
             const int j = __ffsll(static_cast<long long>(left)) - 1;

@@ -36,3 +36,17 @@ def test_first_loads_out_of_cold_memory(lens, hkv):
             assert torch.equal(out, want)
     torch.cuda.synchronize()
     assert err.item() == 0 and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("window", [62, 63, 64, 65])
+def test_windows_as_long_as_the_widest_mask(D, window):
+    """Masks that are no tree: a row of all 64 bits is 64 deeper than one of none, and a
+    window of 64 hides that key from it."""
+    rng = np.random.default_rng(5)
+    ns = [20, 64, 9]
+    masks = [int(x) for x in rng.integers(0, 1 << 63, sum(ns))] + [1] * 3
+    masks[30], masks[31], masks[40] = 0, (1 << 64) - 1, 1 << 63
+    c = make([100, 64, 400], ns, D=D, masks=masks, window=window, seed=window)
+    assert (oracle.tree_visible(masks[20:84], 64, window)[11, 10]) == (window > 64)
+    check(c, run(c))
