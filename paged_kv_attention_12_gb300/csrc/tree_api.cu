@@ -253,7 +253,8 @@ int paged_tree_accept(void* const* pools, int32_t num_pools, int32_t num_blocks,
     return PKA_ERR_NULL;
   st = check_pools(pools, num_pools);
   if (st != PKA_OK) return st;
-  if (num_kv_heads > 1024) return PKA_ERR_SHAPE;  // (255 pools a launch, 4 warps a CTA)
+  // (255 pools a launch, 4 warps a CTA; without pools their sizes are not looked at)
+  if (num_pools > 0 && num_kv_heads > 1024) return PKA_ERR_SHAPE;
   if (pools_overlap(pools, num_pools, pool_bytes(num_blocks, num_kv_heads, head_dim)))
     return PKA_ERR_SHAPE;
   pka::TreeAcceptArgs a{};

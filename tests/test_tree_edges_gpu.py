@@ -38,6 +38,29 @@ def test_first_loads_out_of_cold_memory(lens, hkv):
     assert err.item() == 0 and torch.equal(out, want)
 
 
+def accept(first, lens, parents=(-1, 0, 1), tokens=(5, 6, 7), targets=(6, 7, 8), sizes=(0, 0, 0, 0),
+           in_place=False):
+    """The walk alone, through the C entry point: (status, path, accepted, next tokens, new
+    lengths, error word)."""
+    B, n, width = len(lens), len(parents), 3
+    ins = [i32(x) for x in (parents, tokens, targets, first, lens)]
+    par, tok, tar, dfirst, dlens = (x.data_ptr() for x in ins)
+    outs = [i32(np.full((B, width), 9)), i32([9] * B), i32([9] * B),
+            ins[4] if in_place else i32([9] * B), i32([0])]
+    st = binding.lib().paged_tree_accept(None, 0, *sizes, par, tok, tar, None, dfirst, dlens, B, n,
+                                         width, *(x.data_ptr() for x in outs),
+                                         torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    return (st, *(x.tolist() for x in outs))
+
+
+@pytest.mark.parametrize("sizes", [(0, 0, 0, 0), (-1, 5000, 7, 100), (8, 1025, 16, 128),
+                                   (2 ** 30, 2 ** 31 - 1, 16, 256)])
+def test_the_walk_alone_looks_at_no_sizes(sizes):
+    """(num_blocks, num_kv_heads, block_size, head_dim) of no pools."""
+    assert accept([0, 3], [30], sizes=sizes) == (0, [[0, 1, 2]], [3], [8], [30], [0])
+
+
 @pytest.mark.parametrize("D", [128, 256])
 @pytest.mark.parametrize("window", [62, 63, 64, 65])
 def test_windows_as_long_as_the_widest_mask(D, window):
