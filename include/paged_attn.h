@@ -603,7 +603,9 @@ int paged_tree_attn_ws(const void* q, void* out, const pka_kv_pool* kv,
  * of all trees must be distinct, and so must the pools (layers that share one
  * name it once; PKA_ERR_SHAPE if two share memory).  num_pools = 0: the walk alone (slots and the
  * pools' sizes are not looked at).  A bad span leaves a request as if n = 0
- * (PKA_DEVERR_QUERY_LOC).  num_kv_heads at most 1024. */
+ * (PKA_DEVERR_QUERY_LOC), and so does n > L (PKA_DEVERR_SEQ_LEN; rows move by the
+ * slots alone, which paged_tree_plan makes negative for such a request).
+ * num_kv_heads at most 1024. */
 int paged_tree_accept(void* const* pools, int32_t num_pools, int32_t num_blocks,
                       int32_t num_kv_heads, int32_t block_size, int32_t head_dim,
                       const int32_t* parents, const int32_t* tokens, const int32_t* targets,

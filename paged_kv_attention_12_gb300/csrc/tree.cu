@@ -126,6 +126,8 @@ __global__ void __launch_bounds__(128) tree_accept_kernel(const __grid_constant_
   const int items = max(1, a.num_pools * a.Hkv);
   if (item >= items) return;
   const bool writer = item == 0 && a.write_walk != 0;
+  // (no other thread may read a length: new_seq_lens may be seq_lens)
+  const int L = writer && lane == 0 ? a.seq_lens[b] : 0;
   int q0;
   const int n = tree_span(a.query_start_loc, b, a.total_q, a.max_query_len, &q0);
   if (n < 0 && item == 0 && lane == 0) report(a.err, PKA_DEVERR_QUERY_LOC);
@@ -154,14 +156,20 @@ __global__ void __launch_bounds__(128) tree_accept_kernel(const __grid_constant_
     cur = low != 0 ? __ffs(low) - 1 : 31 + __ffs(high);
   }
   if (writer) {
+    // More tokens than keys: none is accepted.  (The plan gave them no slots, so
+    // that no warp moves a row.)
+    const int cached = __shfl_sync(kAll, L, 0);
+    const bool none = max(n, 0) > cached;
+    if (none && lane == 0) report(a.err, PKA_DEVERR_SEQ_LEN);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       if (lane + 32 * h < a.max_query_len)
-        a.path[static_cast<size_t>(b) * a.max_query_len + lane + 32 * h] = path[h];
+        a.path[static_cast<size_t>(b) * a.max_query_len + lane + 32 * h] =
+            none ? -1 : path[h];
     if (lane == 0) {
-      a.accepted[b] = count;
-      a.next_tokens[b] = next;
-      a.new_seq_lens[b] = a.seq_lens[b] - max(n, 0) + count;
+      a.accepted[b] = none ? 0 : count;
+      a.next_tokens[b] = none ? -1 : next;
+      a.new_seq_lens[b] = none ? cached : cached - max(n, 0) + count;
     }
   }
   if (a.num_pools == 0) return;

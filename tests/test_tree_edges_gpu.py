@@ -61,6 +61,38 @@ def test_the_walk_alone_looks_at_no_sizes(sizes):
     assert accept([0, 3], [30], sizes=sizes) == (0, [[0, 1, 2]], [3], [8], [30], [0])
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_more_tokens_than_keys_accept_none(in_place):
+    """A length below the tree's tokens: nothing is accepted, the length stays, and the
+    error word says so; as many keys as tokens are fine."""
+    got = accept([0, 3, 5, 5, 8], [3, 1, -4, 2], parents=[-1, 0, 1, -1, 0, -1, 0, 1],
+                 tokens=[5, 6, 7, 0, 1, 0, 1, 2], targets=[6, 7, 8, 1, 2, 1, 2, 3], in_place=in_place)
+    assert got == (0, [[0, 1, 2], [-1] * 3, [-1] * 3, [-1] * 3], [3, 0, 0, 0], [8, -1, -1, -1],
+                   [3, 1, -4, 2], [binding.DEVERR_SEQ_LEN])
+    assert accept([0, 3], [3], in_place=in_place)[5] == [0]
+
+
+def test_a_step_of_more_tokens_than_keys_leaves_the_pools():
+    """Plan and acceptance of such a request beside one that is fine."""
+    pools = [torch.randn((6, 2, 16, 128), device=DEV).to(torch.bfloat16) for _ in range(2)]
+    was = [p.clone() for p in pools]
+    parents, first, table = i32([-1, 0, 0, -1, 0, 0]), i32([0, 3, 6]), i32([[0, 1], [2, 3]])
+    lens, err = i32([2, 20]), i32([0])
+    masks = torch.ones(6, dtype=torch.int64, device=DEV)
+    pos, slots = i32([9] * 6), i32([9] * 6)
+    binding.paged_tree_plan(parents, first, lens, table, 6, 3, masks, pos, slots, err=err)
+    path, count, nxt = i32([[9] * 3] * 2), i32([9, 9]), i32([9, 9])
+    binding.paged_tree_accept(pools, parents, i32([1, 2, 3] * 2), i32([3, 0, 7] * 2), slots, first, lens,
+                              path, count, nxt, lens, err)
+    torch.cuda.synchronize()
+    assert err.item() == binding.DEVERR_SEQ_LEN and lens.tolist() == [2, 19]
+    assert path.tolist() == [[-1] * 3, [0, 2, -1]] and count.tolist() == [0, 2]
+    assert nxt.tolist() == [-1, 7]
+    for p, w in zip(pools, was):
+        w[3, :, 2] = w[3, :, 3]         # token 2 (position 19) to the place of token 1
+        assert torch.equal(p, w)
+
+
 @pytest.mark.parametrize("D", [128, 256])
 @pytest.mark.parametrize("window", [62, 63, 64, 65])
 def test_windows_as_long_as_the_widest_mask(D, window):
