@@ -544,7 +544,7 @@ int paged_kv_compact(void* const* pools, int32_t num_pools, int32_t num_blocks,
  *   PKA_DEVERR_TREE into *err and counts as -1.  Rows from query_start_loc[B] on
  *   (padding) get mask 0, position 0, slot -1.  A request whose span is not as
  *   in paged_prefill_attn is left out (PKA_DEVERR_QUERY_LOC, its rows unwritten);
- *   one with n > L or L past its table row gets mask 0, position 0, slot -1
+ *   one with n > L, n > T or L past its table row gets mask 0, position 0, slot -1
  *   (PKA_DEVERR_SEQ_LEN); a table id outside the pool gives slot -1
  *   (PKA_DEVERR_BAD_TABLE).  max_query_len > 64: PKA_ERR_UNSUPPORTED. */
 int paged_tree_plan(const int32_t* parents, const int32_t* query_start_loc,

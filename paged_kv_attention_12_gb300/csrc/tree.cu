@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(128) tree_plan_kernel(const TreePlanArgs a) {
   }
   const int L = a.seq_lens[b];
   const int T = a.total_lens != nullptr ? a.total_lens[b] : L;
-  const bool fits = n <= L && L <= a.max_blocks * kBlockSize;
+  const bool fits = n <= L && n <= T && L <= a.max_blocks * kBlockSize;
   if (!fits && lane == 0) report(a.err, PKA_DEVERR_SEQ_LEN);
   int up[2];
   uint64_t mask[2];

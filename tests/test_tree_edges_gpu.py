@@ -38,6 +38,20 @@ def test_first_loads_out_of_cold_memory(lens, hkv):
     assert err.item() == 0 and torch.equal(out, want)
 
 
+def test_plan_of_sequences_shorter_than_their_trees():
+    """A sequence's length below its tokens would give negative positions."""
+    err, masks = i32([0]), torch.full((9,), 9, dtype=torch.int64, device=DEV)
+    pos, slots = i32([9] * 9), i32([9] * 9)
+    binding.paged_tree_plan(i32([-1, 0, 0] * 3), i32([0, 3, 6, 9]), i32([20, 20, 20]),
+                            i32([[0, 1], [2, 3], [4, 5]]), 6, 3, masks, pos, slots,
+                            total_lens=i32([2, 3, -5]), err=err)
+    torch.cuda.synchronize()
+    assert err.item() == binding.DEVERR_SEQ_LEN
+    assert masks.tolist() == [0] * 3 + [1, 3, 5] + [0] * 3
+    assert pos.tolist() == [0] * 3 + [0, 1, 1] + [0] * 3
+    assert slots.tolist() == [-1] * 3 + [49, 50, 51] + [-1] * 3
+
+
 def accept(first, lens, parents=(-1, 0, 1), tokens=(5, 6, 7), targets=(6, 7, 8), sizes=(0, 0, 0, 0),
            in_place=False):
     """The walk alone, through the C entry point: (status, path, accepted, next tokens, new
