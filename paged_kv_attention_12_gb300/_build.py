@@ -4,6 +4,8 @@ Each ``csrc/*.cu`` file is compiled by nvcc in parallel, then linked into one
 shared library next to this file (``lib/libpaged_attn.so``).  Beside it
 ``csrc/native_binding.cpp``, the Python side of some of the library's calls,
 becomes the module ``lib/_native.so`` (the host compiler, torch's headers).
+The library needs the CUDA toolchain alone: where the module cannot be built,
+there is a warning and the library all the same, and only those calls raise.
 Rebuilds only when a source or header is newer than the libraries.
 """
 from __future__ import annotations
@@ -13,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -81,6 +84,18 @@ def _compile_native() -> None:
     os.replace(tmp, NATIVE_PATH)
 
 
+def _try_native(running=None) -> None:
+    """Builds the module, or waits for ``running``, which does; warns where that fails
+    (and takes away a module of older sources)."""
+    try:
+        _compile_native() if running is None else running.result()
+    except Exception as e:
+        if os.path.exists(NATIVE_PATH):
+            os.remove(NATIVE_PATH)
+        warnings.warn(f"{os.path.basename(NATIVE_PATH)} was not built; the draft-tree and eviction "
+                      f"calls of the Python binding will raise: {e}", RuntimeWarning, stacklevel=3)
+
+
 def _compile(src: str, obj: str, extra) -> None:
     cmd = [nvcc(), *ARCH, "-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
            "-I", INCLUDE, "-I", CSRC, "--expt-relaxed-constexpr", *extra, "-c", src, "-o", obj]
@@ -103,14 +118,13 @@ def build(force: bool = False, verbose: bool = False, extra=(), lib_path: str = 
     out_dir = os.path.dirname(lib_path)
     os.makedirs(out_dir, exist_ok=True)
     if not want_lib:
-        _compile_native()
+        _try_native()
         return lib_path
     srcs = _sources()
     objs = [os.path.join(out_dir, os.path.basename(s)[:-3] + ".o") for s in srcs]
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
         futs = [ex.submit(_compile, s, o, list(extra)) for s, o in zip(srcs, objs)]
-        if want_native:
-            futs.append(ex.submit(_compile_native))
+        native = ex.submit(_compile_native) if want_native else None
         for f in futs:
             f.result()
     tmp = lib_path + ".tmp"
@@ -119,6 +133,8 @@ def build(force: bool = False, verbose: bool = False, extra=(), lib_path: str = 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib_path)
+    if native is not None:
+        _try_native(native)
     if verbose:
         print(f"built {lib_path}", file=sys.stderr)
     return lib_path
