@@ -6,7 +6,8 @@ shared library next to this file (``lib/libpaged_attn.so``).  Beside it
 becomes the module ``lib/_native.so`` (the host compiler, torch's headers).
 The library needs the CUDA toolchain alone: where the module cannot be built,
 there is a warning and the library all the same, and only those calls raise.
-Rebuilds only when a source or header is newer than the libraries.
+Rebuilds only when a source or header is newer than the libraries, and the
+module also when it was compiled for another Python or torch (``lib/_native.abi``).
 """
 from __future__ import annotations
 
@@ -25,6 +26,7 @@ OUT_DIR = os.path.join(HERE, "lib")
 LIB_PATH = os.path.join(OUT_DIR, "libpaged_attn.so")
 NATIVE_SRC = os.path.join(CSRC, "native_binding.cpp")
 NATIVE_PATH = os.path.join(OUT_DIR, "_native.so")
+NATIVE_ABI = os.path.join(OUT_DIR, "_native.abi")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -58,9 +60,29 @@ def up_to_date(lib_path: str = LIB_PATH) -> bool:
     return _newer(lib_path, _deps())
 
 
+def native_abi() -> str:
+    """What a compiled module depends on beside its sources: this Python, and this torch
+    (its C++ classes, and where its libraries lie)."""
+    import sysconfig
+
+    import torch
+    return "\n".join((sysconfig.get_config_var("SOABI") or sys.version, torch.__version__,
+                      str(torch.version.git_version), str(torch._C._GLIBCXX_USE_CXX11_ABI),
+                      os.path.dirname(torch.__file__)))
+
+
+def native_fits() -> bool:
+    """Whether the built module was compiled for this Python and this torch."""
+    try:
+        with open(NATIVE_ABI, encoding="utf-8") as f:
+            return f.read() == native_abi()
+    except OSError:
+        return False
+
+
 def native_up_to_date() -> bool:
     return _newer(NATIVE_PATH, [NATIVE_SRC, os.path.join(INCLUDE, "paged_attn.h"),
-                                os.path.abspath(__file__)])
+                                os.path.abspath(__file__)]) and native_fits()
 
 
 def _compile_native() -> None:
@@ -81,7 +103,13 @@ def _compile_native() -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"the host compiler failed on {os.path.basename(NATIVE_SRC)}:\n{r.stdout}\n{r.stderr}")
+    # (no stamp stands beside a module that it is not of)
+    if os.path.exists(NATIVE_ABI):
+        os.remove(NATIVE_ABI)
     os.replace(tmp, NATIVE_PATH)
+    with open(NATIVE_ABI + ".tmp", "w", encoding="utf-8") as f:
+        f.write(native_abi())
+    os.replace(NATIVE_ABI + ".tmp", NATIVE_ABI)
 
 
 def _try_native(running=None) -> None:
@@ -94,6 +122,13 @@ def _try_native(running=None) -> None:
             os.remove(NATIVE_PATH)
         warnings.warn(f"{os.path.basename(NATIVE_PATH)} was not built; the draft-tree and eviction "
                       f"calls of the Python binding will raise: {e}", RuntimeWarning, stacklevel=3)
+
+
+def _native_done() -> bool:
+    try:
+        return native_up_to_date()
+    except ImportError:  # without torch there is no module (the attempt will say so)
+        return False
 
 
 def _compile(src: str, obj: str, extra) -> None:
@@ -112,7 +147,7 @@ def build(force: bool = False, verbose: bool = False, extra=(), lib_path: str = 
     never replaces the product library.
     """
     want_lib = force or not up_to_date(lib_path)
-    want_native = lib_path == LIB_PATH and (force or not native_up_to_date())
+    want_native = lib_path == LIB_PATH and (force or not _native_done())
     if not want_lib and not want_native:
         return lib_path
     out_dir = os.path.dirname(lib_path)

@@ -659,6 +659,11 @@ def _native():
         if not os.path.exists(path):
             raise RuntimeError(
                 f"{path} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
+        from . import _build
+        if not _build.native_fits():
+            raise RuntimeError(
+                f"{path} was built for another Python or torch: build it again (python -c 'import "
+                "__graft_entry__ as g; g.build()')")
         loader = importlib.machinery.ExtensionFileLoader("_native", path)
         m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_native", loader))
         loader.exec_module(m)

@@ -17,6 +17,7 @@ def small(tmp_path, monkeypatch):
     monkeypatch.setattr(_build, "_sources", lambda: [str(tmp_path / "one.cu")])
     monkeypatch.setattr(_build, "LIB_PATH", str(out / "libone.so"))
     monkeypatch.setattr(_build, "NATIVE_PATH", str(out / "_native.so"))
+    monkeypatch.setattr(_build, "NATIVE_ABI", str(out / "_native.abi"), raising=False)
     monkeypatch.setattr(_build, "NATIVE_SRC", str(tmp_path / "module.cpp"))
     return tmp_path
 
@@ -53,3 +54,29 @@ def test_calls_without_their_module_say_so(monkeypatch):
     monkeypatch.setattr(binding, "HERE", os.path.join(binding.HERE, "nowhere"))
     with pytest.raises(RuntimeError, match="build it first"):
         binding._native()
+
+
+def test_a_module_of_another_torch_is_built_again(small, monkeypatch):
+    """Times of files do not show a change of torch or of Python."""
+    import torch
+    path = build()
+    built = os.stat(_build.NATIVE_PATH).st_mtime_ns
+    assert build() == path and os.stat(_build.NATIVE_PATH).st_mtime_ns == built
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "0.0.1")
+        build()
+        again = os.stat(_build.NATIVE_PATH).st_mtime_ns
+        assert again > built
+    build()
+    assert os.stat(_build.NATIVE_PATH).st_mtime_ns > again
+
+
+def test_a_module_of_another_torch_is_not_loaded(monkeypatch):
+    import torch
+    _build.build()
+    monkeypatch.setattr(binding, "_native_module", None)
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    with pytest.raises(RuntimeError, match="another Python or torch"):
+        binding._native()
+    monkeypatch.undo()
+    assert binding._native() is not None
