@@ -119,3 +119,36 @@ def test_windows_as_long_as_the_widest_mask(D, window):
     c = make([100, 64, 400], ns, D=D, masks=masks, window=window, seed=window)
     assert (oracle.tree_visible(masks[20:84], 64, window)[11, 10]) == (window > 64)
     check(c, run(c))
+
+
+@pytest.mark.parametrize("B", [255, 256, 257, 512, 513])
+@pytest.mark.parametrize("last", [4, 900])
+def test_as_many_requests_as_threads(B, last):
+    """The work is summed by 256 threads, then in rounds of them: batches around whole
+    rounds, whose last request has rows, on a line of work that is cut and on one that
+    is not."""
+    rng = np.random.default_rng(B)
+    ns = [int(x) for x in rng.choice([0, 1, 2], B)]
+    ns[-1] = ns[0] = 3
+    lens = [max(n, int(x)) for n, x in zip(ns, rng.integers(0, 40, B))]
+    lens[-1] = last
+    c = make(lens, ns, hq=4, seed=B)
+    err = i32([0])
+    out = run(c, err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    check(c, out)
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (8, 2), (8, 1)])
+def test_promises_wider_than_the_batch(D, hq, hkv):
+    """Captured steps promise the widest tree and the longest row: 64 tokens over a batch
+    of a few rows, of one, and all of the table's keys."""
+    for lens, ns in (([40, 7, 200], [2, 1, 3]), ([1], [1]), ([33], [1])):
+        c = dict(make(lens, ns, D=D, hq=hq, hkv=hkv, pad=0, seed=D), most=64)
+        keys = 16 * c["table"].shape[1]
+        check(c, run(c, max_len=keys))
+        binding.paged_tree_plan(i32(c["parents"]), i32(c["first"]), i32(c["lens"]), i32(c["table"]),
+                                len(c["k"]), 64, i64([0] * len(c["masks"])), None, None)
+    torch.cuda.synchronize()
