@@ -116,7 +116,8 @@ struct TreeArgs {
   const int32_t* seq_lens;
   int32_t* err;
   float* partial_o;                // fp32 [2 * CTAs][D/4][rows][4]
-  float* partial_lse;              // fp32 [2 * CTAs][rows], log2 domain
+  float* partial_lse;              // fp32 [2 * CTAs][rows], log2 domain; -infinity: sees nothing,
+                                   // +infinity: logits that are all -infinity
   int4* cuts;                      // [CTAs]: the cut segment that begins in the chunk: first
                                    // query row, first head, rows, pieces (0: none)
   int32_t batch, Hq, Hkv, num_blocks, max_blocks, total_q, max_query_len;

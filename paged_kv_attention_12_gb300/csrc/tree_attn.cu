@@ -899,9 +899,17 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
           seen = seen || other != 0.f;
           if (other != -1.f) l += other;
         }
-        // a row whose visible logits are all -infinity: 0 / 0; one that sees
-        // nothing: 0
-        const float inv = l > 0.f ? 1.f / l : (seen ? __int_as_float(0x7fffffff) : 0.f);
+        // A row whose visible logits are all -infinity: 0 / 0; one that sees nothing: 0.
+        // A piece of such logits alone (LSE +infinity) goes on as it is, zeros, or NaN where
+        // V has an infinity or a NaN: with other pieces beside it that is its share.
+        const bool unweighed = l == 0.f && seen;
+        const float inv = l > 0.f                  ? 1.f / l
+                          : !seen                  ? 0.f
+                          : direct || !unweighed   ? __int_as_float(0x7fffffff)
+                                                   : 1.f;
+        const float lse = unweighed  ? INFINITY
+                          : l == 0.f ? -INFINITY
+                                     : m_ref + log2f(l);  // (a NaN sum: NaN)
         const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (p.first ? 1 : 0);
         float* prow = a.partial_o + (slot * (D / 4) * QR + r) * 4;
         uint16_t* orow =
@@ -916,7 +924,6 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
           const float4* rows_here =
               reinterpret_cast<const float4*>(sQ) + half * kKeep * 8 * QR + r;
           float* lse_here = &pair_value[0][0][0] + r;
-          const float lse = l == 0.f ? -INFINITY : m_ref + log2f(l);
           pair_sync();  // the other CTA has done with its queries
           ++met;
 #pragma unroll 1
@@ -936,29 +943,24 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
           pair_sync();
           ++met;
           const float far_lse = *lse_here;
-          const float top = fmaxf(lse, far_lse);
-          const float w = lse == -INFINITY ? 0.f : fast_exp2(lse - top);
-          const float far_w = far_lse == -INFINITY ? 0.f : fast_exp2(far_lse - top);
+          const bool near_weight = fabsf(lse) != INFINITY, far_weight = fabsf(far_lse) != INFINITY;
+          const float top = fmaxf(near_weight ? lse : -INFINITY, far_weight ? far_lse : -INFINITY);
+          const float w = near_weight ? fast_exp2(lse - top) : 0.f;
+          const float far_w = far_weight ? fast_exp2(far_lse - top) : 0.f;
           // (no weight at all: NaN if one of them sees keys, else 0)
           const float den = w + far_w;
           const bool none = den == 0.f;
-          const bool dead = none && (!(inv == 0.f) || !(rows_here[0].x == 0.f));
-          const float f = none              ? (dead ? __int_as_float(0x7fffffff) : 0.f)
-                          : lse == -INFINITY ? 0.f
-                                             : w * inv / den;
+          const float f = !none                                       ? w * inv / den
+                          : lse == INFINITY || far_lse == INFINITY ? __int_as_float(0x7fffffff)
+                                                                    : 0.f;
           const float far_f = none ? 0.f : far_w / den;
 #pragma unroll 1
           for (int c = 0; c < kKeep; ++c) {
             float o[32];
             tmem_ld32(lane_base + S::kTmemO + (keep + c) * 32, o);
-            if (lse == -INFINITY) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = 0.f;
-            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              float4 y = rows_here[(c * 8 + e) * QR];
-              if (far_lse == -INFINITY) y = make_float4(0.f, 0.f, 0.f, 0.f);
+              const float4 y = rows_here[(c * 8 + e) * QR];
               o[4 * e] = fmaf(f, o[4 * e], far_f * y.x);
               o[4 * e + 1] = fmaf(f, o[4 * e + 1], far_f * y.y);
               o[4 * e + 2] = fmaf(f, o[4 * e + 2], far_f * y.z);
@@ -1008,9 +1010,7 @@ __global__ void __launch_bounds__(TreeShape<D, QR>::kThreads, 1)
                               o[4 * e + 3] * inv);
           }
         }
-        if (!direct && half == 0)
-          a.partial_lse[slot * QR + r] =
-              l == 0.f ? -INFINITY : m_ref + log2f(l);  // (a NaN sum: NaN)
+        if (!direct && half == 0) a.partial_lse[slot * QR + r] = lse;
         if (row_valid && *const_cast<volatile int*>(&wild_piece[piece & 1]) == piece) {
           auto add = [&](int lo, int hi) {
             if (direct)
@@ -1123,10 +1123,18 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) tree_merge_kernel(
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        // (a piece without a weight counts as nothing; its row is NaN if it
-        // sees keys whose logits are all -infinity, else zeros)
-        if (lse[i] == -INFINITY) {
-          dead = dead || !(y[i][0].x == 0.f);
+        // a piece that sees nothing; one of logits that are all -infinity, whose
+        // row holds zeros and the infinities and NaN of V, 0 times which is NaN
+        if (lse[i] == -INFINITY) continue;
+        if (lse[i] == INFINITY) {
+          dead = true;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            x.acc[q].x += 0.f * y[i][q].x;
+            x.acc[q].y += 0.f * y[i][q].y;
+            x.acc[q].z += 0.f * y[i][q].z;
+            x.acc[q].w += 0.f * y[i][q].w;
+          }
           continue;
         }
         const float nm = fmaxf(x.M, lse[i]);
@@ -1158,9 +1166,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) tree_merge_kernel(
         for (int w = warp; w < warp + share; ++w) {
           const float m = sm[w][0][lane], d = sm[w][1][lane];
           if (d == -1.f) nothing = true;
-          if (d == 0.f || d == -1.f) continue;
-          const float f = m == -INFINITY ? 1.f : fast_exp2(m - top);  // (-infinity: a NaN sum)
-          sum += f * d;
+          // (without a weight: zeros and NaN; -infinity beside one: a NaN sum)
+          const bool no_weight = d == 0.f || d == -1.f;
+          const float f = no_weight || m == -INFINITY ? 1.f : fast_exp2(m - top);
+          if (!no_weight) sum += f * d;
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const float4 v = so[w][q][lane];

@@ -9,6 +9,7 @@ from tests.test_tree_gpu import check, f64, i32, i64, make, run, workspace
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
+NAN = float("nan")
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -152,3 +153,31 @@ def test_promises_wider_than_the_batch(D, hq, hkv):
         binding.paged_tree_plan(i32(c["parents"]), i32(c["first"]), i32(c["lens"]), i32(c["table"]),
                                 len(c["k"]), 64, i64([0] * len(c["masks"])), None, None)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("lens,first", [
+    ([60], 0), ([500, 500], 0),                       # whole; pairs of CTAs
+    ([3000], 0), ([3000], 2048), ([9000, 4000], 0),   # cut: the first pieces, the last, many
+    ([24000], 0)])
+@pytest.mark.parametrize("value", [NAN, float("inf")])
+def test_what_v_holds_behind_logits_of_minus_infinity(D, lens, first, value):
+    """A key whose logit is -infinity has no weight, and 0 times an infinity or NaN in its
+    V is NaN: also where a whole piece of the keys is such, and however keys are cut."""
+    c = make(lens, [5] * len(lens), D=D, hq=4, hkv=1, seed=len(lens))
+    c["q"][:] = c["q"].abs() + 0.1
+    for b, L in enumerate(lens):
+        for t in range(first, max(first, 3 * L // 5 if first == 0 else L - 5)):
+            c["k"][c["table"][b, t // 16], 0, t % 16, 0] = -float("inf")
+    clean = run(c)
+    at = first + 3
+    d = dict(c, v=c["v"].clone())
+    d["v"][c["table"][0, at // 16], 0, at % 16, 7] = value
+    rows, got = c["first"][-1], run(d)
+    with np.errstate(invalid="ignore"):
+        want = oracle.tree_attention(f64(d["q"]), f64(d["k"]), f64(d["v"]), d["table"], d["first"],
+                                     d["masks"], d["lens"], d["scale"])
+    assert np.array_equal(np.isfinite(f64(got))[:rows], np.isfinite(want)[:rows])
+    keep = torch.isfinite(got.float())
+    assert torch.equal(got[keep], clean[keep]) and not keep[:5, :, 7].any()
+    assert torch.isfinite(clean.float()).all()
