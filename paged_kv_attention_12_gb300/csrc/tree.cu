@@ -126,11 +126,17 @@ __global__ void __launch_bounds__(128) tree_accept_kernel(const __grid_constant_
   const int items = max(1, a.num_pools * a.Hkv);
   if (item >= items) return;
   const bool writer = item == 0 && a.write_walk != 0;
-  // (no other thread may read a length: new_seq_lens may be seq_lens)
-  const int L = writer && lane == 0 ? a.seq_lens[b] : 0;
+  // (no other warp may read a length: new_seq_lens may be seq_lens)
+  const int L = writer ? a.seq_lens[b] : 0x7fffffff;
   int q0;
   const int n = tree_span(a.query_start_loc, b, a.total_q, a.max_query_len, &q0);
-  if (n < 0 && item == 0 && lane == 0) report(a.err, PKA_DEVERR_QUERY_LOC);
+  // What is wrong is reported once, in the end: a branch at each place costs 0.4 us
+  // of 5.1 (four layers of wide trees).
+  int bad = n < 0 && item == 0 ? PKA_DEVERR_QUERY_LOC : 0;
+  // More tokens than keys: none is accepted.  (The plan gave them no slots, so that no
+  // warp moves a row.)
+  const bool none = max(n, 0) > L;
+  if (none) bad |= PKA_DEVERR_SEQ_LEN;
   int parent[2], token[2], target[2], slot[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -140,7 +146,7 @@ __global__ void __launch_bounds__(128) tree_accept_kernel(const __grid_constant_
     token[h] = in ? a.tokens[q0 + i] : 0;
     target[h] = in ? a.targets[q0 + i] : 0;
     slot[h] = in && a.num_pools > 0 ? a.slots[q0 + i] : -1;
-    if (in && item == 0 && (parent[h] < -1 || parent[h] >= i)) report(a.err, PKA_DEVERR_TREE);
+    if (in && item == 0 && (parent[h] < -1 || parent[h] >= i)) bad |= PKA_DEVERR_TREE;
   }
   // path[h]: index of the path's token number lane + 32 h
   int path[2] = {-1, -1}, count = 0, next = -1;
@@ -156,23 +162,21 @@ __global__ void __launch_bounds__(128) tree_accept_kernel(const __grid_constant_
     cur = low != 0 ? __ffs(low) - 1 : 31 + __ffs(high);
   }
   if (writer) {
-    // More tokens than keys: none is accepted.  (The plan gave them no slots, so
-    // that no warp moves a row.)
-    const int cached = __shfl_sync(kAll, L, 0);
-    const bool none = max(n, 0) > cached;
-    if (none && lane == 0) report(a.err, PKA_DEVERR_SEQ_LEN);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       if (lane + 32 * h < a.max_query_len)
-        a.path[static_cast<size_t>(b) * a.max_query_len + lane + 32 * h] =
-            none ? -1 : path[h];
+        a.path[static_cast<size_t>(b) * a.max_query_len + lane + 32 * h] = none ? -1 : path[h];
+    __syncwarp();  // every lane has read the length
     if (lane == 0) {
       a.accepted[b] = none ? 0 : count;
       a.next_tokens[b] = none ? -1 : next;
-      a.new_seq_lens[b] = none ? cached : cached - max(n, 0) + count;
+      a.new_seq_lens[b] = none ? L : L - max(n, 0) + count;
     }
   }
-  if (a.num_pools == 0) return;
+  if (a.num_pools == 0) {
+    if (bad != 0) report(a.err, bad);
+    return;
+  }
   const int pool = item / a.Hkv, head = item - pool * a.Hkv;
   uint8_t* base = static_cast<uint8_t*>(a.pools[pool]);
   constexpr int kLanes = D / 8;          // lanes of a row, 16 bytes each
@@ -188,7 +192,7 @@ __global__ void __launch_bounds__(128) tree_accept_kernel(const __grid_constant_
       const int src = of_token(slot[0], slot[1], p), dst = of_token(slot[0], slot[1], k & 63);
       if (k >= count || p == k || src < 0 || dst < 0) continue;
       if (src / kBlockSize >= a.num_blocks || dst / kBlockSize >= a.num_blocks) {
-        if (part == 0) report(a.err, PKA_DEVERR_BAD_TABLE);
+        bad |= PKA_DEVERR_BAD_TABLE;
         continue;
       }
       here |= 1u << u;
@@ -207,6 +211,7 @@ __global__ void __launch_bounds__(128) tree_accept_kernel(const __grid_constant_
     }
     __syncwarp();
   }
+  if (bad != 0) report(a.err, bad);
 }
 
 }  // namespace
