@@ -181,3 +181,99 @@ def test_what_v_holds_behind_logits_of_minus_infinity(D, lens, first, value):
     keep = torch.isfinite(got.float())
     assert torch.equal(got[keep], clean[keep]) and not keep[:5, :, 7].any()
     assert torch.isfinite(clean.float()).all()
+
+
+def test_pools_past_four_gib():
+    """Blocks whose bytes lie past 2^32 and whose elements past 2^31: attention,
+    acceptance and eviction give what they give in a small pool."""
+    hkv, D, blocks, small = 8, 256, 70000, 24
+    if torch.cuda.mem_get_info()[0] < 3 * blocks * hkv * 16 * D * 2:
+        pytest.skip("not enough free memory")
+    near = [torch.randn((small, hkv, 16, D), device=DEV).to(torch.bfloat16) for _ in range(2)]
+    far = [torch.empty((blocks, hkv, 16, D), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    assert far[0].numel() > 1 << 31 and 2 * far[0].numel() > 1 << 32
+    up = blocks - small
+    for f, n in zip(far, near):
+        f[up:] = n
+    parents, first, lens = [-1, 0, 0, 1, 2, -1, 0, 1], i32([0, 5, 8]), [192, 97]
+    table = np.arange(24).reshape(2, 12)
+    tokens, targets = i32([1, 2, 3, 4, 5, 1, 2, 3]), i32([3, 0, 5, 0, 0, 2, 9, 0])
+    q = torch.randn((8, 8, D), device=DEV).to(torch.bfloat16)
+    results = []
+    for pools, base in ((near, 0), (far, up)):
+        seq, tab, err = i32(lens), i32(table + base), i32([0])
+        masks, slots = torch.zeros(8, dtype=torch.int64, device=DEV), i32([0] * 8)
+        binding.paged_tree_plan(i32(parents), first, seq, tab, len(pools[0]), 5, masks, None, slots,
+                                err=err)
+        pools[1][base + 11, 3, 15, 9] = float("inf")         # request 0's last drafted key
+        out = torch.zeros_like(q)
+        ws = torch.zeros(binding.paged_tree_attn_ws_bytes(8, hkv, D, 5), dtype=torch.uint8, device=DEV)
+        binding.paged_tree_attn_ws(q, out, *pools, tab, first, masks, seq, 5, 192, ws, scale=0.06,
+                                   err=err)
+        path, few = i32(np.zeros((2, 5))), [i32([0, 0]) for _ in range(2)]
+        binding.paged_tree_accept(pools, i32(parents), tokens, targets, slots, first, seq, path, *few, seq,
+                                  err)
+        mass = torch.arange(2 * hkv * 192, device=DEV).float().view(1, 2, hkv, 192) % 37
+        kpos = torch.full(mass.shape, -1, dtype=torch.int32, device=DEV)
+        n = binding.paged_kv_evict_ws_bytes(1, 2, hkv, 12, 60)
+        binding.paged_kv_evict(pools, mass, kpos, tab, seq, None, 60, 4, 16, mass, kpos, seq,
+                               torch.zeros(n, dtype=torch.uint8, device=DEV), err=err)
+        torch.cuda.synchronize()
+        assert err.item() == 0
+        results.append([out, slots - 16 * base, path, *few, seq, mass, kpos, *(p[base:base + small] for p in pools)])
+    for x, y in zip(*results):
+        assert torch.equal(x.view(torch.int16) if x.dtype == torch.bfloat16 else x,
+                           y.view(torch.int16) if y.dtype == torch.bfloat16 else y)
+
+
+def test_two_streams_at_once():
+    """Steps on two streams, each with workspaces of its own, give what they give alone:
+    shared and cut segments, acceptance and eviction beside one another."""
+    cases = [make([600] * 6, [9] * 6, D=256, seed=1), make([5000, 300, 2200], [16, 3, 16], D=128, seed=2)]
+    jobs = []
+    for c in cases:
+        B, keys = len(c["lens"]), 16 * c["table"].shape[1]
+        rows = len(c["masks"])
+        args = dict(c=c, B=B, keys=keys, tab=i32(c["table"]), first=i32(c["first"]), lens=i32(c["lens"]),
+                    masks=i64(c["masks"]), parents=i32(c["parents"]), ws=workspace(c),
+                    tokens=i32([1] * rows), slots=i32([0] * rows),
+                    mass=torch.rand((1, B, 2, keys), device=DEV),
+                    kpos=torch.full((1, B, 2, keys), -1, dtype=torch.int32, device=DEV),
+                    ews=torch.zeros(binding.paged_kv_evict_ws_bytes(1, B, 2, keys // 16, 256),
+                                    dtype=torch.uint8, device=DEV))
+        jobs.append(args)
+
+    def step(j):
+        c, B = j["c"], j["B"]
+        pools = [c["k"].clone(), c["v"].clone()]
+        out, lens = torch.zeros_like(c["q"]), j["lens"].clone()
+        mass, kpos = j["mass"].clone(), j["kpos"].clone()
+        path, few = torch.zeros((B, c["most"]), dtype=torch.int32, device=DEV), \
+            [torch.zeros(B, dtype=torch.int32, device=DEV) for _ in range(2)]
+        for _ in range(3):
+            binding.paged_tree_attn_ws(c["q"], out, *pools, j["tab"], j["first"], j["masks"], lens,
+                                       c["most"], max(c["lens"]), j["ws"], scale=c["scale"])
+        binding.paged_tree_plan(j["parents"], j["first"], lens, j["tab"], len(pools[0]), c["most"], None,
+                                None, j["slots"])
+        binding.paged_tree_accept(pools, j["parents"], j["tokens"], j["tokens"], j["slots"], j["first"],
+                                  lens, path, *few, lens)
+        binding.paged_kv_evict(pools, mass, kpos, j["tab"], lens, None, 256, 4, 16, mass, kpos, lens,
+                               j["ews"])
+        return [out, path, *few, lens, mass, kpos, *pools]
+
+    alone = [step(j) for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(10):
+        for i, (j, s) in enumerate(zip(jobs, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(step(j))
+    torch.cuda.synchronize()
+    for want, runs in zip(alone, got):
+        for r in runs:
+            for x, y in zip(r, want):
+                assert torch.equal(x.view(torch.int16) if x.dtype == torch.bfloat16 else x,
+                                   y.view(torch.int16) if y.dtype == torch.bfloat16 else y)
