@@ -561,7 +561,10 @@ int paged_tree_plan(const int32_t* parents, const int32_t* query_start_loc,
  *     or d_i - d_j < window.
  * The masks need not come from a tree.  No visible key: output 0; visible
  * logits that are all -infinity: NaN.  Infinities and NaN in K or V reach the
- * queries that see them and no others.  Rows of no request are not written.
+ * queries that see them, at a weight of 0 too, and no others.  Rows of no request
+ * are not written.  Logits, maxima and sums are fp32; each weight is rounded
+ * to bf16 for its product with V (by 2^-8 of it at most; the sum that divides
+ * is of the unrounded ones), as in the other calls over bf16 pools.
  * Keys are cache positions: with a window the cache has to hold the sequence
  * unevicted.
  * One launch, or two: the segments (request, KV head, tile of 128 / G or 64 / G
@@ -569,7 +572,11 @@ int paged_tree_plan(const int32_t* parents, const int32_t* query_start_loc,
  * a chunk cuts is merged in key order by the second launch.  Where max_seq_len
  * and the number of segments let none be cut there is no second launch; few of
  * them are shared by two CTAs each.  The same call gives the same bits every
- * time.  max_seq_len is a promise; longer rows are computed all the same.
+ * time.  max_seq_len is a promise; longer rows are computed all the same, and the
+ * nearest one finds the fastest of these forms.
+ * The call gathers no key mass (paged_decode_key_mass does, after a plain decode
+ * step): tokens that are accepted from trees have mass 0 until a decode step sees
+ * them, and are the first that paged_kv_evict gives up once they are not recent.
  * workspace: 16-byte aligned, at least paged_tree_attn_ws_bytes() bytes (which
  * depend on no length and no batch), needs no initialisation.  Calls sharing one
  * workspace must not overlap on the GPU.

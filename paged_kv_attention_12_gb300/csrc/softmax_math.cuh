@@ -56,9 +56,6 @@ __device__ __forceinline__ float tanh_via_exp2(float y) {
   return 1.f - __fdividef(2.f, e + 1.f);
 }
 
-// tanh(y) for |y| < 0.5 from its odd Taylor series through y^11 (the first
-// omitted term, 21844 y^13 / 6081075, is below 4.5e-7 there): FMA-pipe work
-// only, where the exp2 form needs two MUFU operations.
 // tanh(y) for |y| < 1/8 from y - y^3/3 + 2 y^5/15 (the first omitted term,
 // 17 y^7 / 315, is below 2.6e-8 there): four FMA-pipe operations.
 __device__ __forceinline__ float tanh_taylor_short(float y) {
@@ -67,6 +64,9 @@ __device__ __forceinline__ float tanh_taylor_short(float y) {
   return fmaf(y * y2, q, y);
 }
 
+// tanh(y) for |y| < 0.5 from its odd Taylor series through y^11 (the first
+// omitted term, 21844 y^13 / 6081075, is below 4.5e-7 there): FMA-pipe work
+// only, where the exp2 form needs two MUFU operations.
 __device__ __forceinline__ float tanh_taylor(float y) {
   const float y2 = y * y;
   float q = fmaf(y2, -1382.f / 155925.f, 62.f / 2835.f);

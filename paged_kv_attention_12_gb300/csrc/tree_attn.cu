@@ -30,13 +30,13 @@
 // Where the time goes (a serving layer: 32 trees of 8 to 16 tokens over 512 to
 // 4096 keys, 2 KV heads, D = 256; 154 MB, 38.8 us; global-timer stamps): 0.6 us to
 // the chunk, 2 to the first copy, 2.5 to the first S, then 1.4 us for each tile of
-// 64 keys, 7.0 TB/s over the SMs (softmax and MMAs, 0.5 us each, are hidden behind
-// the loads), 2 after the last copy has landed, 1.3 for the pieces' rows, and 6 for
+// 64 keys, 7.0 TB/s over the SMs (softmax, 0.8 us with its stamps, and MMAs, 0.5, are
+// hidden behind the loads), 2 after the last copy has landed, 1.3 for the pieces' rows, and 6 for
 // the merge and its launch.  DRAM reads are the keys' bytes.  A sliding layer of
-// them (512 keys each, 64 segments on 64 pairs): 17.4 us (19.3 with a CTA each),
-// latency.  Four long requests (D = 128, 33 to 131 K keys, 672 MB): 116
-// us, 5.8 TB/s.  64 tokens x 4 heads are two row tiles, which read their keys twice,
-// the second time from L2: 43.7 us, 1.37 a tile, 7.4 TB/s out of L2.
+// them (512 keys each, 64 segments on 64 pairs): 17.1 us (19.3 with a CTA each),
+// latency.  Four long requests (D = 128, 33 to 131 K keys, 672 MB): 114
+// us, 5.9 TB/s.  64 tokens x 4 heads are two row tiles, which read their keys twice,
+// the second time from L2: 44.3 us, 1.37 a tile, 7.3 TB/s out of L2.
 //
 // Measured and dropped: one pass over S with a reference that moves only when the
 // weights' sum shows that it must (few instructions, which are cold in every launch:
